@@ -1,0 +1,187 @@
+// paged.hip - the paged key/value cache: a step's block tables, slots and positions, and the
+// write of new keys and values into their pages.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "quant_device.hpp"
+#include "serving.hpp"
+
+namespace fp8amax {
+namespace {
+
+constexpr int kPlanThreads = 256;
+
+// Inclusive sums over the workgroup of two non-negative values per thread; `total` gets the
+// last thread's.  `part` holds one pair per wave.
+__device__ __forceinline__ void scan2(int64_t& a, int64_t& b, int64_t (*part)[2], int64_t total[2]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t x = __shfl_up(a, d), y = __shfl_up(b, d);
+    if (lane >= d) { a += x; b += y; }
+  }
+  if (lane == 63) { part[wave][0] = a; part[wave][1] = b; }
+  __syncthreads();
+  total[0] = total[1] = 0;
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    if (w == wave) { a += total[0]; b += total[1]; }
+    total[0] += part[w][0];
+    total[1] += part[w][1];
+  }
+  __syncthreads();   // part is written again by the next round
+}
+
+// The first i with sums[i] > x, for inclusive sums of n > 0 entries and x < sums[n - 1].
+__device__ __forceinline__ int owner(const int* sums, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int pages_for(int64_t len, int shift, int width) {
+  const int64_t p = (len + (int64_t{1} << shift) - 1) >> shift;
+  return static_cast<int>(min(p, static_cast<int64_t>(width)));
+}
+
+// One launch: every workgroup forms the prefix sums of the new tokens and of the new pages over
+// the whole batch in LDS (8 bytes a request, from L2 after the first workgroup), then takes its
+// share of the tokens and of the new table entries, each found by a search in the sums.  A token
+// on a new page takes the page from the free list itself rather than from the table, which other
+// workgroups are writing.
+__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
+  extern __shared__ int sums[];
+  int* const cu = sums;                 // inclusive sums of the new tokens, at most 2^31 - 1
+  int* const pg = sums + a.batch;       // inclusive sums of the new pages
+  __shared__ int64_t part[kPlanThreads / 64][2];
+  int64_t base[2] = {0, 0}, lost = 0;
+  const bool first = blockIdx.x == 0;
+  for (int i0 = 0; i0 < a.batch; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    int64_t na = 0, np = 0;
+    if (i < a.batch) {
+      const int64_t c = max(a.cached[i], 0), n = max(a.added[i], 0);
+      na = n;
+      const int had = pages_for(c, a.page_shift, a.width);
+      np = pages_for(c + n, a.page_shift, a.width) - had;
+      if (first) {
+        a.lens[i] = static_cast<int>(min(c + n, int64_t{0x7fffffff}));
+        const int64_t one = int64_t{1} << a.page_shift;   // entries the table does not have
+        lost += max(int64_t{0}, ((c + n + one - 1) >> a.page_shift) - max((c + one - 1) >> a.page_shift, int64_t{a.width}));
+      }
+    }
+    int64_t total[2];
+    scan2(na, np, part, total);
+    if (i < a.batch) {
+      cu[i] = static_cast<int>(min(base[0] + na, int64_t{0x7fffffff}));
+      pg[i] = static_cast<int>(min(base[1] + np, int64_t{0x7fffffff}));
+      if (first) a.cu[i + 1] = cu[i];
+    }
+    base[0] += total[0];
+    base[1] += total[1];
+  }
+  __syncthreads();
+  const int taken = max(*a.taken_in, 0);
+  const int left = max(a.n_free - taken, 0);
+  const int tokens = static_cast<int>(min(base[0], int64_t{a.tokens}));
+  const int fresh = static_cast<int>(min(base[1], int64_t{0x7fffffff}));
+  if (first) {
+    int64_t none = 0, total[2];
+    scan2(lost, none, part, total);
+    if (threadIdx.x == 0) {
+      a.cu[0] = 0;
+      *a.taken_out = *a.taken_in + min(fresh, left);
+      *a.missing = static_cast<int>(min(total[0] + max(fresh - left, 0), int64_t{0x7fffffff}));
+    }
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
+  for (int64_t x = start; x < fresh; x += step) {
+    const int i = owner(pg, a.batch, static_cast<int>(x));
+    const int rank = static_cast<int>(x) - (i ? pg[i - 1] : 0);
+    const int col = pages_for(max(a.cached[i], 0), a.page_shift, a.width) + rank;
+    a.table[static_cast<int64_t>(i) * a.width + col] = x < left ? a.free_pages[taken + x] : -1;
+  }
+  for (int64_t t = start; t < a.tokens; t += step) {
+    int position = -1;
+    int64_t slot = -1;
+    if (t < tokens) {
+      const int i = owner(cu, a.batch, static_cast<int>(t));
+      const int c = max(a.cached[i], 0);
+      const int64_t at = int64_t{c} + (static_cast<int>(t) - (i ? cu[i - 1] : 0));
+      position = static_cast<int>(min(at, int64_t{0x7fffffff}));
+      const int col = position >> a.page_shift;
+      if (at == position && col < a.width) {
+        const int had = pages_for(c, a.page_shift, a.width);
+        int page;
+        if (col < had) {
+          page = a.table[static_cast<int64_t>(i) * a.width + col];
+        } else {
+          const int x = (i ? pg[i - 1] : 0) + col - had;
+          page = x < left ? a.free_pages[taken + x] : -1;
+        }
+        if (page >= 0) slot = (static_cast<int64_t>(page) << a.page_shift) + (position & ((1 << a.page_shift) - 1));
+      }
+    }
+    a.positions[t] = position;
+    a.slots[t] = slot;
+  }
+}
+
+constexpr int kAppendThreads = 256;
+
+// One group of D / 8 lanes per token, head and tensor: 16 bytes a lane, the row's largest
+// magnitude by DPP within the group, then the codes (8 bytes a lane) and the scale, or the 16
+// bytes as they are.
+template <int DT, int D, bool E4M3>
+__global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
+  constexpr int kLanes = D / 8;
+  const int rows = a.tokens * a.heads;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / kLanes) + threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  if (id >= rows) return;
+  const bool is_v = blockIdx.y != 0;
+  const int t = static_cast<int>(id / a.heads), h = static_cast<int>(id - static_cast<int64_t>(t) * a.heads);
+  const int64_t slot = a.slots[t];
+  if (slot < 0 || slot >= a.n_slots) return;   // the whole group together
+  const uint16_t* x = static_cast<const uint16_t*>(is_v ? a.v : a.k) + t * (is_v ? a.vts : a.kts) + h * (is_v ? a.vhs : a.khs);
+  const U4 w = load16(x + lane * 8);
+  const int64_t page = slot >> a.page_shift, at = slot & ((1 << a.page_shift) - 1);
+  const int64_t row = ((page * a.heads + h) << a.page_shift) + at;
+  void* c = is_v ? a.vc : a.kc;
+  if constexpr (E4M3) {
+    const uint32_t key = kLanes == 16 ? max16(key8(w)) : max8(key8(w));
+    const float s = scale_from_amax(amax_from_key<DT>(key));
+    const bool fast = fast_scale(s);
+    const uint2 q = enc8<DT>(w, s, 1.0f / s, fast);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c) + row * D + lane * 8) = q;
+    if (lane == 0) (is_v ? a.vs : a.ks)[row] = s;
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c) + row * D + lane * 8) = make_uint4(w.x, w.y, w.z, w.w);
+  }
+}
+
+template <int DT, int D>
+void append(bool e4m3, const AppendArgs& a, hipStream_t s) {
+  constexpr int kRows = kAppendThreads / (D / 8);
+  const dim3 grid((a.tokens * a.heads + kRows - 1) / kRows, 2);
+  if (e4m3) kv_append_kernel<DT, D, true><<<grid, kAppendThreads, 0, s>>>(a);
+  else kv_append_kernel<DT, D, false><<<grid, kAppendThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+void launch_paged_plan(const PlanArgs& a, hipStream_t s) {
+  const int groups = max(1, min((a.tokens + kPlanThreads - 1) / kPlanThreads, 1024));
+  paged_plan_kernel<<<groups, kPlanThreads, static_cast<size_t>(a.batch) * 8, s>>>(a);
+}
+
+void launch_kv_append(int dt, int head_dim, bool e4m3, const AppendArgs& a, hipStream_t s) {
+  if (dt == DT_BF16) head_dim == 128 ? append<DT_BF16, 128>(e4m3, a, s) : append<DT_BF16, 64>(e4m3, a, s);
+  else head_dim == 128 ? append<DT_F16, 128>(e4m3, a, s) : append<DT_F16, 64>(e4m3, a, s);
+}
+
+}  // namespace fp8amax

@@ -37,6 +37,9 @@ It is a plain, slow, obviously correct restatement of what the pages define:
   scales).  Source: "FP8 chi tiết", its section on MoE experts (grouped_mm / batched_mm,
   DeepGEMM expert kernels) with the opening bullets' block scaling.
 
+* ``serving`` (imported by its own name) - the step plan of a paged key/value cache and causal
+  attention with grouped heads, in plain loops and float64.
+
 * ``delayed`` - static scaling (a scale fixed in advance; saturation) and the
   delayed-scaling amax history (max over the window, times 2^margin, every
   `interval` steps).  Source: the task page's DelayedScaling recipe and calibration

@@ -1,0 +1,393 @@
+"""The serving operators against plain float64 references: step plan, cache append, attention
+over packed prompts and over a paged cache, at the sizes, strides and masks where they can go
+wrong.  Bounds are derived in oracle.serving and in serving_util."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_quantized_gemm_amax_amd as fp8
+from oracle import decode_e4m3, quantize_rowwise
+from oracle.serving import attention_ref, paged_plan_ref
+from parity_util import DEV
+from serving_util import TORCH, Cache, bits_of, check_paged, check_prompt, check_rows, cu_of, f64_of, normal
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------------------------------ plan
+
+@pytest.mark.parametrize("cached,added,page,width,free,taken,tokens", [
+    ([], [], 16, 4, 3, 0, 5),
+    ([0], [1], 16, 1, 1, 0, 1),
+    ([15, 16, 17, 0], [1, 1, 1, 0], 16, 4, 8, 2, 3),
+    ([0, 31, 64, 7], [100, 1, 0, 64], 32, 6, 40, 3, 200),        # padded token count
+    ([5, 5, 5], [40, 40, 40], 16, 8, 5, 1, 120),                 # the free list runs out
+    ([30, 0], [10, 50], 16, 2, 20, 0, 60),                       # the table is too narrow
+    ([10, 20], [30, 40], 64, 4, 9, 0, 33),                       # more new tokens than places
+    ([-3, 4], [2, -5], 16, 3, 9, 0, 4),                          # negative lengths count as 0
+    ([3], [70000], 128, 600, 700, 0, 70000),
+    ([0] * 5, [0] * 5, 16, 2, 0, 0, 0),
+])
+def test_plan_cases(cached, added, page, width, free, taken, tokens):
+    run_plan(cached, added, page, width, free, taken, tokens)
+
+
+@pytest.mark.parametrize("batch", [2, 63, 64, 65, 255, 256, 257, 1000, 16384])
+@pytest.mark.parametrize("page", [16, 1024])
+def test_plan_batches(batch, page):
+    rng = np.random.default_rng(batch)
+    cached = rng.integers(0, 200, batch)
+    added = np.where(rng.random(batch) < 0.7, 1, rng.integers(0, 40, batch))
+    run_plan(cached, added, page, 20, batch * 4, 0, int(added.sum()) + 3)
+
+
+def run_plan(cached, added, page, width, free, taken, tokens):
+    rng = np.random.default_rng(1)
+    b = len(cached)
+    table = rng.integers(0, 1 << 20, (b, width)).astype(np.int32)
+    pages = rng.permutation(1 << 20)[:free].astype(np.int32)
+    want = paged_plan_ref(cached, added, table, pages, taken, tokens, page)
+    full = torch.full((b * width + 64,), -77, dtype=torch.int32, device=DEV)
+    dev_table = full[: b * width].view(b, width)
+    dev_table.copy_(torch.from_numpy(table))
+    guard = {n: torch.full((s + 64,), -77, dtype=d, device=DEV) for n, s, d in (
+        ("cu_tokens", b + 1, torch.int32), ("seq_lens", b, torch.int32), ("positions", tokens, torch.int32),
+        ("slots", tokens, torch.int64), ("taken", 1, torch.int32), ("missing", 1, torch.int32))}
+    out = fp8.PagedPlan(**{n: t[:-64] for n, t in guard.items()})
+    fp8.fp8_paged_plan(i32(cached), i32(added), dev_table, i32(pages), i32([taken]), tokens, page, out=out)
+    torch.cuda.synchronize()
+    got = (out.cu_tokens, out.seq_lens, out.positions, out.slots, dev_table, out.taken, out.missing)
+    for name, g, w in zip(("cu_tokens", "seq_lens", "positions", "slots", "table", "taken", "missing"), got, want):
+        assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), name
+    assert (full[b * width:] == -77).all() and all((t[-64:] == -77).all() for t in guard.values())
+    again = fp8.fp8_paged_plan(i32(cached), i32(added), dev_table, i32(pages), i32([taken]), tokens, page)
+    assert all(torch.equal(x, y) for x, y in zip(again, out))      # same inputs, allocated outputs
+
+
+# ---------------------------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("tokens,heads,dim,page", [(1, 1, 64, 16), (1, 8, 128, 16), (33, 3, 64, 32), (130, 8, 128, 64), (515, 2, 128, 1024)])
+def test_append(dtype, e4m3, tokens, heads, dim, page):
+    rng = np.random.default_rng(tokens)
+    fused = normal((tokens, 3 * heads + 1, dim), dtype, tokens, 3.0)     # k and v inside a wider row
+    k, v = fused[:, 1:1 + heads], fused[:, 1 + 2 * heads:]
+    if tokens > 4:
+        k[1] = 0.0                                                       # a zero row: scale 1
+        k[2, 0, 5], v[3, 0, 0] = float("nan"), float("inf")
+        v[4] *= 2.0 ** -14                                               # subnormal fp16
+    pages = -(-tokens // page) + 2
+    slots = rng.permutation(pages * page)[:tokens].astype(np.int64)
+    if tokens > 4:
+        slots[-1], slots[-2], slots[0] = -1, pages * page, -(1 << 40)    # skipped
+    shape = (pages, heads, page, dim)
+    kind = torch.uint8 if e4m3 else TORCH[dtype]
+    caches = [torch.full(shape, 9, dtype=kind, device=DEV) for _ in "kv"]
+    scales = [torch.full(shape[:3], -5.0, device=DEV) for _ in "kv"] if e4m3 else [None, None]
+    fp8.fp8_kv_append(k, v, torch.from_numpy(slots).to(DEV), *caches, *scales)
+    torch.cuda.synchronize()
+    for x, cache, scale in zip((k, v), caches, scales):
+        bits = bits_of(x).reshape(-1, dim)
+        want = np.full(shape, 9, dtype=np.uint8) if e4m3 else bits_of(torch.full(shape, 9, dtype=kind)).copy()
+        wscale = np.full(shape[:3], -5.0, dtype=np.float32)
+        rows, s = quantize_rowwise(bits, dtype) if e4m3 else (bits, np.zeros(len(bits), np.float32))
+        for t, slot in enumerate(slots):
+            if 0 <= slot < pages * page:
+                want[slot // page, :, slot % page] = rows.reshape(tokens, heads, dim)[t]
+                wscale[slot // page, :, slot % page] = s.reshape(tokens, heads)[t]
+        got = cache.cpu().numpy() if e4m3 else bits_of(cache)
+        assert np.array_equal(got, want)
+        if e4m3:
+            assert np.array_equal(scale.cpu().numpy().view(np.uint32), wscale.view(np.uint32))
+
+
+# ---------------------------------------------------------------------------------------- prompt
+
+def run_prompt(lens, hq, hk, dim, dtype, window=0, scale=None, seed=0, qscale=1.0, layout="fused"):
+    t = sum(lens)
+    if layout == "fused":
+        x = normal((t, hq + 2 * hk, dim), dtype, seed)
+        q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    elif layout == "head_major":          # [heads, tokens, dim] seen as [tokens, heads, dim]
+        q, k, v = (normal((h, t, dim), dtype, seed + i).transpose(0, 1) for i, h in enumerate((hq, hk, hk)))
+    elif layout == "odd":                 # strides that are no multiple of 8: copied by the binding
+        q, k, v = (normal((t, h, dim + 3), dtype, seed + i)[..., 1:dim + 1] for i, h in enumerate((hq, hk, hk)))
+    q = q * qscale if qscale != 1.0 else q
+    full = torch.full((t * hq * dim + 512,), -7.0, dtype=TORCH[dtype], device=DEV)
+    out = full[: t * hq * dim].view(t, hq, dim)
+    _, lse = fp8.fp8_attn_prompt(q, k, v, cu_of(lens), softmax_scale=scale, window=window, out=out, return_lse=True)
+    torch.cuda.synchronize()
+    assert (full[t * hq * dim:] == -7.0).all()
+    check_prompt(q, k, v, lens, out, lse, dtype, scale or 1 / math.sqrt(dim), window)
+    assert torch.equal(fp8.fp8_attn_prompt(q, k, v, cu_of(lens), softmax_scale=scale, window=window), out)   # no lse, same bits
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens", [[1], [2], [31], [32], [33], [63, 1, 64, 65], [0, 5, 0, 0, 129, 0], [127, 128], [257]])
+def test_prompt_lengths(lens, dim, dtype):
+    run_prompt(lens, 4, 2, dim, dtype)
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 3), (5, 1), (7, 1), (8, 1), (10, 2), (32, 8), (12, 4), (64, 2), (40, 1)])
+def test_prompt_heads(hq, hk):
+    run_prompt([70, 3, 41], hq, hk, 128, "bf16", seed=hq)
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 500, 1 << 40])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_windows(window, dim):
+    run_prompt([300, 17, 64], 4, 2, dim, "bf16", window=window if window < 1 << 40 else 1 << 40)
+
+
+@pytest.mark.parametrize("layout", ["head_major", "odd"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_strides(layout, dim):
+    run_prompt([100, 29], 6, 2, dim, "f16", layout=layout)
+
+
+@pytest.mark.parametrize("qscale,scale", [(30.0, None), (1.0, 2.0), (0.001, None), (1.0, 1e-6)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_prompt_score_sizes(qscale, scale, dtype):
+    """Weights that all but vanish next to the largest, and weights that are all alike."""
+    run_prompt([200], 2, 1, 64, dtype, qscale=qscale, scale=scale)
+
+
+def test_prompt_many_requests():
+    rng = np.random.default_rng(0)
+    run_prompt([int(x) for x in rng.integers(0, 9, 150)], 4, 4, 64, "f16")
+
+
+def test_prompt_long():
+    run_prompt([1500], 2, 1, 128, "bf16")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_masked_places_do_not_matter(bad, dim):
+    """A key or value that is not finite reaches only the queries that see it."""
+    n, hq, hk = 150, 4, 2
+    q, k, v = (normal((n, h, dim), "bf16", i) for i, h in enumerate((hq, hk, hk)))
+    good = fp8.fp8_attn_prompt(q, k, v, cu_of([n]))
+    for at in (149, 100, 64, 40):
+        k2, v2 = k.clone(), v.clone()
+        v2[at, 1, 7] = bad
+        out = fp8.fp8_attn_prompt(q, k, v2, cu_of([n]))
+        assert torch.equal(out[:at], good[:at]) and torch.equal(out[:, :2], good[:, :2])
+        got, want = out[at:, 2:, 7].float(), torch.full((n - at, 2), bad, device=DEV)
+        assert torch.equal(got, want) or (math.isnan(bad) and got.isnan().all())
+        if math.isnan(bad):
+            k2[at, 1] = bad
+            out = fp8.fp8_attn_prompt(q, k2, v, cu_of([n]))
+            assert torch.equal(out[:at], good[:at]) and out[at:, 2:].isnan().all()
+
+
+# ----------------------------------------------------------------------------------------- paged
+
+def run_paged(lens, new, hq, hk, dim, page, dtype, e4m3, window=0, seed=0, max_new=None, width=None, kscale=1.0):
+    cache = Cache(lens, hk, dim, page, dtype, e4m3, seed + 1, width=width, kscale=kscale)
+    t = sum(new)
+    q = normal((t, hq + 1, dim), dtype, seed)[:, 1:]
+    full = torch.full((t * hq * dim + 512,), -7.0, dtype=TORCH[dtype], device=DEV)
+    out = full[: t * hq * dim].view(t, hq, dim)
+    kw = dict(window=window, max_new=max(new) if max_new is None else max_new)
+    args = (q, cache.k, cache.v, cache.dev_table, cache.dev_lens, cu_of(new), cache.ks, cache.vs)
+    _, lse = fp8.fp8_attn_paged(*args, out=out, return_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert (full[t * hq * dim:] == -7.0).all()
+    check_paged(q, cache, new, out, lse, dtype, 1 / math.sqrt(dim), window)
+    assert torch.equal(fp8.fp8_attn_paged(*args, **kw), out)
+    return cache, q, out
+
+
+KINDS = [("bf16", False), ("bf16", True), ("f16", False), ("f16", True)]
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [16, 64, 1024])
+def test_paged_single_tokens(page, dim, dtype, e4m3):
+    run_paged([1, 15, 16, 17, 31, 32, 33, 127, 128, 129, 300, 1025], [1] * 12, 8, 2, dim, page, dtype, e4m3)
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 128])
+def test_paged_chunks(page, dim, dtype, e4m3):
+    run_paged([1, 40, 64, 129, 200, 333], [1, 40, 2, 100, 33, 70], 4, 2, dim, page, dtype, e4m3)
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (5, 1), (8, 1), (16, 2), (32, 32), (40, 1), (64, 1), (12, 4)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 7, 3]])
+def test_paged_heads(hq, hk, new):
+    run_paged([9, 100, 257], new, hq, hk, 128, 16, "bf16", False, seed=hq)
+
+
+@pytest.mark.parametrize("window", [1, 15, 16, 40, 128, 1000])
+@pytest.mark.parametrize("dtype,e4m3", [("bf16", False), ("f16", True)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 60, 90]])
+def test_paged_windows(window, dtype, e4m3, new):
+    run_paged([5, 260, 700], new, 8, 2, 128, 32, dtype, e4m3, window=window)
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+def test_paged_long(dtype, e4m3):
+    """Few rows over a long axis: the work is split and joined."""
+    run_paged([9000, 3, 2500], [1, 1, 1], 8, 2, 128, 64, dtype, e4m3)
+    run_paged([5000], [2], 2, 2, 64, 16, dtype, e4m3)
+
+
+@pytest.mark.parametrize("max_new", [0, 1, 64, 4096])
+def test_paged_hint_changes_no_meaning(max_new):
+    run_paged([100, 300, 64], [1, 130, 0], 8, 2, 128, 16, "bf16", False, max_new=max_new)
+
+
+def test_paged_wide_table_and_many_requests():
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(1, 200, 300)]
+    run_paged(lens, [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 3, 300))], 4, 1, 64, 16, "f16", False, width=100)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[3, 2, 4], [40, 70, 90]])
+def test_paged_rows_without_keys(dim, new):
+    """Requests whose cache holds fewer tokens than they bring (or none): rows without keys give 0
+    and -inf."""
+    lens = [1, 0, 66]
+    cache = Cache(lens, 2, dim, 16, "bf16", False, 5)
+    q = normal((sum(new), 4, dim), "bf16", 6)
+    out, lse = fp8.fp8_attn_paged(q, cache.k, cache.v, cache.dev_table, cache.dev_lens, cu_of(new), max_new=max(new), return_lse=True)
+    check_paged(q, cache, new, out, lse, "bf16", 1 / math.sqrt(dim), 0, rel=False)
+    assert (out[new[0]:new[0] + new[1]] == 0).all() and lse[new[0]:new[0] + new[1]].isneginf().all()
+
+
+def test_paged_fp8_scale_range():
+    """fp16 queries over e4m3 rows whose scales lie far below and above fp16's range of products."""
+    lens, new = [150, 90], [1, 20]
+    cache = Cache(lens, 2, 128, 16, "f16", True, 7)
+    mult = torch.logspace(-5, 2, 16, device=DEV)[torch.arange(cache.vs.numel(), device=DEV) % 16].view(cache.vs.shape)
+    for m in (1.0, 2.0 ** -12, 2.0 ** 8):
+        vs = cache.vs * mult * m
+        vals = decode_e4m3(cache.v.cpu().numpy()).astype(np.float64) * vs.cpu().numpy().astype(np.float64)[..., None]
+        cache.values["v"] = vals
+        q = normal((sum(new), 8, 128), "f16", 8)
+        out = fp8.fp8_attn_paged(q, cache.k, cache.v, cache.dev_table, cache.dev_lens, cu_of(new), cache.ks, vs, max_new=20)
+        # a weight times its scale is rounded with 11 bits or better: relative to the largest product
+        at = 0
+        for r, n in enumerate(new):
+            kk, vv = cache.request("k", r), cache.request("v", r)
+            ref = attention_ref(f64_of(q[at:at + n]), kk, vv, len(kk) - n, 1 / math.sqrt(128), 0)
+            check_rows(out[at:at + n], None, ref, "f16", len(kk), 128, float(np.abs(vv).max()), f"{m} {r}")
+            at += n
+
+
+def test_paged_pages_that_do_not_exist():
+    """Table entries outside the cache read as zero keys and values."""
+    cache = Cache([80, 40], 2, 128, 16, "bf16", False, 9)
+    q = normal((2, 4, 128), "bf16", 10)
+    table = cache.dev_table.clone()
+    table[0, 2], table[1, 0] = -1, 1 << 30
+    out = fp8.fp8_attn_paged(q, cache.k, cache.v, table, cache.dev_lens, cu_of([1, 1]), max_new=1)
+    for r, (lo, hi) in enumerate(((32, 48), (0, 16))):
+        kk, vv = cache.request("k", r).copy(), cache.request("v", r).copy()
+        kk[lo:hi], vv[lo:hi] = 0, 0
+        ref = attention_ref(f64_of(q[r:r + 1]), kk, vv, len(kk) - 1, 1 / math.sqrt(128), 0)
+        check_rows(out[r:r + 1], None, ref, "bf16", len(kk), 128, 6.0, f"request {r}")
+
+
+def test_lengths_beyond_their_tensors_stay_inside():
+    """cu_tokens past the tokens and seq_lens past the table are clamped; rows nobody covers stay."""
+    cache = Cache([64], 2, 64, 16, "bf16", False, 11, width=4)
+    q = normal((10, 2, 64), "bf16", 12)
+    out = torch.full((10, 2, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_attn_paged(q, cache.k, cache.v, cache.dev_table, i32([1 << 30]), i32([-4, 6]), out=out, max_new=6)
+    check_paged(q[:6], cache, [6], out[:6], None, "bf16", 1 / 8, 0)
+    assert (out[6:] == 3.0).all()
+    q2 = normal((10, 2, 64), "bf16", 13)
+    out2 = torch.full_like(out, 3.0)
+    fp8.fp8_attn_prompt(q, q2, q, i32([0, 4, 1 << 30]), out=out2)
+    check_prompt(q, q2, q, [4, 6], out2, None, "bf16", 1 / 8, 0)
+
+
+# ------------------------------------------------------------------------------- streams, graphs
+
+def step_inputs():
+    cached, added, page = [70, 5, 0, 33], [1, 1, 40, 1], 16
+    lens = [c + a for c, a in zip(cached, added)]
+    cache = Cache(lens, 2, 128, page, "bf16", True, 21)
+    t = sum(added)
+    x = normal((t, 8 + 4, 128), "bf16", 22)
+    return cached, added, page, lens, cache, x[:, :8], x[:, 8:10], x[:, 10:]
+
+
+def one_step(cached, added, table, free, taken, t, page, cache, q, k, v, plan=None, out=None):
+    plan = fp8.fp8_paged_plan(cached, added, table, free, taken, t, page, out=plan)
+    fp8.fp8_kv_append(k, v, plan.slots, cache.k, cache.v, cache.ks, cache.vs)
+    return plan, fp8.fp8_attn_paged(q, cache.k, cache.v, table, plan.seq_lens, plan.cu_tokens, cache.ks, cache.vs, max_new=40, out=out)
+
+
+def test_step_on_another_stream_and_in_a_graph():
+    """Plan, append and attention of one step: on a side stream, and captured in a graph that is
+    replayed with eager work between; every result equals the eager one."""
+    cached, added, page, lens, cache, q, k, v = step_inputs()
+    t = sum(added)
+    c, a, taken = i32(cached), i32(added), i32([0])
+    free = torch.arange(cache.k.shape[0] - 1, -1, -1, dtype=torch.int32, device=DEV)
+    table = torch.full_like(cache.dev_table, -1)
+    for r, n in enumerate(cached):
+        table[r, : -(-n // page)] = cache.dev_table[r, : -(-n // page)]
+    owned = set(table.cpu().numpy().reshape(-1).tolist()) - {-1}
+    free = torch.tensor([p for p in free.cpu().tolist() if p not in owned], dtype=torch.int32, device=DEV)
+    plan, want = one_step(c, a, table, free, taken, t, page, cache, q, k, v)
+    torch.cuda.synchronize()
+    assert int(plan.missing) == 0
+    keep = [x.clone() for x in (*plan, table, want)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        plan2, got = one_step(c, a, table, free, taken, t, page, cache, q, k, v)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((*plan2, table, got), keep))
+    bufs, out = fp8.paged_plan_buffers(len(cached), t, DEV), torch.empty_like(want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one_step(c, a, table, free, taken, t, page, cache, q, k, v, plan=bufs, out=out)
+    for rep in range(4):
+        out.fill_(7.0)
+        for x in bufs:
+            x.fill_(-9)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((*bufs, table, out), keep)), rep
+        _ = (want.float() * 2).sum()
+    # and the eager result is the reference's, over what the cache holds
+    cache.table, cache.lens = table.cpu().numpy(), lens
+    for n in "kv":
+        vals = decode_e4m3(getattr(cache, n).cpu().numpy()).astype(np.float64) * getattr(cache, n + "s").cpu().numpy().astype(np.float64)[..., None]
+        cache.values[n] = vals
+    check_paged(q, cache, added, want, None, "bf16", 1 / math.sqrt(128), 0)
+
+
+def test_prompt_equals_chunk_of_everything():
+    """A whole prompt and the same prompt appended to an empty cache and read back agree to two roundings."""
+    n, hq, hk, dim, page = 200, 8, 2, 128, 16
+    x = normal((n, hq + 2 * hk, dim), "bf16", 31)
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    pages = -(-n // page)
+    table = torch.randperm(pages, device=DEV).int()[None].contiguous()
+    slots = (table[0, torch.arange(n, device=DEV) // page].long() * page + torch.arange(n, device=DEV) % page)
+    kc, vc = (torch.full((pages, hk, page, dim), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in "kv")
+    fp8.fp8_kv_append(k, v, slots, kc, vc)
+    a = fp8.fp8_attn_prompt(q, k, v, cu_of([n])).double()
+    b = fp8.fp8_attn_paged(q, kc, vc, table, i32([n]), cu_of([n]), max_new=n).double()
+    assert float((a - b).norm() / a.norm()) <= 4 * 2.0 ** -8
