@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8amax.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemv.hip", "serving_api.hip", "paged.hip", "attention.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemv.hip", "serving_api.hip", "paged.hip", "attention.hip",
+           "attn_tile.hip"]
 OBJ_DIR = os.path.join(PKG, "_build")
 
 HIPCC_FLAGS = [

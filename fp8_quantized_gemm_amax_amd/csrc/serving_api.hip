@@ -118,6 +118,7 @@ fp8_status_t fp8_attn_prompt(const void* q, const void* k, const void* v, fp8_dt
   if ((st = check_strides(tokens, q_heads, q_token_stride, q_head_stride)) != FP8_OK) return st;
   if ((st = check_strides(tokens, kv_heads, k_token_stride, k_head_stride)) != FP8_OK) return st;
   if ((st = check_strides(tokens, kv_heads, v_token_stride, v_head_stride)) != FP8_OK) return st;
+  if (tokens > 1 && (k_token_stride < head_dim || v_token_stride < head_dim)) return FP8_ERR_BAD_SHAPE;
   if (k_token_stride > (int64_t{1} << 20) || v_token_stride > (int64_t{1} << 20)) return FP8_ERR_TOO_LARGE;
   if (tokens == 0 || batch == 0) return FP8_OK;
   if (!q || !k || !v || !cu_tokens || !out) return FP8_ERR_NULL_POINTER;

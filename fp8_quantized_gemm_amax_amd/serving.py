@@ -92,13 +92,14 @@ def _dense(t, what, dtype, shape):
 
 def _rows(t, what, heads_dim=None):
     """A [tokens, heads, dim] operand whose rows the kernels read 16 bytes at a time: as it lies
-    if its last index is contiguous and the other strides are multiples of 8, else a copy."""
+    if its last index is contiguous, the other strides are multiples of 8 and tokens do not overlap,
+    else a copy."""
     if t.dim() != 3:
         raise ValueError(f"{what} must be [tokens, heads, head_dim], got shape {tuple(t.shape)}")
     if heads_dim is not None and t.shape[2] != heads_dim:
         raise ValueError(f"{what} must have head_dim {heads_dim}, got {t.shape[2]}")
     ts, hs, one = t.stride()
-    if one != 1 or (ts | hs) & 7 or t.data_ptr() & 15:
+    if one != 1 or (ts | hs) & 7 or t.data_ptr() & 15 or ts < t.shape[2] or ts > 1 << 20:
         t = t.contiguous()
         if t.data_ptr() & 15:
             t = t.clone()

@@ -87,6 +87,7 @@ fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t
  *   out_i = sum_j softmax_j(softmax_scale * q_i . k_j) v_j
  *   lse_i = log sum_j exp(softmax_scale * q_i . k_j)
  *   out : [tokens, q_heads, head_dim] of dt, dense.  lse : NULL or float32 [tokens, q_heads].
+ *   The token strides of k and v are at least head_dim (with more than one token) and at most 2^20.
  *   softmax_scale : finite and > 0.  window : 0 (none) or the number of keys a query sees.
  * Scores, the running maximum and sum, and the output accumulate in float32; the weights are
  * rounded to dt for the product with v, and the result once to dt.
