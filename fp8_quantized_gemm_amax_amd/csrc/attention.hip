@@ -9,6 +9,12 @@ namespace fp8amax {
 namespace attn {
 namespace {
 
+// Whether a batch goes to the kernel for few rows: where every request has at most 32 rows a key
+// head.  Without max_new, by the average.
+bool few_rows(int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
+  return (max_new > 0 ? max_new : (tokens + batch - 1) / (batch > 0 ? batch : 1)) * group <= 32;
+}
+
 // One wave per row and a workgroup per four rows of a tile: out = sum_i 2^(m_i - m) o_i / sum_i
 // 2^(m_i - m) l_i over the tile's partial results, in their order.
 template <int DT, int D>
@@ -62,14 +68,15 @@ void launch_attn_join(int dt, int head_dim, int size, const AttnArgs& a, hipStre
 }  // namespace attn
 
 void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnArgs& a, hipStream_t s) {
-  attn::launch_attn_tile(dt, head_dim, e4m3, a, s);
+  if (attn::few_rows(max_new, a.group, a.tokens, a.batch)) attn::launch_attn_few(dt, head_dim, e4m3, a, s);
+  else attn::launch_attn_tile(dt, head_dim, e4m3, a, s);
 }
 
 int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
                              int64_t max_new) {
   using namespace attn;
   if (!may_split(batch, capacity)) return 0;
-  const int size = 128;
+  const int size = few_rows(max_new, hq / hk, tokens, batch) ? 32 : 128;
   return info_bytes(tile_bound(tokens, hq / hk, batch, size), hk) + slot_bound(hk) * size * (head_dim + 2) * 4;
 }
 

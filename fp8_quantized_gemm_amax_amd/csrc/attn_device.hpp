@@ -48,9 +48,9 @@ __device__ __forceinline__ int scalar_int(const int* p) {
   return *reinterpret_cast<const __attribute__((address_space(4))) int*>(reinterpret_cast<uintptr_t>(p));
 }
 
-// Waits for this wave's LDS reads: before a barrier after which another wave may overwrite what
-// they read.
-__device__ __forceinline__ void wait_lds_reads() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+// Waits for this wave's LDS reads and writes: before what they read may be overwritten by a DMA or,
+// after a barrier, by another wave.  Memory accesses stay on their side of it.
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 template <int DT>
 __device__ __forceinline__ v16f mfma(const v8s& a, const v8s& b, const v16f& c) {

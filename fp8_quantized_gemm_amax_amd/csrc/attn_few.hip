@@ -1,0 +1,357 @@
+// attn_few.hip - attention over a paged cache for at most 32 packed rows a request and key head
+// (single tokens, short drafts): the keys are the work.  A workgroup of four waves takes one unit of
+// keys; each wave walks over its own tiles of them, through its own LDS without a barrier, for all
+// rows, and the four results are joined in LDS at the end.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "attn_device.hpp"
+
+namespace fp8amax {
+namespace attn {
+namespace {
+
+constexpr int kRows = 32;
+
+// One dword from `p` into LDS at lds + lane * 4, where `on` holds for the lane.
+__device__ __forceinline__ void dma4_lane(const float* p, uint32_t lds, bool on) {
+  if (on) asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+
+template <int DT, int D, int SRC>
+__global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split) {
+  constexpr bool kCodes = SRC == SRC_E4M3, kRange = kCodes && DT == DT_F16;
+  constexpr int kTileKeys = !kCodes && D == 128 ? 32 : 64;   // keys a wave takes at a time: 8 KB of K (4: codes of 64 channels)
+  constexpr int kSub = kTileKeys / 32, kGroups = kTileKeys / 16, kSteps = D / 16;
+  constexpr int kRowBytes = kCodes && D == 64 ? 64 : 128;    // of a key in a plane
+  constexpr int kPlanes = !kCodes && D == 128 ? 2 : 1;
+  constexpr int kPlaneBytes = kTileKeys * kRowBytes, kTile = kPlanes * kPlaneBytes;
+  constexpr int kDma = kTile / 1024;                         // DMA instructions of a tile
+  __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * kTile];
+  __shared__ __attribute__((aligned(16))) float scales[kCodes ? 4 : 1][2][64];
+  __shared__ float stats[2][4][32];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  Unit unit;
+  if (split) {
+    if (!find_unit<kRows>(a, blockIdx.x, reinterpret_cast<int*>(lds), unit)) return;
+  } else {
+    unit.head = blockIdx.x % a.hk;
+    if (!find_rows(a, blockIdx.x / a.hk, kRows, true, unit.r)) return;
+    tile_keys(a, unit.r, kRows, unit.j0, unit.j1);
+    unit.slot = 0;
+    unit.count = 1;
+    unit.first = true;
+  }
+  const Rows& r = unit.r;
+  const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
+  const int last_row = min(r.row0 + 31, r.rows - 1);
+  const int first_pos = r.pos0 + r.row0 / a.group, last_pos = r.pos0 + last_row / a.group;
+  const int row = min(r.row0 + col, last_row), tok = row / a.group, pos = r.pos0 + tok;
+  const int low = a.window > 0 ? pos - a.window + 1 : 0;
+  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (r.begin + tok) * a.qts + (h * a.group + row - tok * a.group) * a.qhs;
+  v8s q[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)   // codes are read 16 channels at a time: their order over two steps
+    q[s] = *reinterpret_cast<const v8s*>(qp + (kCodes ? 32 * (s / 2) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half));
+
+  char* const kt = lds + wave * 2 * kTile;
+  char* const vt = kt + kTile;
+  const uint32_t kbase = lds_addr(kt), vbase = kbase + kTile;
+  float* const my_ks = scales[kCodes ? wave : 0][0];
+  float* const my_vs = scales[kCodes ? wave : 0][1];
+  if constexpr (kCodes) {   // a lane without a key leaves its place as it was
+    my_ks[lane] = my_vs[lane] = 0.0f;
+    wait_lds_reads();
+  }
+
+  // Chunk of 16 bytes at position x of key row i in LDS; rows of 64 bytes hold four.
+  auto chunk_of = [](int x, int i) { return kRowBytes == 128 ? x ^ gemm::swz(i & 15) : x ^ ((i >> 1) & 3); };
+  uint32_t off[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int i = kRowBytes == 128 ? 8 * g + (lane >> 3) : lane >> 2;
+    off[g] = i * (kCodes ? D : 2 * D) + chunk_of(lane & (kRowBytes / 16 - 1), i) * 16;
+  }
+  auto page_of = [&](int at) -> int {
+    return at < j1 ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
+  };
+  auto bring = [&](const void* p, int t, const int (&pages)[kGroups], uint32_t to) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      v4i rs = key_rows<SRC, D>(a, r, p, 0, 0, h, t + 16 * g, 16, pages[g]);
+      settle(rs);
+#pragma unroll
+      for (int x = 0; x < kPlanes; ++x)
+#pragma unroll
+        for (int y = 0; y < kRowBytes / 64; ++y)
+          dma16_safe(rs, to + x * kPlaneBytes + g * 16 * kRowBytes + y * 1024, off[y] + x * 128);
+    }
+  };
+  auto bring_scales = [&](const float* p, int t, const int (&pages)[kGroups], uint32_t to) {
+    int page = pages[0];
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) page = lane >> 4 == g ? pages[g] : page;
+    const int at = t + lane;
+    const int64_t x = ((static_cast<int64_t>(page) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+    dma4_lane(p + x, to, at < r.len && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages));
+  };
+
+  // this lane's operands in LDS
+  const int vr = kCodes ? 4 * half + ((lane >> 1) & 3) + 8 * ((lane >> 3) & 1) : 4 * half + ((lane & 15) >> 2);
+  const int vdsub = (lane >> 4) & 1;
+
+  const float c = a.scale * kLog2e;
+  v16f o[D / 32];
+  float m, l;
+  int unit_exp;
+  auto walk = [&](auto odd_c) {
+    constexpr bool ODD = decltype(odd_c)::value;
+    m = -INFINITY;
+    l = 0.0f;
+    unit_exp = -200;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
+    int pages[kGroups];
+    int t = j0 + wave * kTileKeys;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t + 16 * g);
+    if (t < j1) {
+      if constexpr (kCodes) bring_scales(a.ks, t, pages, lds_addr(my_ks));
+      bring(a.k, t, pages, kbase);
+      if constexpr (kCodes) bring_scales(a.vs, t, pages, lds_addr(my_vs));
+      bring(a.v, t, pages, vbase);
+    }
+    for (; t < j1; t += 4 * kTileKeys) {
+      const int t1 = t + 4 * kTileKeys;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t1 + 16 * g);
+      wait_vmcnt<kDma>();      // K is there: at least the DMAs of V came after it
+      asm volatile("" ::: "memory");
+      v16f s[kSub];
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        s[u] = 0.0f;
+        const int i = 32 * u + col;
+        if constexpr (kCodes) {
+#pragma unroll
+          for (int x = 0; x < kSteps / 2; ++x) {
+            const v4u w = *reinterpret_cast<const v4u*>(kt + i * kRowBytes + (chunk_of(2 * x + half, i) << 4));
+            s[u] = mfma<DT>(__builtin_bit_cast(v8s, codes8<DT>(w[0], w[1])), q[2 * x], s[u]);
+            s[u] = mfma<DT>(__builtin_bit_cast(v8s, codes8<DT>(w[2], w[3])), q[2 * x + 1], s[u]);
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const v4f x = *reinterpret_cast<const v4f*>(my_ks + 32 * u + 8 * g + 4 * half);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[u][4 * g + y] *= x[y];
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < kSteps; ++x) {
+            const v8s k = *reinterpret_cast<const v8s*>(kt + (x / 4) * kPlaneBytes + i * 128 + (chunk_of(2 * (x & 3) + half, i) << 4));
+            s[u] = mfma<DT>(k, q[x], s[u]);
+          }
+        }
+      }
+      wait_lds_reads();
+      if (t1 < j1) {
+        if constexpr (kCodes) bring_scales(a.ks, t1, pages, lds_addr(my_ks));
+        bring(a.k, t1, pages, kbase);
+      }
+      if (t + kTileKeys - 1 > first_pos || (a.window > 0 && t < last_pos - a.window + 1)) {
+        const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = 32 * u + 8 * (i / 4) + i % 4;
+            s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int i = 1; i < 16 * kSub; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+      top = max_halves(top) * c;
+      if (__any(top > m)) {
+        const float m1 = fmaxf(m, top);
+        const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+        m = m1;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[i][x] *= keep;
+      }
+      const float mb = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], c, -mb));
+          l += s[u][i];
+        }
+      // V is there: at least the DMAs of the next K came after it, if there is one
+      if (t1 < j1) wait_vmcnt<kDma>();
+      else wait_vmcnt<0>();
+      asm volatile("" ::: "memory");
+      if constexpr (kCodes) {
+        float unit_inv = 1.0f;
+        if constexpr (kRange) {
+          float most = 0.0f;
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const v4f x = *reinterpret_cast<const v4f*>(my_vs + 32 * u + 8 * g + 4 * half);
+              most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
+            }
+          most = max_halves(most);
+          const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
+          if (e > unit_exp) {
+            const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
+            unit_exp = e;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[i][x] *= keep;
+          }
+          unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
+        }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const v4f x = *reinterpret_cast<const v4f*>(my_vs + 32 * u + 8 * g + 4 * half);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float z = s[u][4 * g + y] * (kRange ? x[y] * unit_inv : x[y]);
+              s[u][4 * g + y] = ODD && s[u][4 * g + y] == 0.0f ? 0.0f : z;
+            }
+          }
+      }
+#pragma unroll
+      for (int w = 0; w < kTileKeys / 16; ++w) {
+        v4u x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = pack2<DT>(s[w / 2][8 * (w & 1) + 2 * i], s[w / 2][8 * (w & 1) + 2 * i + 1]);
+        const v8s p = __builtin_bit_cast(v8s, x);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          v8s v;
+          if constexpr (kCodes) {
+            typedef int v2i __attribute__((ext_vector_type(2)));
+            const int key = 16 * w + vr;
+            const char* at = vt + key * kRowBytes + (chunk_of(2 * i + vdsub, key) << 4) + (lane & 1) * 8;
+            const v2i y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)at);
+            v = __builtin_bit_cast(v8s, codes8<DT>(y[0], y[1]));
+          } else {
+            const int chunk = (i & 1) * 4 + vdsub * 2 + ((lane & 3) >> 1);
+            const char* at = vt + (i / 2) * kPlaneBytes + (lane & 1) * 8;
+            const int k0 = 16 * w + vr, k1 = k0 + 8;
+            const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k0 * 128 + (chunk_of(chunk, k0) << 4)));
+            const v4s z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k1 * 128 + (chunk_of(chunk, k1) << 4)));
+            v = __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+          if constexpr (ODD) o[i] = mfma_odd<DT>(v, p, o[i]);
+          else o[i] = mfma<DT>(v, p, o[i]);
+        }
+      }
+      wait_lds_reads();
+      if (t1 < j1) {
+        if constexpr (kCodes) bring_scales(a.vs, t1, pages, lds_addr(my_vs));
+        bring(a.v, t1, pages, vbase);
+      }
+    }
+    l = add_halves(l);
+    if constexpr (kRange) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[i][x] = __builtin_ldexpf(o[i][x], unit_exp);
+    }
+    // join the four waves: wave w adds up channels 32 w .. 32 w + 31 and keeps them in o[0]
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<v4f*>(lds + (wave * (D / 32) + i) * 4096 + g * 1024 + lane * 16) =
+            v4f{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
+    if (half == 0) {
+      stats[0][wave][col] = m;
+      stats[1][wave][col] = l;
+    }
+    __syncthreads();
+    float mw[4];
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, mw[w] = stats[0][w][col]);
+    l = 0.0f;
+    o[0] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = mw[w] == m ? 1.0f : __builtin_amdgcn_exp2f(mw[w] - m);
+      l = __builtin_fmaf(f, stats[1][w][col], l);
+      if (wave < D / 32) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const v4f x = *reinterpret_cast<const v4f*>(lds + (w * (D / 32) + wave) * 4096 + g * 1024 + lane * 16);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[0][4 * g + y] = __builtin_fmaf(f, x[y], o[0][4 * g + y]);
+        }
+      }
+    }
+  };
+  walk(std::false_type{});
+  bool fine = true;
+#pragma unroll
+  for (int x = 0; x < 16; ++x) fine &= __builtin_isfinite(o[0][x]);
+  if (__syncthreads_or(!fine)) walk(std::true_type{});
+
+  if (split) leave_info(a, unit, kRows);
+  if (wave >= D / 32 || r.row0 + col >= r.rows) return;
+  if (unit.count > 1) {
+    const Workspace ws = workspace(a, kRows);
+    const int64_t at = static_cast<int64_t>(unit.slot) * kRows + col;
+    if (wave == 0 && half == 0) *reinterpret_cast<float2*>(ws.stats + at * 2) = make_float2(m, l);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<v4f*>(ws.out + at * D + 32 * wave + 8 * g + 4 * half) = v4f{o[0][4 * g], o[0][4 * g + 1], o[0][4 * g + 2], o[0][4 * g + 3]};
+    return;
+  }
+  const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + h * a.group + (row - tok * a.group);
+  const float inv = pos < 0 ? 0.0f : 1.0f / l;
+  if (a.lse && wave == 0 && half == 0) a.lse[out_row] = pos < 0 ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * D + 32 * wave + 4 * half;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    *reinterpret_cast<uint2*>(out + 8 * g) = make_uint2(pack2<DT>(o[0][4 * g] * inv, o[0][4 * g + 1] * inv),
+                                                        pack2<DT>(o[0][4 * g + 2] * inv, o[0][4 * g + 3] * inv));
+}
+
+template <int DT, int D, int SRC>
+void launch(const AttnArgs& a, hipStream_t s) {
+  const int64_t tiles = tile_bound(a.tokens, a.group, a.batch, kRows);
+  const bool split = may_split(a.batch, static_cast<int64_t>(a.width) << a.page_shift);
+  const int64_t units = (tiles + (split ? extra_units(a.hk) : 0)) * a.hk;
+  attn_few_kernel<DT, D, SRC><<<static_cast<unsigned>(units), 256, 0, s>>>(a, split);
+  if (split) launch_attn_join(DT, D, kRows, a, s);
+}
+
+template <int SRC>
+void launch_typed(int dt, int head_dim, const AttnArgs& a, hipStream_t s) {
+  if (dt == DT_BF16) head_dim == 128 ? launch<DT_BF16, 128, SRC>(a, s) : launch<DT_BF16, 64, SRC>(a, s);
+  else head_dim == 128 ? launch<DT_F16, 128, SRC>(a, s) : launch<DT_F16, 64, SRC>(a, s);
+}
+
+}  // namespace
+
+void launch_attn_few(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s) {
+  e4m3 ? launch_typed<SRC_E4M3>(dt, head_dim, a, s) : launch_typed<SRC_PAGED>(dt, head_dim, a, s);
+}
+
+}  // namespace attn
+}  // namespace fp8amax
