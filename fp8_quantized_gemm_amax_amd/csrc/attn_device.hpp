@@ -166,13 +166,14 @@ __device__ __forceinline__ v4i key_rows(const AttnArgs& a, const Rows& r, const 
 constexpr int kUnits = 1024;       // units wanted on the card, over all key heads
 constexpr int kMinSteps = 4;       // no chunk below 256 keys: a unit's start and end cost about that
 constexpr int kMaxSplitBatch = 1024;   // above, there are enough units without cuts
+constexpr int kMaxSplitHeads = 1024;
 
 struct Unit {
   Rows r;
   int head;
   int j0, j1;       // its keys
-  bool first;       // the tile's first chunk
-  int slot, count;  // its place among the partial results, and how many there are of its tile; count 1: none
+  int piece, count; // its chunk and how many there are of the tile (1: the whole)
+  int slot;         // where the tile's partial results begin, hk apart
 };
 
 // Keys [j0, j1) that the rows of a tile see between them, j0 a multiple of 64.
@@ -187,8 +188,8 @@ __host__ __device__ constexpr int64_t tile_bound(int64_t tokens, int64_t group, 
   return tokens * group / size + batch;
 }
 // Whether a batch can be cut at all: `capacity` is the most keys a request can have.
-__host__ __device__ constexpr bool may_split(int64_t batch, int64_t capacity) {
-  return batch <= kMaxSplitBatch && capacity > kMinSteps * kKeys;
+__host__ __device__ constexpr bool may_split(int64_t batch, int64_t hk, int64_t capacity) {
+  return batch <= kMaxSplitBatch && hk <= kMaxSplitHeads && capacity > kMinSteps * kKeys;
 }
 // Units per key head are at most the tiles and this many more, and partial results at most twice it.
 __host__ __device__ constexpr int64_t extra_units(int64_t hk) { return (kUnits + hk - 1) / hk; }
@@ -257,7 +258,8 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
     before_slots += total_slots;
   }
   __syncthreads();
-  if (unit >= before) return false;
+  // more units than the launch holds: cu_tokens decreases somewhere, and nothing is computed
+  if (unit >= before || static_cast<int64_t>(before) * a.hk > gridDim.x) return false;
   int lo = 0, hi = a.batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -289,38 +291,114 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
   if (piece >= u.count) return false;
   u.j0 = j0 + piece * per * kKeys;
   u.j1 = min(j1, u.j0 + per * kKeys);
-  u.first = piece == 0;
-  u.slot = (first_slot + tile * chunks + piece) * a.hk + u.head;
+  u.piece = piece;
+  u.slot = (first_slot + tile * chunks) * a.hk + u.head;
   return true;
 }
 
-// The workspace: for every tile number and head the first partial result and their count, then the
-// partial results' maxima and sums [slot][row][2], then their outputs [slot][row][D], float32.
+// The workspace: a counter for every partial result, then the partial results' maxima and sums
+// [slot][row][2], then their outputs [slot][row][D], float32.  The counters are zero between calls.
+constexpr int64_t kCounterBytes = FP8_ATTN_COUNTER_BYTES;
+static_assert(kCounterBytes >= 4 * 2 * (kUnits + kMaxSplitHeads), "slot_bound is at most 2 (kUnits + hk - 1)");
+__host__ __device__ inline int64_t slot_bound(int64_t hk) { return 2 * extra_units(hk) * hk; }
 struct Workspace {
-  int2* info;
+  int* counters;
   float* stats;
   float* out;
 };
-__host__ __device__ inline int64_t info_bytes(int64_t tiles, int64_t hk) { return (tiles * hk * 8 + 15) & ~int64_t{15}; }
-__host__ __device__ inline int64_t slot_bound(int64_t hk) { return 2 * extra_units(hk) * hk; }
 __device__ __forceinline__ Workspace workspace(const AttnArgs& a, int size) {
-  char* p = a.ws;
   Workspace w;
-  w.info = reinterpret_cast<int2*>(p);
-  p += info_bytes(tile_bound(a.tokens, a.group, a.batch, size), a.hk);
-  w.stats = reinterpret_cast<float*>(p);
+  w.counters = reinterpret_cast<int*>(a.ws);
+  w.stats = reinterpret_cast<float*>(a.ws + kCounterBytes);
   w.out = w.stats + slot_bound(a.hk) * size * 2;
   return w;
 }
-// The number find_rows knows a tile by.
-__device__ __forceinline__ int tile_number(const AttnArgs& a, const Rows& r, int size) {
-  return static_cast<int>(static_cast<int64_t>(r.begin) * a.group / size) + r.request + r.row0 / size;
+
+// Partial results pass between workgroups of one launch, whose XCDs' L2 caches do not see each
+// other: they are written and read with agent-scope accesses, which go through to memory, and a
+// writer waits for its stores before it counts itself.  (Fences in their place write back and
+// empty the whole L2: measured, they doubled the time of every split case.)
+__device__ __forceinline__ void leave2(float* p, float x, float y) {
+  const uint64_t v = static_cast<uint64_t>(__float_as_uint(x)) | static_cast<uint64_t>(__float_as_uint(y)) << 32;
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 pick2(const float* p) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
 }
 
-// Where the join finds a tile's partial results (the workgroup of the tile's first chunk tells).
-__device__ __forceinline__ void leave_info(const AttnArgs& a, const Unit& u, int size) {
-  if (threadIdx.x == 0 && u.first)
-    workspace(a, size).info[static_cast<int64_t>(tile_number(a, u.r, size)) * a.hk + u.head] = make_int2(u.slot, u.count);
+// After a workgroup's partial result is stored: the workgroup that finds itself the last of its
+// tile joins them all, in their order, so the result does not depend on who that is:
+//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// D / 4 lanes take a row's channels; with few rows, several such groups share a row's partial
+// results.  `flag` and `lds` (8 KB) are LDS that nothing else uses any more.
+template <int DT, int D, int SIZE>
+__device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, int* flag, float* lds) {
+  constexpr int kLanes = D / 4, kTeams = 256 / kLanes;
+  const Workspace ws = workspace(a, SIZE);
+  const Rows& r = u.r;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every thread's stores before the count
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int* n = ws.counters + u.slot;
+    const bool last = __hip_atomic_fetch_add(n, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == u.count - 1;
+    if (last) __hip_atomic_store(n, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = last;
+  }
+  __syncthreads();
+  if (!*flag) return;
+  const int rows = min(SIZE, r.rows - r.row0);
+  const int lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes;
+  int share = 1;        // teams to a row
+  while (2 * share * rows <= kTeams) share *= 2;
+  const int part = team % share;
+  const int passes = (rows * share + kTeams - 1) / kTeams;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int local = (pass * kTeams + team) / share;
+    const bool on = local < rows;
+    const int64_t at = static_cast<int64_t>(u.slot) * SIZE + (on ? local : 0), step = static_cast<int64_t>(a.hk) * SIZE;
+    float m = -INFINITY;
+    for (int i = lane; i < u.count; i += kLanes) m = fmaxf(m, pick2(ws.stats + (at + i * step) * 2).x);
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float mb = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+    v4f o;
+    o = 0.0f;
+#pragma unroll 4
+    for (int i = part; i < u.count; i += share) {
+      const float2 st = pick2(ws.stats + (at + i * step) * 2);
+      const float* from = ws.out + (at + i * step) * D + 4 * lane;
+      const float2 x0 = pick2(from), x1 = pick2(from + 2);
+      const float x[4] = {x0.x, x0.y, x1.x, x1.y};
+      const float w = __builtin_amdgcn_exp2f(st.x - mb);
+      l = __builtin_fmaf(w, st.y, l);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[y] = __builtin_fmaf(w, x[y], o[y]);
+    }
+    if (share > 1) {    // one pass only
+      float* to = lds + (team * kLanes + lane) * 8;
+      *reinterpret_cast<v4f*>(to) = o;
+      to[4] = l;
+      __syncthreads();
+      if (part == 0)
+        for (int k = 1; k < share; ++k) {
+          const float* from = to + k * kLanes * 8;
+          const v4f x = *reinterpret_cast<const v4f*>(from);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[y] += x[y];
+          l += from[4];
+        }
+    }
+    if (!on || part != 0) continue;
+    const int row = r.row0 + local, tok = row / a.group;
+    const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + u.head * a.group + (row - tok * a.group);
+    const bool none = r.pos0 + tok < 0;
+    const float inv = none ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D + 4 * lane) =
+        make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv));
+    if (a.lse && lane == 0) a.lse[out_row] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -373,10 +451,9 @@ __device__ __forceinline__ v16f mfma_odd(const v8s& v, const v8s& p, v16f o) {
   return o;
 }
 
-// Host side: the paged kernels for many rows and for few, and the join of partial results.
+// Host side: the paged kernels for many rows and for few.
 void launch_attn_tile(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
 void launch_attn_few(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
-void launch_attn_join(int dt, int head_dim, int size, const AttnArgs& a, hipStream_t s);
 
 }  // namespace attn
 }  // namespace fp8amax

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
     tile_keys(a, unit.r, kRows, unit.j0, unit.j1);
     unit.slot = 0;
     unit.count = 1;
-    unit.first = true;
+    unit.piece = 0;
   }
   const Rows& r = unit.r;
   const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
@@ -311,17 +311,19 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   for (int x = 0; x < 16; ++x) fine &= __builtin_isfinite(o[0][x]);
   if (__syncthreads_or(!fine)) walk(std::true_type{});
 
-  if (split) leave_info(a, unit, kRows);
-  if (wave >= D / 32 || r.row0 + col >= r.rows) return;
+  const bool mine = wave < D / 32 && r.row0 + col < r.rows;
   if (unit.count > 1) {
-    const Workspace ws = workspace(a, kRows);
-    const int64_t at = static_cast<int64_t>(unit.slot) * kRows + col;
-    if (wave == 0 && half == 0) *reinterpret_cast<float2*>(ws.stats + at * 2) = make_float2(m, l);
+    if (mine) {
+      const Workspace ws = workspace(a, kRows);
+      const int64_t at = (unit.slot + static_cast<int64_t>(unit.piece) * a.hk) * kRows + col;
+      if (wave == 0 && half == 0) leave2(ws.stats + at * 2, m, l);
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      *reinterpret_cast<v4f*>(ws.out + at * D + 32 * wave + 8 * g + 4 * half) = v4f{o[0][4 * g], o[0][4 * g + 1], o[0][4 * g + 2], o[0][4 * g + 3]};
+      for (int i = 0; i < 16; i += 2) leave2(ws.out + at * D + 32 * wave + 8 * (i / 4) + 4 * half + i % 4, o[0][i], o[0][i + 1]);
+    }
+    join_partials<DT, D, kRows>(a, unit, reinterpret_cast<int*>(stats), reinterpret_cast<float*>(lds));
     return;
   }
+  if (!mine) return;
   const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + h * a.group + (row - tok * a.group);
   const float inv = pos < 0 ? 0.0f : 1.0f / l;
   if (a.lse && wave == 0 && half == 0) a.lse[out_row] = pos < 0 ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
@@ -335,10 +337,9 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
 template <int DT, int D, int SRC>
 void launch(const AttnArgs& a, hipStream_t s) {
   const int64_t tiles = tile_bound(a.tokens, a.group, a.batch, kRows);
-  const bool split = may_split(a.batch, static_cast<int64_t>(a.width) << a.page_shift);
+  const bool split = may_split(a.batch, a.hk, static_cast<int64_t>(a.width) << a.page_shift);
   const int64_t units = (tiles + (split ? extra_units(a.hk) : 0)) * a.hk;
   attn_few_kernel<DT, D, SRC><<<static_cast<unsigned>(units), 256, 0, s>>>(a, split);
-  if (split) launch_attn_join(DT, D, kRows, a, s);
 }
 
 template <int SRC>

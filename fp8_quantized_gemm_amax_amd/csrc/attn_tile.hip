@@ -22,7 +22,7 @@ __device__ __forceinline__ bool unit_of(const AttnArgs& a, bool split, char* lds
   // heavy tiles first: a prompt's last rows see the most keys
   if (!find_rows(a, gridDim.x / a.hk - 1 - blockIdx.x / a.hk, SIZE, PAGED, u.r)) return false;
   tile_keys(a, u.r, SIZE, u.j0, u.j1);
-  u.slot = 0;
+  u.slot = u.piece = 0;
   u.count = 1;
   return true;
 }
@@ -288,10 +288,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     for (int x = 0; x < 16; ++x) fine &= __builtin_isfinite(o[i][x]);
   if (__syncthreads_or(!fine)) walk(std::true_type{});
 
-  if constexpr (kPaged) {
-    if (split) leave_info(a, unit, kRows);
-  }
-  if (r.row0 + 32 * wave >= r.rows) return;
   l = add_halves(l);
   if constexpr (kRange) {
 #pragma unroll
@@ -301,18 +297,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
   }
   const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + h * a.group + (row - tok * a.group);
   const bool store = r.row0 + 32 * wave + col < r.rows;
-  if (kPaged && unit.count > 1) {      // a partial result: maximum, sum and output as they are
-    const Workspace ws = workspace(a, kRows);
-    const int64_t at = static_cast<int64_t>(unit.slot) * kRows + 32 * wave + col;
-    if (!store) return;
-    if (half == 0) *reinterpret_cast<float2*>(ws.stats + at * 2) = make_float2(m, l);
+  if constexpr (kPaged) {
+    if (unit.count > 1) {      // a partial result: maximum, sum and output as they are
+      if (store) {
+        const Workspace ws = workspace(a, kRows);
+        const int64_t at = (unit.slot + static_cast<int64_t>(unit.piece) * a.hk) * kRows + 32 * wave + col;
+        if (half == 0) leave2(ws.stats + at * 2, m, l);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+        for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<v4f*>(ws.out + at * D + 32 * i + 8 * g + 4 * half) = v4f{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
-    return;
+          for (int x = 0; x < 16; x += 2) leave2(ws.out + at * D + 32 * i + 8 * (x / 4) + 4 * half + x % 4, o[i][x], o[i][x + 1]);
+      }
+      join_partials<DT, D, kRows>(a, unit, reinterpret_cast<int*>(lds), reinterpret_cast<float*>(lds + 1024));
+      return;
+    }
   }
+  if (r.row0 + 32 * wave >= r.rows) return;
   const float inv = pos < 0 ? 0.0f : 1.0f / l;
   if (a.lse && store && half == 0) a.lse[out_row] = pos < 0 ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
   uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * D + 8 * half;
@@ -333,10 +333,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 template <int DT, int D, int SRC>
 void launch(const AttnArgs& a, hipStream_t s) {
   const int64_t tiles = tile_bound(a.tokens, a.group, a.batch, kRows);
-  const bool split = SRC != SRC_PACKED && may_split(a.batch, static_cast<int64_t>(a.width) << a.page_shift);
+  const bool split = SRC != SRC_PACKED && may_split(a.batch, a.hk, static_cast<int64_t>(a.width) << a.page_shift);
   const int64_t units = (tiles + (split ? extra_units(a.hk) : 0)) * a.hk;
   attn_tile_kernel<DT, D, SRC><<<static_cast<unsigned>(units), 64 * kWaves, 0, s>>>(a, split);
-  if (split) launch_attn_join(DT, D, kRows, a, s);
 }
 
 template <int SRC>

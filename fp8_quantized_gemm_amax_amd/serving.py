@@ -15,6 +15,7 @@ from . import binding
 from .binding import FP8_BF16, FP8_F16, Fp8Error
 
 FP8_KV_SAME, FP8_KV_E4M3 = 0, 1
+COUNTER_BYTES = 16384          # FP8_ATTN_COUNTER_BYTES
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -263,6 +264,24 @@ def fp8_attn_prompt(q, k, v, cu_tokens, softmax_scale=None, window=0, out=None, 
     return (out, lse) if return_lse else out
 
 
+_workspaces = {}
+
+
+def _workspace(device, need):
+    """A workspace of the current stream, its counters zero at first and kept: a call leaves it fit
+    for the next.  A call that is being captured in a HIP graph gets its own, since the graph may
+    be replayed on any stream."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = device.index, _stream(device)
+    have = None if capturing else _workspaces.get(key)
+    if have is None or have.shape[0] < need:
+        have = torch.empty((need,), dtype=torch.uint8, device=device)
+        have[:COUNTER_BYTES].zero_()
+        if not capturing:
+            _workspaces[key] = have
+    return have
+
+
 def fp8_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scales=None, v_scales=None,
                    softmax_scale=None, window=0, max_new=0, out=None, return_lse=False, workspace=None):
     """Causal attention of each request's new tokens over its pages, the new ones among them.
@@ -270,8 +289,8 @@ def fp8_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scal
     q [tokens, q_heads, head_dim] packed by cu_tokens int32 [batch + 1]; caches and scales as
     fp8_kv_append writes them; block_table int32 [batch, width]; seq_lens int32 [batch], tokens in
     the cache.  max_new: the largest number of new tokens of a request if known (it only chooses
-    the kernel).  workspace: uint8, at least fp8_attn_paged_workspace(...) bytes; allocated per
-    call by default.  Returns as fp8_attn_prompt."""
+    the kernel).  workspace: uint8, at least fp8_attn_paged_workspace(...) bytes, its first
+    16 KiB zero before the first call; one per stream is kept by default.  Returns as fp8_attn_prompt."""
     dt = _dt(q, "q")
     (pages, hk, page, dim), fmt = _cache(k_cache, v_cache, k_scales, v_scales, q.dtype)
     q = _rows(q, "q", dim)
@@ -288,7 +307,7 @@ def fp8_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scal
     fns = _lib()
     need = fns["fp8_attn_paged_workspace"](tokens, batch, hq, hk, dim, width, page, max_new)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+        workspace = _workspace(q.device, need) if need else None
     else:
         if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous uint8 vector")
