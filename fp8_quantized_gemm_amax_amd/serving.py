@@ -61,50 +61,52 @@ def _dt(t, what):
     return dt
 
 
-def _check(name, code):
-    if code:
-        raise Fp8Error(name, code, binding.lib().fp8_status_string(code).decode())
+def _refuse(name, code):
+    raise Fp8Error(name, code, binding.lib().fp8_status_string(code).decode())
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# The current stream's handle of a GPU; torch.cuda.current_stream builds an object around it, which
+# takes 1.8 of the 8 to 11 us that a call takes on the host.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on(like, **tensors):
     """Every given tensor is a tensor on like's GPU (the library launches on like's stream)."""
-    device = like.device
-    if device.type != "cuda":
+    if not like.is_cuda:
         raise ValueError("all tensors must be on the GPU")
     for what, t in tensors.items():
-        if t.device != device:
-            raise ValueError(f"{what} must be on {device}, got {t.device}")
+        if t.device != like.device:
+            raise ValueError(f"{what} must be on {like.device}, got {t.device}")
 
 
 def _dense(t, what, dtype, shape):
     """A dense operand of one type and shape, read or written where it lies."""
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t
 
 
-def _rows(t, what, heads_dim=None):
+def _rows(t, what, head_dim=None):
     """A [tokens, heads, dim] operand whose rows the kernels read 16 bytes at a time: as it lies
     if its last index is contiguous, the other strides are multiples of 8 and tokens do not overlap,
-    else a copy."""
+    else a copy.  Returns the tensor, its address and its token and head strides."""
     if t.dim() != 3:
         raise ValueError(f"{what} must be [tokens, heads, head_dim], got shape {tuple(t.shape)}")
-    if heads_dim is not None and t.shape[2] != heads_dim:
-        raise ValueError(f"{what} must have head_dim {heads_dim}, got {t.shape[2]}")
+    if head_dim is not None and t.shape[2] != head_dim:
+        raise ValueError(f"{what} must have head_dim {head_dim}, got {t.shape[2]}")
     ts, hs, one = t.stride()
-    if one != 1 or (ts | hs) & 7 or t.data_ptr() & 15 or ts < t.shape[2] or ts > 1 << 20:
+    at = t.data_ptr()
+    if one != 1 or (ts | hs | at >> 1) & 7 or ts < t.shape[2] or ts > 1 << 20:
         t = t.contiguous()
         if t.data_ptr() & 15:
             t = t.clone()
-    return t
+        ts, hs, _ = t.stride()
+        at = t.data_ptr()
+    return t, at, ts, hs
 
 
 def _vector(t, what, dtype=torch.int32, size=None):
@@ -131,11 +133,13 @@ class PagedPlan(NamedTuple):
 
 def paged_plan_buffers(batch, tokens, device):
     """Buffers for fp8_paged_plan's `out` (to reuse them, or to capture the call in a HIP graph)."""
-    # one allocation: the int64 slots first, then the int32 outputs
-    ints = torch.empty((2 * tokens + 2 * batch + 1 + tokens + 2,), dtype=torch.int32, device=device)
-    slots = ints[: 2 * tokens].view(torch.int64)
-    positions, cu, lens, taken, missing = ints[2 * tokens:].split([tokens, batch + 1, batch, 1, 1])
-    return PagedPlan(cu, lens, positions, slots, taken, missing)
+    return _plan_buffers(torch.empty((3 * tokens + 2 * batch + 3,), dtype=torch.int32, device=device), batch, tokens)
+
+
+def _plan_buffers(ints, batch, tokens):
+    # one allocation, the 64-bit slots first
+    slots, positions, cu, lens, taken, missing = ints.unsafe_split_with_sizes([2 * tokens, tokens, batch + 1, batch, 1, 1])
+    return PagedPlan(cu, lens, positions, slots.view(torch.int64), taken, missing)
 
 
 def fp8_paged_plan(cached, added, block_table, free_pages, taken, tokens, page_size, out=None):
@@ -149,49 +153,57 @@ def fp8_paged_plan(cached, added, block_table, free_pages, taken, tokens, page_s
     cached, added = _vector(cached, "cached"), _vector(added, "added", size=batch)
     free_pages, taken = _vector(free_pages, "free_pages"), _vector(taken, "taken", size=1)
     _table(block_table, batch)
-    _on(cached, added=added, block_table=block_table, free_pages=free_pages, taken=taken)
+    gpu = cached.get_device()
+    if gpu < 0 or not gpu == added.get_device() == block_table.get_device() == free_pages.get_device() == taken.get_device():
+        _on(cached, added=added, block_table=block_table, free_pages=free_pages, taken=taken)
     if out is None:
         if tokens < 0:
             raise ValueError(f"tokens must not be negative, got {tokens}")
-        out = paged_plan_buffers(batch, tokens, cached.device)
+        ints = cached.new_empty(3 * tokens + 2 * batch + 3)
+        out = _plan_buffers(ints, batch, tokens)
+        # the parts' addresses, in paged_plan_buffers' order
+        slots = ints.data_ptr()
+        positions = slots + 8 * tokens
+        cu = positions + 4 * tokens
+        lens = cu + 4 * (batch + 1)
+        taken_out = lens + 4 * batch
+        missing = taken_out + 4
     else:
         for what, dtype, n in (("cu_tokens", torch.int32, batch + 1), ("seq_lens", torch.int32, batch),
                                ("positions", torch.int32, tokens), ("slots", torch.int64, tokens),
                                ("taken", torch.int32, 1), ("missing", torch.int32, 1)):
             t = getattr(out, what)
             binding._check_out(t, (n,), (dtype,), f"out.{what}", cached, (cached, added, block_table, free_pages, taken))
-    _check("fp8_paged_plan", _lib()["fp8_paged_plan"](
+        cu, lens, positions, slots, taken_out, missing = (t.data_ptr() for t in out)
+    code = (_fns or _lib())["fp8_paged_plan"](
         cached.data_ptr(), added.data_ptr(), batch, page_size, block_table.data_ptr(), block_table.shape[1],
-        free_pages.data_ptr(), free_pages.shape[0], taken.data_ptr(), tokens, out.cu_tokens.data_ptr(),
-        out.seq_lens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(), out.taken.data_ptr(),
-        out.missing.data_ptr(), _stream(cached.device)))
+        free_pages.data_ptr(), free_pages.shape[0], taken.data_ptr(), tokens, cu, lens, positions, slots, taken_out,
+        missing, _raw_stream(gpu))
+    if code:
+        _refuse("fp8_paged_plan", code)
     return out
 
 
-def _cache(k_cache, v_cache, k_scales, v_scales, dtype, what="k_cache"):
+def _cache(k_cache, v_cache, k_scales, v_scales, dtype):
     """Shape (pages, heads, page_size, dim) and format of a cache."""
-    if k_cache.dim() != 4:
-        raise ValueError(f"{what} must be [pages, kv_heads, page_size, head_dim], got {tuple(k_cache.shape)}")
-    shape = tuple(k_cache.shape)
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError(f"k_cache and v_cache must have one type, got {k_cache.dtype} and {v_cache.dtype}")
-    _dense(k_cache, "k_cache", k_cache.dtype, shape)
-    _dense(v_cache, "v_cache", k_cache.dtype, shape)
+    shape, kind = k_cache.shape, k_cache.dtype
+    if len(shape) != 4:
+        raise ValueError(f"k_cache must be [pages, kv_heads, page_size, head_dim], got {tuple(shape)}")
+    if v_cache.dtype != kind:
+        raise TypeError(f"k_cache and v_cache must have one type, got {kind} and {v_cache.dtype}")
+    _dense(k_cache, "k_cache", kind, shape)
+    _dense(v_cache, "v_cache", kind, shape)
     if (k_scales is None) != (v_scales is None):
         raise ValueError("k_scales and v_scales go together")
     if k_scales is None:
-        if k_cache.dtype != dtype:
-            raise TypeError(f"a cache without scales must be {dtype}, got {k_cache.dtype}")
+        if kind != dtype:
+            raise TypeError(f"a cache without scales must be {dtype}, got {kind}")
         return shape, FP8_KV_SAME
-    if k_cache.dtype not in _CODE_TYPES:
-        raise TypeError(f"a cache with scales must be uint8 or float8_e4m3fn, got {k_cache.dtype}")
+    if kind not in _CODE_TYPES:
+        raise TypeError(f"a cache with scales must be uint8 or float8_e4m3fn, got {kind}")
     _dense(k_scales, "k_scales", torch.float32, shape[:3])
     _dense(v_scales, "v_scales", torch.float32, shape[:3])
     return shape, FP8_KV_E4M3
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
 
 
 def fp8_kv_append(k, v, slots, k_cache, v_cache, k_scales=None, v_scales=None):
@@ -202,28 +214,36 @@ def fp8_kv_append(k, v, slots, k_cache, v_cache, k_scales=None, v_scales=None):
     if v.dtype != k.dtype or v.shape != k.shape:
         raise ValueError(f"v must be like k, got {v.dtype} {tuple(v.shape)} and {k.dtype} {tuple(k.shape)}")
     (pages, heads, page, dim), fmt = _cache(k_cache, v_cache, k_scales, v_scales, k.dtype)
-    k, v = _rows(k, "k", dim), _rows(v, "v", dim)
+    k, k_at, kts, khs = _rows(k, "k", dim)
+    v, v_at, vts, vhs = _rows(v, "v", dim)
+    tokens = k.shape[0]
     if k.shape[1] != heads:
         raise ValueError(f"k has {k.shape[1]} heads, the cache {heads}")
-    tokens = k.shape[0]
     slots = _vector(slots, "slots", torch.int64, tokens)
-    _on(k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache)
+    gpu = k.get_device()
+    if gpu < 0 or not gpu == v.get_device() == slots.get_device() == k_cache.get_device() == v_cache.get_device():
+        _on(k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache)
+    ks = vs = None
     if fmt == FP8_KV_E4M3:
-        _on(k, k_scales=k_scales, v_scales=v_scales)
-    _check("fp8_kv_append", _lib()["fp8_kv_append"](
-        k.data_ptr(), v.data_ptr(), dt, tokens, heads, dim, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-        slots.data_ptr(), pages, page, fmt, k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scales), _at(v_scales),
-        _stream(k.device)))
+        if not gpu == k_scales.get_device() == v_scales.get_device():
+            _on(k, k_scales=k_scales, v_scales=v_scales)
+        ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+    code = (_fns or _lib())["fp8_kv_append"](
+        k_at, v_at, dt, tokens, heads, dim, kts, khs, vts, vhs, slots.data_ptr(), pages, page, fmt,
+        k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, _raw_stream(gpu))
+    if code:
+        _refuse("fp8_kv_append", code)
     return k_cache, v_cache
 
 
-def _outputs(q, out, return_lse, inputs):
-    shape = tuple(q.shape)
+def _output(q, out, inputs):
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    else:
-        binding._check_out(out, shape, (q.dtype,), "out", q, inputs)
-    return out, torch.empty(shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+        return torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
+    return binding._check_out(out, tuple(q.shape), (q.dtype,), "out", q, [_span_of(t) for t in inputs if t is not None])
+
+
+def _sums(q, return_lse):
+    return torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
 
 
 def _scale(softmax_scale, dim):
@@ -249,33 +269,39 @@ def fp8_attn_prompt(q, k, v, cu_tokens, softmax_scale=None, window=0, out=None, 
     dt = _dt(q, "q")
     if k.dtype != q.dtype or v.dtype != q.dtype or v.shape != k.shape:
         raise ValueError(f"k and v must be alike and of q's type, got {k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
-    q = _rows(q, "q")
+    q, q_at, qts, qhs = _rows(q, "q")
     tokens, hq, dim = q.shape
-    k, v = _rows(k, "k", dim), _rows(v, "v", dim)
+    k, k_at, kts, khs = _rows(k, "k", dim)
+    v, v_at, vts, vhs = _rows(v, "v", dim)
     if k.shape[0] != tokens:
         raise ValueError(f"q has {tokens} tokens, k {k.shape[0]}")
     cu_tokens = _vector(cu_tokens, "cu_tokens")
-    _on(q, k=k, v=v, cu_tokens=cu_tokens)
-    out, lse = _outputs(q, out, return_lse, () if out is None else (_span_of(q), _span_of(k), _span_of(v), cu_tokens))
-    _check("fp8_attn_prompt", _lib()["fp8_attn_prompt"](
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, tokens, cu_tokens.data_ptr(), cu_tokens.shape[0] - 1, hq,
-        k.shape[1], dim, q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-        _scale(softmax_scale, dim), window, out.data_ptr(), _at(lse), _stream(q.device)))
+    gpu = q.get_device()
+    if gpu < 0 or not gpu == k.get_device() == v.get_device() == cu_tokens.get_device():
+        _on(q, k=k, v=v, cu_tokens=cu_tokens)
+    out = _output(q, out, (q, k, v, cu_tokens))
+    lse = _sums(q, return_lse)
+    code = (_fns or _lib())["fp8_attn_prompt"](
+        q_at, k_at, v_at, dt, tokens, cu_tokens.data_ptr(), cu_tokens.shape[0] - 1, hq, k.shape[1], dim, qts, qhs, kts,
+        khs, vts, vhs, _scale(softmax_scale, dim), window, out.data_ptr(), lse.data_ptr() if return_lse else None,
+        _raw_stream(gpu))
+    if code:
+        _refuse("fp8_attn_prompt", code)
     return (out, lse) if return_lse else out
 
 
 _workspaces = {}
 
 
-def _workspace(device, need):
+def _workspace(q, stream, need):
     """A workspace of the current stream, its counters zero at first and kept: a call leaves it fit
     for the next.  A call that is being captured in a HIP graph gets its own, since the graph may
     be replayed on any stream."""
     capturing = torch.cuda.is_current_stream_capturing()
-    key = device.index, _stream(device)
+    key = q.get_device(), stream
     have = None if capturing else _workspaces.get(key)
     if have is None or have.shape[0] < need:
-        have = torch.empty((need,), dtype=torch.uint8, device=device)
+        have = torch.empty((max(need, COUNTER_BYTES),), dtype=torch.uint8, device=q.device)
         have[:COUNTER_BYTES].zero_()
         if not capturing:
             _workspaces[key] = have
@@ -293,30 +319,37 @@ def fp8_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scal
     16 KiB zero before the first call; one per stream is kept by default.  Returns as fp8_attn_prompt."""
     dt = _dt(q, "q")
     (pages, hk, page, dim), fmt = _cache(k_cache, v_cache, k_scales, v_scales, q.dtype)
-    q = _rows(q, "q", dim)
+    q, q_at, qts, qhs = _rows(q, "q", dim)
     tokens, hq, _ = q.shape
     seq_lens = _vector(seq_lens, "seq_lens")
     batch = seq_lens.shape[0]
     cu_tokens = _vector(cu_tokens, "cu_tokens", size=batch + 1)
     width = _table(block_table, batch).shape[1]
-    _on(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, cu_tokens=cu_tokens)
+    gpu = q.get_device()
+    if gpu < 0 or not gpu == k_cache.get_device() == v_cache.get_device() == block_table.get_device() == seq_lens.get_device() == cu_tokens.get_device():
+        _on(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, cu_tokens=cu_tokens)
+    ks = vs = None
     if fmt == FP8_KV_E4M3:
-        _on(q, k_scales=k_scales, v_scales=v_scales)
-    out, lse = _outputs(q, out, return_lse, () if out is None else (
-        _span_of(q), k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scales, v_scales))
-    fns = _lib()
-    need = fns["fp8_attn_paged_workspace"](tokens, batch, hq, hk, dim, width, page, max_new)
+        if not gpu == k_scales.get_device() == v_scales.get_device():
+            _on(q, k_scales=k_scales, v_scales=v_scales)
+        ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+    out = _output(q, out, (q, k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scales, v_scales))
+    lse = _sums(q, return_lse)
+    fns = _fns or _lib()
+    stream = _raw_stream(gpu)
     if workspace is None:
-        workspace = _workspace(q.device, need) if need else None
+        workspace = _workspace(q, stream, fns["fp8_attn_paged_workspace"](tokens, batch, hq, hk, dim, width, page, max_new))
     else:
         if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous uint8 vector")
         _on(q, workspace=workspace)
-    _check("fp8_attn_paged", fns["fp8_attn_paged"](
-        q.data_ptr(), dt, tokens, cu_tokens.data_ptr(), batch, hq, hk, dim, q.stride(0), q.stride(1), fmt,
-        k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scales), _at(v_scales), pages, page, block_table.data_ptr(),
-        width, seq_lens.data_ptr(), _scale(softmax_scale, dim), window, max_new, out.data_ptr(), _at(lse),
-        _at(workspace), 0 if workspace is None else workspace.shape[0], _stream(q.device)))
+    code = fns["fp8_attn_paged"](
+        q_at, dt, tokens, cu_tokens.data_ptr(), batch, hq, hk, dim, qts, qhs, fmt, k_cache.data_ptr(),
+        v_cache.data_ptr(), ks, vs, pages, page, block_table.data_ptr(), width, seq_lens.data_ptr(),
+        _scale(softmax_scale, dim), window, max_new, out.data_ptr(), lse.data_ptr() if return_lse else None,
+        workspace.data_ptr(), workspace.shape[0], stream)
+    if code:
+        _refuse("fp8_attn_paged", code)
     return (out, lse) if return_lse else out
 
 
