@@ -1,4 +1,4 @@
-// attention.hip - attention over a paged cache: the choice of kernel and the workspace.
+// attention.hip - the choice of kernel for attention over a paged cache, and its workspace.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,9 +25,9 @@ void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnA
 int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
                              int64_t max_new) {
   using namespace attn;
-  if (!may_split(batch, hk, capacity)) return 0;
-  const int size = few_rows(max_new, hq / hk, tokens, batch) ? 32 : 128;
-  return kCounterBytes + slot_bound(hk) * size * (head_dim + 2) * 4;
+  if (!may_split(tokens, hq / hk, batch, hk, capacity)) return 0;
+  const bool few = few_rows(max_new, hq / hk, tokens, batch);
+  return workspace_bytes(few ? 2 * kFewGroups : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
 }
 
 }  // namespace fp8amax

@@ -157,23 +157,21 @@ __device__ __forceinline__ v4i key_rows(const AttnArgs& a, const Rows& r, const 
 
 // ------------------------------------------------------------------------------------------
 // Splitting a long axis.  Few rows over many keys would leave most of the card idle, so the keys
-// of a tile of rows are cut into chunks that different workgroups take, each leaving its maximum,
-// sum and output for attn_join.  The requests' lengths are on the device, so the cut is made there:
-// every workgroup sums the work of the whole batch (three integers a request) and takes
-//   steps of 64 keys a chunk = max(kMinSteps, work / kUnits)
-// which cuts long requests into more chunks than short ones and leaves a full batch of equal
-// lengths uncut.  Then units (request, tile, chunk) are numbered request by request.
-constexpr int kUnits = 1024;       // units wanted on the card, over all key heads
-constexpr int kMinSteps = 4;       // no chunk below 256 keys: a unit's start and end cost about that
-constexpr int kMaxSplitBatch = 1024;   // above, there are enough units without cuts
+// of a tile of rows are cut into pieces that different workgroups take, each leaving its maximum,
+// sum and output, which the last of them joins.  The requests' lengths are on the device, so the
+// cut is made there: every workgroup sums the batch's work (three integers a request).
+constexpr int kMaxSplitBatch = 1024;   // above, there is enough to do without cuts
 constexpr int kMaxSplitHeads = 1024;
+constexpr int kMinKeys = 256;          // no piece below: a piece's start and end cost about that
+constexpr int kMaxSlots = 4096;        // partial results of a launch
 
 struct Unit {
   Rows r;
   int head;
-  int j0, j1;       // its keys
-  int piece, count; // its chunk and how many there are of the tile (1: the whole)
-  int slot;         // where the tile's partial results begin, hk apart
+  int j0, j1;        // its keys
+  int piece, count;  // its piece and how many there are of the tile (1: the whole)
+  int slot0, slot1, slot_step;   // the tile's partial results: slot0, then slot1 and every slot_step
+  __device__ __forceinline__ int64_t slot(int p) const { return p == 0 ? slot0 : slot1 + static_cast<int64_t>(p - 1) * slot_step; }
 };
 
 // Keys [j0, j1) that the rows of a tile see between them, j0 a multiple of 64.
@@ -187,21 +185,43 @@ __device__ __forceinline__ void tile_keys(const AttnArgs& a, const Rows& r, int 
 __host__ __device__ constexpr int64_t tile_bound(int64_t tokens, int64_t group, int64_t batch, int size) {
   return tokens * group / size + batch;
 }
-// Whether a batch can be cut at all: `capacity` is the most keys a request can have.
-__host__ __device__ constexpr bool may_split(int64_t batch, int64_t hk, int64_t capacity) {
-  return batch <= kMaxSplitBatch && hk <= kMaxSplitHeads && capacity > kMinSteps * kKeys;
+// Whether a batch is cut at all: `capacity` is the most keys a request can have.
+__host__ __device__ constexpr bool may_split(int64_t tokens, int64_t group, int64_t batch, int64_t hk, int64_t capacity) {
+  return batch <= kMaxSplitBatch && hk <= kMaxSplitHeads && capacity > kMinKeys &&
+         tile_bound(tokens, group, batch, 32) * (capacity / kKeys + 1) < (int64_t{1} << 30);
 }
-// Units per key head are at most the tiles and this many more, and partial results at most twice it.
-__host__ __device__ constexpr int64_t extra_units(int64_t hk) { return (kUnits + hk - 1) / hk; }
 
-// The inclusive sum of x over the workgroup's 256 threads; total gets the last one's.
-__device__ __forceinline__ int scan256(int x, int* part, int& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Tiles of a request, and steps of `step` keys that its rows see between them.
+struct Shape {
+  int tiles, steps, low;   // low: the first key
+  bool bad;                // cu_tokens decreases here
+};
+template <int SIZE, bool PAGED>
+__device__ __forceinline__ Shape shape_of(const AttnArgs& a, int i, int step) {
+  const int begin = min(max(a.cu[i], 0), a.tokens), n = min(max(a.cu[i + 1], 0), a.tokens) - begin;
+  const int len = PAGED ? min(max(a.lens[i], 0), a.width << a.page_shift) : max(n, 0);
+  Shape s;
+  s.bad = a.cu[i + 1] < a.cu[i];
+  s.tiles = n > 0 ? static_cast<int>((static_cast<int64_t>(n) * a.group + SIZE - 1) / SIZE) : 0;
+  s.low = a.window > 0 ? max(0, len - n - a.window + 1) & ~(kKeys - 1) : 0;
+  s.steps = max(1, (len - s.low + step - 1) / step);
+  return s;
+}
+
+// The inclusive sum of x over a wave.
+__device__ __forceinline__ int scan64(int x) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int y = __shfl_up(x, d);
     if (lane >= d) x += y;
   }
+  return x;
+}
+// The same over the workgroup's 256 threads; total gets the last one's.
+__device__ __forceinline__ int scan256(int x, int* part, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  x = scan64(x);
   __syncthreads();
   if (lane == 63) part[wave] = x;
   __syncthreads();
@@ -214,93 +234,133 @@ __device__ __forceinline__ int scan256(int x, int* part, int& total) {
   return x;
 }
 
-// Unit `block` of the launch (block = unit * hk + head); `lds`: 4 * (2 * kMaxSplitBatch + 8) bytes,
-// free again on return.  False where there is none.
-template <int SIZE>
-__device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds, Unit& u) {
-  u.head = block % a.hk;
-  const int unit = block / a.hk;
-  int *ends = lds, *slots = lds + kMaxSplitBatch, *part = lds + 2 * kMaxSplitBatch;
-  auto shape = [&](int i, int& tiles, int& steps) {
-    const int begin = min(max(a.cu[i], 0), a.tokens), n = min(max(a.cu[i + 1], 0), a.tokens) - begin;
-    const int len = min(max(a.lens[i], 0), a.width << a.page_shift);
-    tiles = n > 0 ? static_cast<int>((static_cast<int64_t>(n) * a.group + SIZE - 1) / SIZE) : 0;
-    const int lo = a.window > 0 ? max(0, len - n - a.window + 1) & ~(kKeys - 1) : 0;
-    steps = max(1, (len - lo + kKeys - 1) / kKeys);
-  };
-  int64_t work = 0;
-  for (int i = threadIdx.x; i < a.batch; i += 256) {
-    int tiles, steps;
-    shape(i, tiles, steps);
-    work += static_cast<int64_t>(tiles) * steps;
-  }
-  for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);
-  int64_t* sums = reinterpret_cast<int64_t*>(part);
-  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = work;
-  __syncthreads();
-  work = sums[0] + sums[1] + sums[2] + sums[3];
-  const int64_t want = (work * a.hk + kUnits - 1) / kUnits;
-  const int chunk = static_cast<int>(max(want, int64_t{kMinSteps}));
-  int before = 0, before_slots = 0;
-  for (int i0 = 0; i0 < a.batch; i0 += 256) {
-    const int i = i0 + threadIdx.x;
-    int tiles = 0, steps = 1;
-    if (i < a.batch) shape(i, tiles, steps);
-    const int chunks = (steps + chunk - 1) / chunk;
-    int total, total_slots;
-    const int e = scan256(tiles * chunks, part, total);
-    const int s = scan256(chunks > 1 ? tiles * chunks : 0, part, total_slots);
-    if (i < a.batch) {
-      ends[i] = before + e;
-      slots[i] = before_slots + s;
+// Inclusive sums over the requests of a number each has: in the lanes of every wave for up to 64
+// requests (no barrier), else in LDS (`ends`, kMaxSplitBatch, and `part`, 4 integers).
+// A batch whose cu_tokens decreases somewhere has a total of 0: nothing is computed for it.
+struct Sums {
+  int *ends, *part;
+  int mine, total;
+  template <int SIZE, bool PAGED, typename F>
+  __device__ __forceinline__ void make(const AttnArgs& a, int step, F number) {
+    bool bad = false;
+    auto at = [&](int i) {
+      const Shape s = shape_of<SIZE, PAGED>(a, i, step);
+      bad |= s.bad;
+      return number(s);
+    };
+    if (a.batch <= 64) {
+      const int lane = threadIdx.x & 63;
+      mine = scan64(lane < a.batch ? at(lane) : 0);
+      total = __any(bad) ? 0 : __builtin_amdgcn_readlane(mine, 63);
+      return;
     }
-    before += total;
-    before_slots += total_slots;
+    int before = 0;
+    for (int i0 = 0; i0 < a.batch; i0 += 256) {
+      const int i = i0 + threadIdx.x;
+      int sum;
+      const int e = scan256(i < a.batch ? at(i) : 0, part, sum);
+      if (i < a.batch) ends[i] = before + e;
+      before += sum;
+    }
+    total = __syncthreads_or(bad) ? 0 : before;
   }
-  __syncthreads();
-  // more units than the launch holds: cu_tokens decreases somewhere, and nothing is computed
-  if (unit >= before || static_cast<int64_t>(before) * a.hk > gridDim.x) return false;
-  int lo = 0, hi = a.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ends[mid] > unit) hi = mid;
-    else lo = mid + 1;
+  // The first request whose sum is above x < total, and the sum up to it (uniform).
+  __device__ __forceinline__ int find(int batch, int x, int& end) const {
+    if (batch <= 64) {
+      const int i = __builtin_ctzll(__ballot(mine > x) | (uint64_t{1} << 63));
+      end = __builtin_amdgcn_readlane(mine, i);
+      return i;
+    }
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > x) hi = mid;
+      else lo = mid + 1;
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    end = __builtin_amdgcn_readfirstlane(ends[lo]);
+    return lo;
   }
-  const int i = __builtin_amdgcn_readfirstlane(lo);
-  int tiles, steps;
-  shape(i, tiles, steps);
-  const int chunks = (steps + chunk - 1) / chunk;
-  const int local = unit - (ends[i] - tiles * chunks);
-  // the last tiles see the most keys: they go first
-  const int tile = __builtin_amdgcn_readfirstlane(tiles - 1 - local / chunks), piece = __builtin_amdgcn_readfirstlane(local % chunks);
-  const int first_slot = __builtin_amdgcn_readfirstlane(slots[i]) - tiles * chunks;
-  __syncthreads();
-  Rows& r = u.r;
+};
+
+template <int SIZE, bool PAGED>
+__device__ __forceinline__ void set_rows(const AttnArgs& a, int i, int tile, Rows& r) {
   r.request = i;
   r.begin = clamp_cu(a, i);
   r.tokens = clamp_cu(a, i + 1) - r.begin;
   r.rows = r.tokens * a.group;
   r.row0 = tile * SIZE;
-  r.len = min(max(scalar_int(a.lens + i), 0), a.width << a.page_shift);
+  r.len = PAGED ? min(max(scalar_int(a.lens + i), 0), a.width << a.page_shift) : r.tokens;
   r.pos0 = r.len - r.tokens;
+}
+
+// The cut for many rows, where the work of tiles differs (a prompt's last rows see the most keys)
+// and the hardware's own order of workgroups balances it: pieces of
+//   max(kMinKeys, work / kUnits)
+// keys, numbered request by request, the tiles that see the most first.  A full batch of equal
+// lengths stays uncut.
+constexpr int kUnits = 1024;
+// Units per key head are at most the tiles and this many more, and partial results at most twice it.
+__host__ __device__ constexpr int64_t extra_units(int64_t hk) { return (kUnits + hk - 1) / hk; }
+static_assert(2 * (kUnits + kMaxSplitHeads) <= kMaxSlots, "partial results of the cut for many rows");
+
+// Unit `block` of the launch (block = unit * hk + head).  `lds`: 4 * (kMaxSplitBatch + 4) bytes, free
+// again on return.  False where there is none.
+template <int SIZE, bool PAGED>
+__device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds, Unit& u) {
+  u.head = block % a.hk;
+  const int unit = block / a.hk;
+  Sums sums{lds, lds + kMaxSplitBatch, 0, 0};
+  sums.make<SIZE, PAGED>(a, kKeys, [](const Shape& s) { return s.tiles * s.steps; });
+  const int64_t want = (static_cast<int64_t>(sums.total) * a.hk + kUnits - 1) / kUnits;
+  const int most = static_cast<int>(max(want, int64_t{kMinKeys / kKeys}));   // steps a piece
+  sums.make<SIZE, PAGED>(a, kKeys, [&](const Shape& s) { return s.tiles * ((s.steps + most - 1) / most); });
+  if (unit >= sums.total) return false;
+  int end;
+  const int i = sums.find(a.batch, unit, end);
+  const Shape s = shape_of<SIZE, PAGED>(a, i, kKeys);
+  const int pieces = __builtin_amdgcn_readfirstlane((s.steps + most - 1) / most);
+  const int tiles = __builtin_amdgcn_readfirstlane(s.tiles);
+  const int local = unit - (end - tiles * pieces);
+  const int tile = tiles - 1 - local / pieces;
+  u.piece = local % pieces;
+  u.slot0 = 0;
+  if (pieces > 1) {
+    sums.make<SIZE, PAGED>(a, kKeys, [&](const Shape& x) {
+      const int n = (x.steps + most - 1) / most;
+      return n > 1 ? x.tiles * n : 0;
+    });
+    int slots;
+    if (a.batch <= 64) slots = __builtin_amdgcn_readlane(sums.mine, i);
+    else slots = __builtin_amdgcn_readfirstlane(sums.ends[i]);
+    u.slot0 = (slots - tiles * pieces + tile * pieces) * a.hk + u.head;
+  }
+  if (a.batch > 64) __syncthreads();
+  set_rows<SIZE, PAGED>(a, i, tile, u.r);
   int j0, j1;
-  tile_keys(a, r, SIZE, j0, j1);
+  tile_keys(a, u.r, SIZE, j0, j1);
   const int own = (j1 - j0 + kKeys - 1) / kKeys;
-  const int per = max(1, (own + chunks - 1) / chunks);
+  const int per = max(1, (own + pieces - 1) / pieces);
   u.count = max(1, (own + per - 1) / per);
-  if (piece >= u.count) return false;
-  u.j0 = j0 + piece * per * kKeys;
+  if (u.piece >= u.count) return false;
+  u.j0 = j0 + u.piece * per * kKeys;
   u.j1 = min(j1, u.j0 + per * kKeys);
-  u.piece = piece;
-  u.slot = (first_slot + tile * chunks) * a.hk + u.head;
+  u.slot1 = u.slot0 + a.hk;
+  u.slot_step = a.hk;
   return true;
 }
 
+// The cut for few rows, where the keys are read once and every step costs the same: the batch's
+// steps in one line, an equal stretch for each of kFewGroups workgroups (two to a CU).
+constexpr int kFewGroups = 512;
+static_assert(2 * kFewGroups <= kMaxSlots, "partial results of the cut for few rows");
+
 // The workspace: a counter for every partial result, then the partial results' maxima and sums
-// [slot][row][2], then their outputs [slot][row][D], float32.  The counters are zero between calls.
+// [slot][row][2], then their outputs, float32.  The counters are zero between calls.  An output lies
+// as the matrix unit leaves it, so that whole lines are written: [slot][row / 32][channel / 32]
+// [channel % 32 / 8][channel % 8 / 4][row % 32][channel % 4].
 constexpr int64_t kCounterBytes = FP8_ATTN_COUNTER_BYTES;
-static_assert(kCounterBytes >= 4 * 2 * (kUnits + kMaxSplitHeads), "slot_bound is at most 2 (kUnits + hk - 1)");
-__host__ __device__ inline int64_t slot_bound(int64_t hk) { return 2 * extra_units(hk) * hk; }
+static_assert(kCounterBytes >= 4 * kMaxSlots, "a counter a slot");
 struct Workspace {
   int* counters;
   float* stats;
@@ -310,8 +370,11 @@ __device__ __forceinline__ Workspace workspace(const AttnArgs& a, int size) {
   Workspace w;
   w.counters = reinterpret_cast<int*>(a.ws);
   w.stats = reinterpret_cast<float*>(a.ws + kCounterBytes);
-  w.out = w.stats + slot_bound(a.hk) * size * 2;
+  w.out = w.stats + static_cast<int64_t>(kMaxSlots) * size * 2;
   return w;
+}
+__host__ __device__ constexpr int64_t workspace_bytes(int64_t slots, int size, int head_dim) {
+  return kCounterBytes + int64_t{kMaxSlots} * size * 8 + slots * size * head_dim * 4;
 }
 
 // Partial results pass between workgroups of one launch, whose XCDs' L2 caches do not see each
@@ -326,21 +389,41 @@ __device__ __forceinline__ float2 pick2(const float* p) {
   const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
 }
+// A lane's 16 outputs of 32 channels: `to` the block of its 32 rows and 32 channels.
+__device__ __forceinline__ void leave_block(float* to, const v16f& o) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    leave2(to + g * 256 + lane * 4, o[4 * g], o[4 * g + 1]);
+    leave2(to + g * 256 + lane * 4 + 2, o[4 * g + 2], o[4 * g + 3]);
+  }
+}
+
+// A sum of weights and outputs relative to the largest exponent met.
+struct Joined {
+  float m, l, o[4];
+  __device__ __forceinline__ void add(float m2, float l2, const float (&x)[4]) {
+    const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.0f : top;
+    const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(m2 - base);
+    l = __builtin_fmaf(g, l2, l * f);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) o[y] = __builtin_fmaf(g, x[y], o[y] * f);
+    m = top;
+  }
+};
 
 // After a workgroup's partial result is stored: the workgroup that finds itself the last of its
-// tile joins them all, in their order, so the result does not depend on who that is:
-//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-// D / 4 lanes take a row's channels; with few rows, several such groups share a row's partial
-// results.  `flag` and `lds` (8 KB) are LDS that nothing else uses any more.
+// tile joins them all, in their order, so the result does not depend on who that is.  A thread takes
+// four channels of a row; with few rows, several share the row's partial results.  `flag` and `lds`
+// (8 KB) are LDS that nothing else uses any more.
 template <int DT, int D, int SIZE>
 __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, int* flag, float* lds) {
-  constexpr int kLanes = D / 4, kTeams = 256 / kLanes;
   const Workspace ws = workspace(a, SIZE);
   const Rows& r = u.r;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every thread's stores before the count
   __syncthreads();
   if (threadIdx.x == 0) {
-    int* n = ws.counters + u.slot;
+    int* n = ws.counters + u.slot0;
     const bool last = __hip_atomic_fetch_add(n, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == u.count - 1;
     if (last) __hip_atomic_store(n, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     *flag = last;
@@ -348,56 +431,54 @@ __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, 
   __syncthreads();
   if (!*flag) return;
   const int rows = min(SIZE, r.rows - r.row0);
-  const int lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes;
-  int share = 1;        // teams to a row
-  while (2 * share * rows <= kTeams) share *= 2;
-  const int part = team % share;
-  const int passes = (rows * share + kTeams - 1) / kTeams;
-  for (int pass = 0; pass < passes; ++pass) {
-    const int local = (pass * kTeams + team) / share;
+  int bits = 0;                       // rows, rounded up to a power of two
+  while ((1 << bits) < rows) ++bits;
+  const int items = (D / 4) << bits;
+  const int share = items < 256 ? 256 / items : 1;
+  for (int n = threadIdx.x; n < max(items, 256); n += 256) {
+    const int part = n / items, at = n - part * items;
+    const int local = at & ((1 << bits) - 1), quad = at >> bits;   // quad: channels 4 quad .. 4 quad + 3
     const bool on = local < rows;
-    const int64_t at = static_cast<int64_t>(u.slot) * SIZE + (on ? local : 0), step = static_cast<int64_t>(a.hk) * SIZE;
-    float m = -INFINITY;
-    for (int i = lane; i < u.count; i += kLanes) m = fmaxf(m, pick2(ws.stats + (at + i * step) * 2).x);
+    const int row = on ? local : 0;
+    const int64_t off = ((row >> 5) * (D / 32) + (quad >> 3)) * 1024 + ((quad >> 1) & 3) * 256 + (quad & 1) * 128 + (row & 31) * 4;
+    Joined j{-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int i0 = part; i0 < u.count; i0 += 8 * share) {
+      float2 st[8], x0[8], x1[8];
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    const float mb = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    v4f o;
-    o = 0.0f;
-#pragma unroll 4
-    for (int i = part; i < u.count; i += share) {
-      const float2 st = pick2(ws.stats + (at + i * step) * 2);
-      const float* from = ws.out + (at + i * step) * D + 4 * lane;
-      const float2 x0 = pick2(from), x1 = pick2(from + 2);
-      const float x[4] = {x0.x, x0.y, x1.x, x1.y};
-      const float w = __builtin_amdgcn_exp2f(st.x - mb);
-      l = __builtin_fmaf(w, st.y, l);
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * share;
+        if (i < u.count) {
+          const int64_t slot = u.slot(i);
+          const float* from = ws.out + slot * (SIZE * D) + off;
+          st[k] = pick2(ws.stats + (slot * SIZE + row) * 2);
+          x0[k] = pick2(from);
+          x1[k] = pick2(from + 2);
+        }
+      }
 #pragma unroll
-      for (int y = 0; y < 4; ++y) o[y] = __builtin_fmaf(w, x[y], o[y]);
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * share < u.count) j.add(st[k].x, st[k].y, {x0[k].x, x0[k].y, x1[k].x, x1[k].y});
     }
     if (share > 1) {    // one pass only
-      float* to = lds + (team * kLanes + lane) * 8;
-      *reinterpret_cast<v4f*>(to) = o;
-      to[4] = l;
+      float* to = lds + threadIdx.x * 8;
+      *reinterpret_cast<v4f*>(to) = v4f{j.o[0], j.o[1], j.o[2], j.o[3]};
+      to[4] = j.m;
+      to[5] = j.l;
       __syncthreads();
       if (part == 0)
         for (int k = 1; k < share; ++k) {
-          const float* from = to + k * kLanes * 8;
-          const v4f x = *reinterpret_cast<const v4f*>(from);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) o[y] += x[y];
-          l += from[4];
+          const float* from = to + k * items * 8;
+          j.add(from[4], from[5], {from[0], from[1], from[2], from[3]});
         }
     }
     if (!on || part != 0) continue;
-    const int row = r.row0 + local, tok = row / a.group;
-    const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + u.head * a.group + (row - tok * a.group);
+    const int tok = (r.row0 + row) / a.group;
+    const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + u.head * a.group + (r.row0 + row - tok * a.group);
     const bool none = r.pos0 + tok < 0;
-    const float inv = none ? 0.0f : 1.0f / l;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D + 4 * lane) =
-        make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv));
-    if (a.lse && lane == 0) a.lse[out_row] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    const float inv = none ? 0.0f : 1.0f / j.l;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D + 4 * quad) =
+        make_uint2(pack2<DT>(j.o[0] * inv, j.o[1] * inv), pack2<DT>(j.o[2] * inv, j.o[3] * inv));
+    if (a.lse && quad == 0) a.lse[out_row] = none ? -INFINITY : (j.m + __builtin_amdgcn_logf(j.l)) * kLn2;
   }
 }
 

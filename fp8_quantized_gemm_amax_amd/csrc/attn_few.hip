@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_device.hpp"
@@ -32,31 +33,9 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * kTile];
   __shared__ __attribute__((aligned(16))) float scales[kCodes ? 4 : 1][2][64];
   __shared__ float stats[2][4][32];
+  __shared__ int ends[kMaxSplitBatch + 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  Unit unit;
-  if (split) {
-    if (!find_unit<kRows>(a, blockIdx.x, reinterpret_cast<int*>(lds), unit)) return;
-  } else {
-    unit.head = blockIdx.x % a.hk;
-    if (!find_rows(a, blockIdx.x / a.hk, kRows, true, unit.r)) return;
-    tile_keys(a, unit.r, kRows, unit.j0, unit.j1);
-    unit.slot = 0;
-    unit.count = 1;
-    unit.piece = 0;
-  }
-  const Rows& r = unit.r;
-  const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
-  const int last_row = min(r.row0 + 31, r.rows - 1);
-  const int first_pos = r.pos0 + r.row0 / a.group, last_pos = r.pos0 + last_row / a.group;
-  const int row = min(r.row0 + col, last_row), tok = row / a.group, pos = r.pos0 + tok;
-  const int low = a.window > 0 ? pos - a.window + 1 : 0;
-  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (r.begin + tok) * a.qts + (h * a.group + row - tok * a.group) * a.qhs;
-  v8s q[kSteps];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s)   // codes are read 16 channels at a time: their order over two steps
-    q[s] = *reinterpret_cast<const v8s*>(qp + (kCodes ? 32 * (s / 2) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half));
-
   char* const kt = lds + wave * 2 * kTile;
   char* const vt = kt + kTile;
   const uint32_t kbase = lds_addr(kt), vbase = kbase + kTile;
@@ -75,6 +54,19 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
     const int i = kRowBytes == 128 ? 8 * g + (lane >> 3) : lane >> 2;
     off[g] = i * (kCodes ? D : 2 * D) + chunk_of(lane & (kRowBytes / 16 - 1), i) * 16;
   }
+  auto run = [&](const Unit& unit) {
+  const Rows& r = unit.r;
+  const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
+  const int last_row = min(r.row0 + 31, r.rows - 1);
+  const int first_pos = r.pos0 + r.row0 / a.group, last_pos = r.pos0 + last_row / a.group;
+  const int row = min(r.row0 + col, last_row), tok = row / a.group, pos = r.pos0 + tok;
+  const int low = a.window > 0 ? pos - a.window + 1 : 0;
+  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (r.begin + tok) * a.qts + (h * a.group + row - tok * a.group) * a.qhs;
+  v8s q[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)   // codes are read 16 channels at a time: their order over two steps
+    q[s] = *reinterpret_cast<const v8s*>(qp + (kCodes ? 32 * (s / 2) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half));
+
   auto page_of = [&](int at) -> int {
     return at < j1 ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
   };
@@ -315,10 +307,9 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   if (unit.count > 1) {
     if (mine) {
       const Workspace ws = workspace(a, kRows);
-      const int64_t at = (unit.slot + static_cast<int64_t>(unit.piece) * a.hk) * kRows + col;
-      if (wave == 0 && half == 0) leave2(ws.stats + at * 2, m, l);
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) leave2(ws.out + at * D + 32 * wave + 8 * (i / 4) + 4 * half + i % 4, o[0][i], o[0][i + 1]);
+      const int64_t slot = unit.slot(unit.piece);
+      if (wave == 0 && half == 0) leave2(ws.stats + (slot * kRows + col) * 2, m, l);
+      leave_block(ws.out + slot * (kRows * D) + wave * 1024, o[0]);
     }
     join_partials<DT, D, kRows>(a, unit, reinterpret_cast<int*>(stats), reinterpret_cast<float*>(lds));
     return;
@@ -332,14 +323,62 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   for (int g = 0; g < 4; ++g)
     *reinterpret_cast<uint2*>(out + 8 * g) = make_uint2(pack2<DT>(o[0][4 * g] * inv, o[0][4 * g + 1] * inv),
                                                         pack2<DT>(o[0][4 * g + 2] * inv, o[0][4 * g + 3] * inv));
+  };   // run
+
+  // The work of the batch as one line of steps, head by head, request by request, cut into one equal
+  // stretch for each workgroup: a stretch may end one tile, hold others whole and begin the next.
+  // Without cuts a workgroup takes a whole tile.
+  constexpr int kStep = 4 * kTileKeys;
+  Sums sums{ends, ends + kMaxSplitBatch, 0, 0};
+  if (split) sums.make<kRows, true>(a, kStep, [](const Shape& s) { return s.tiles * s.steps; });
+  const int64_t total = split ? static_cast<int64_t>(sums.total) * a.hk : gridDim.x;
+  const int64_t each = split ? max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(max(1, kMinKeys / kStep))) : 1;
+  const int64_t to = min(total, (blockIdx.x + 1) * each);
+  for (int64_t from = blockIdx.x * each; from < to;) {
+    Unit unit;
+    int n = 1;
+    if (split) {
+      unit.head = static_cast<int>(from / sums.total);
+      int end;
+      const int x = static_cast<int>(from - static_cast<int64_t>(unit.head) * sums.total);
+      const int i = sums.find(a.batch, x, end);
+      const Shape s = shape_of<kRows, true>(a, i, kStep);
+      const int tiles = __builtin_amdgcn_readfirstlane(s.tiles), steps = __builtin_amdgcn_readfirstlane(s.steps);
+      const int low = __builtin_amdgcn_readfirstlane(s.low);
+      const int local = x - (end - tiles * steps), tile = local / steps, step = local - tile * steps;
+      n = static_cast<int>(min(to - from, static_cast<int64_t>(steps - step)));
+      set_rows<kRows, true>(a, i, tile, unit.r);
+      tile_keys(a, unit.r, kRows, unit.j0, unit.j1);
+      unit.j0 = max(unit.j0, low + step * kStep);
+      unit.j1 = min(unit.j1, low + (step + n) * kStep);
+      // the tile's pieces: a workgroup has at most two partial results, of its first tile and its last
+      const int64_t begin = from - step;
+      const int first = static_cast<int>(begin / each), last = static_cast<int>((begin + steps - 1) / each);
+      unit.piece = static_cast<int>(blockIdx.x) - first;
+      unit.count = last - first + 1;
+      unit.slot0 = 2 * first + (begin == first * each ? 0 : 1);
+      unit.slot1 = 2 * (first + 1);
+      unit.slot_step = 2;
+    } else {
+      unit.head = blockIdx.x % a.hk;
+      if (!find_rows(a, blockIdx.x / a.hk, kRows, true, unit.r)) return;
+      tile_keys(a, unit.r, kRows, unit.j0, unit.j1);
+      unit.piece = 0;
+      unit.count = 1;
+    }
+    run(unit);
+    from += n;
+    if (from < to) __syncthreads();   // before the next tile takes the LDS over
+  }
 }
 
 template <int DT, int D, int SRC>
 void launch(const AttnArgs& a, hipStream_t s) {
   const int64_t tiles = tile_bound(a.tokens, a.group, a.batch, kRows);
-  const bool split = may_split(a.batch, a.hk, static_cast<int64_t>(a.width) << a.page_shift);
-  const int64_t units = (tiles + (split ? extra_units(a.hk) : 0)) * a.hk;
-  attn_few_kernel<DT, D, SRC><<<static_cast<unsigned>(units), 256, 0, s>>>(a, split);
+  const int64_t capacity = static_cast<int64_t>(a.width) << a.page_shift;
+  const bool split = may_split(a.tokens, a.group, a.batch, a.hk, capacity);
+  const int64_t pieces = tiles * a.hk * ((capacity + kMinKeys - 1) / kMinKeys);   // no more than these have work
+  attn_few_kernel<DT, D, SRC><<<static_cast<unsigned>(split ? std::min<int64_t>(kFewGroups, pieces) : tiles * a.hk), 256, 0, s>>>(a, split);
 }
 
 template <int SRC>

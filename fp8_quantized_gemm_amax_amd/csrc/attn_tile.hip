@@ -13,16 +13,17 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
+constexpr float kSlack = 8.0f;
 
 // The workgroup's unit: cut from the batch's work (find_unit) or a whole tile of rows.
 template <int SIZE, bool PAGED>
 __device__ __forceinline__ bool unit_of(const AttnArgs& a, bool split, char* lds, Unit& u) {
-  if (PAGED && split) return find_unit<SIZE>(a, blockIdx.x, reinterpret_cast<int*>(lds), u);
+  if (PAGED && split) return find_unit<SIZE, PAGED>(a, blockIdx.x, reinterpret_cast<int*>(lds), u);
   u.head = blockIdx.x % a.hk;
   // heavy tiles first: a prompt's last rows see the most keys
   if (!find_rows(a, gridDim.x / a.hk - 1 - blockIdx.x / a.hk, SIZE, PAGED, u.r)) return false;
   tile_keys(a, u.r, SIZE, u.j0, u.j1);
-  u.slot = u.piece = 0;
+  u.piece = 0;
   u.count = 1;
   return true;
 }
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 #pragma unroll
       for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
       top = max_halves(top) * c;
-      if (__any(top > m)) {
+      if (__any(top > m + kSlack)) {
         const float m1 = fmaxf(m, top);
         const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
         m = m1;
@@ -297,20 +298,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
   }
   const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + h * a.group + (row - tok * a.group);
   const bool store = r.row0 + 32 * wave + col < r.rows;
-  if constexpr (kPaged) {
-    if (unit.count > 1) {      // a partial result: maximum, sum and output as they are
-      if (store) {
-        const Workspace ws = workspace(a, kRows);
-        const int64_t at = (unit.slot + static_cast<int64_t>(unit.piece) * a.hk) * kRows + 32 * wave + col;
-        if (half == 0) leave2(ws.stats + at * 2, m, l);
+  if (kPaged && unit.count > 1) {      // a partial result: maximum, sum and output as they are
+    if (store) {
+      const Workspace ws = workspace(a, kRows);
+      const int64_t slot = unit.slot(unit.piece);
+      if (half == 0) leave2(ws.stats + (slot * kRows + 32 * wave + col) * 2, m, l);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int x = 0; x < 16; x += 2) leave2(ws.out + at * D + 32 * i + 8 * (x / 4) + 4 * half + x % 4, o[i][x], o[i][x + 1]);
-      }
-      join_partials<DT, D, kRows>(a, unit, reinterpret_cast<int*>(lds), reinterpret_cast<float*>(lds + 1024));
-      return;
+      for (int i = 0; i < D / 32; ++i) leave_block(ws.out + slot * (kRows * D) + (wave * (D / 32) + i) * 1024, o[i]);
     }
+    join_partials<DT, D, kRows>(a, unit, reinterpret_cast<int*>(lds), reinterpret_cast<float*>(lds + 1024));
+    return;
   }
   if (r.row0 + 32 * wave >= r.rows) return;
   const float inv = pos < 0 ? 0.0f : 1.0f / l;
@@ -333,7 +330,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 template <int DT, int D, int SRC>
 void launch(const AttnArgs& a, hipStream_t s) {
   const int64_t tiles = tile_bound(a.tokens, a.group, a.batch, kRows);
-  const bool split = SRC != SRC_PACKED && may_split(a.batch, a.hk, static_cast<int64_t>(a.width) << a.page_shift);
+  const bool split = SRC != SRC_PACKED && may_split(a.tokens, a.group, a.batch, a.hk, static_cast<int64_t>(a.width) << a.page_shift);
   const int64_t units = (tiles + (split ? extra_units(a.hk) : 0)) * a.hk;
   attn_tile_kernel<DT, D, SRC><<<static_cast<unsigned>(units), 64 * kWaves, 0, s>>>(a, split);
 }

@@ -308,6 +308,12 @@ def _workspace(q, stream, need):
     return have
 
 
+def _check_workspace(q, workspace):
+    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 vector")
+    _on(q, workspace=workspace)
+
+
 def fp8_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scales=None, v_scales=None,
                    softmax_scale=None, window=0, max_new=0, out=None, return_lse=False, workspace=None):
     """Causal attention of each request's new tokens over its pages, the new ones among them.
@@ -340,9 +346,7 @@ def fp8_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, k_scal
     if workspace is None:
         workspace = _workspace(q, stream, fns["fp8_attn_paged_workspace"](tokens, batch, hq, hk, dim, width, page, max_new))
     else:
-        if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
-            raise TypeError("workspace must be a contiguous uint8 vector")
-        _on(q, workspace=workspace)
+        _check_workspace(q, workspace)
     code = fns["fp8_attn_paged"](
         q_at, dt, tokens, cu_tokens.data_ptr(), batch, hq, hk, dim, qts, qhs, fmt, k_cache.data_ptr(),
         v_cache.data_ptr(), ks, vs, pages, page, block_table.data_ptr(), width, seq_lens.data_ptr(),

@@ -108,10 +108,10 @@ fp8_status_t fp8_attn_prompt(const void* q, const void* k, const void* v, fp8_dt
  *   max_new  : the largest number of new tokens of a request, 0 if unknown; it chooses the
  *              kernel and has no effect on what is computed.
  *   workspace : workspace_bytes of device memory, 16-byte aligned, of at least
- *              fp8_attn_paged_workspace() bytes for the same sizes.  Its first
+ *              fp8_attn_paged_workspace() bytes for the same sizes (may be 0).  Its first
  *              FP8_ATTN_COUNTER_BYTES must be zero before the first call; every call leaves it fit
- *              for the next one, of the same or of other sizes.
- *              Calls that may run at the same time need different ones.
+ *              for the next one, of the same or of other sizes.  Calls that may run at the same time
+ *              need different ones.
  */
 #define FP8_ATTN_COUNTER_BYTES 16384
 

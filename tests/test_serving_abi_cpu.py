@@ -90,6 +90,11 @@ def test_paged_refusals(change, status):
     assert call("fp8_attn_paged", PAGED, **change) == status
 
 
+def test_prompt_tokens_may_not_overlap():
+    assert call("fp8_attn_prompt", PROMPT, kts=120) == SHAPE
+    assert call("fp8_attn_prompt", PROMPT, vts=0) == SHAPE
+
+
 def test_workspace_sizes():
     w = fns()["fp8_attn_paged_workspace"]
     assert w(4, 2, 8, 2, 128, 4, 16, 0) >= 0
@@ -97,6 +102,7 @@ def test_workspace_sizes():
                 (4, 2, 8, 2, 128, 4, 10, 0), (4, 2, 8, 2, 128, 4, 16, -1)]:
         assert w(*bad) == 0
     need = w(64, 64, 32, 8, 128, 2048, 16, 1)
+    assert need > 0
     if need:
         assert call("fp8_attn_paged", PAGED, tokens=64, batch=64, hq=32, hk=8, width=2048, max_new=1, ws_bytes=need - 1) == SHAPE
         assert call("fp8_attn_paged", PAGED, tokens=64, batch=64, hq=32, hk=8, width=2048, max_new=1, ws=None) == NULLP
