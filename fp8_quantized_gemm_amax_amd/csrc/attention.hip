@@ -1,4 +1,5 @@
-// attention.hip - the choice of kernel for attention over a paged cache, and its workspace.
+// attention.hip - attention over a paged cache: the choice of kernel, the workspace, and the join of the
+// partial results for many rows.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -14,7 +15,80 @@ bool few_rows(int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
   return (max_new > 0 ? max_new : (tokens + batch - 1) / (batch > 0 ? batch : 1)) * group <= 32;
 }
 
+// Joins the partial results of the launch for many rows, of 128 rows each: a thread takes one row and
+// every eighth (fourth) group of four channels of it, and goes over the row's pieces once:
+//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// Workgroup (x, y): the tile whose first partial result is x, quarter y of its channels.
+constexpr int kQuarters = 4;
+template <int DT, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  constexpr int kSize = 128, kEach = D / 4 * kSize / 256 / kQuarters;
+  const Workspace ws = workspace(a, kSize);
+  const int slot = blockIdx.x;
+  if (slot >= *ws.used) return;
+  const Partial p = ws.partials[slot];
+  if (p.count <= 1) return;
+  Rows r;
+  set_rows<kSize, true>(a, __builtin_amdgcn_readfirstlane(p.request), __builtin_amdgcn_readfirstlane(p.tile), r);
+  const int row = threadIdx.x & 127, quad0 = blockIdx.y * (D / 4 / kQuarters) + (threadIdx.x >> 7);
+  if (r.row0 + row >= r.rows) return;
+  const int64_t stride = static_cast<int64_t>(a.hk) * kSize;
+  const float* stats = ws.stats + (static_cast<int64_t>(slot) * kSize + row) * 2;
+  const float* out = ws.out + static_cast<int64_t>(slot) * kSize * D;
+  float m = -INFINITY, l = 0.0f, o[kEach][4] = {};
+  for (int i0 = 0; i0 < p.count; i0 += 4) {
+    float2 st[4];
+    v4f x[4][kEach];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = min(i0 + k, p.count - 1);
+      st[k] = *reinterpret_cast<const float2*>(stats + i * stride * 2);
+      if (i0 + k >= p.count) st[k] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) x[k][e] = *reinterpret_cast<const v4f*>(out + i * stride * D + partial_at<D>(row, quad0 + 2 * e));
+    }
+    const float top = fmaxf(fmaxf(fmaxf(m, st[0].x), fmaxf(st[1].x, st[2].x)), st[3].x);
+    const float base = top == -INFINITY ? 0.0f : top, keep = __builtin_amdgcn_exp2f(m - base);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[e][y] *= keep;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i0 + k >= p.count) break;
+      const float f = __builtin_amdgcn_exp2f(st[k].x - base);
+      l = __builtin_fmaf(f, st[k].y, l);
+#pragma unroll
+      for (int e = 0; e < kEach; ++e)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[e][y] = __builtin_fmaf(f, x[k][e][y], o[e][y]);
+    }
+  }
+  const int tok = (r.row0 + row) / a.group;
+  const bool none = r.pos0 + tok < 0;
+  const float inv = none ? 0.0f : 1.0f / l;
+  const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + p.head * a.group + (r.row0 + row - tok * a.group);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D + 4 * (quad0 + 2 * e)) =
+        make_uint2(pack2<DT>(o[e][0] * inv, o[e][1] * inv), pack2<DT>(o[e][2] * inv, o[e][3] * inv));
+  if (a.lse && quad0 == 0) a.lse[out_row] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <int DT, int D>
+void join(const AttnArgs& a, hipStream_t s) {
+  attn_join_kernel<DT, D><<<dim3(static_cast<unsigned>(2 * extra_units(a.hk) * a.hk), kQuarters), 256, 0, s>>>(a);
+}
+
 }  // namespace
+
+void launch_attn_join(int dt, int head_dim, const AttnArgs& a, hipStream_t s) {
+  if (dt == DT_BF16) head_dim == 128 ? join<DT_BF16, 128>(a, s) : join<DT_BF16, 64>(a, s);
+  else head_dim == 128 ? join<DT_F16, 128>(a, s) : join<DT_F16, 64>(a, s);
+}
+
 }  // namespace attn
 
 void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnArgs& a, hipStream_t s) {

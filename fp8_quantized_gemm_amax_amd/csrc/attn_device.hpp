@@ -188,7 +188,7 @@ __host__ __device__ constexpr int64_t tile_bound(int64_t tokens, int64_t group, 
 // Whether a batch is cut at all: `capacity` is the most keys a request can have.
 __host__ __device__ constexpr bool may_split(int64_t tokens, int64_t group, int64_t batch, int64_t hk, int64_t capacity) {
   return batch <= kMaxSplitBatch && hk <= kMaxSplitHeads && capacity > kMinKeys &&
-         tile_bound(tokens, group, batch, 32) * (capacity / kKeys + 1) < (int64_t{1} << 30);
+         tile_bound(tokens, group, batch, 32) * (capacity / kKeys + 1) < (int64_t{1} << 30) / hk;   // steps are counted in int
 }
 
 // Tiles of a request, and steps of `step` keys that its rows see between them.
@@ -294,12 +294,86 @@ __device__ __forceinline__ void set_rows(const AttnArgs& a, int i, int tile, Row
   r.pos0 = r.len - r.tokens;
 }
 
+// Packed prompts of up to 64 requests: tile `rank` of them all in the order of their index in their
+// request, the last first, so that the tiles that see the most keys start first whatever request
+// they are of (hardware starts workgroups in order).  Up to kSlots workgroups are all on the card at
+// once, two to a CU: there the second of a CU is the lightest left, not the next.
+constexpr int kSlots = 512;
+template <int SIZE>
+__device__ __forceinline__ bool find_ranked(const AttnArgs& a, Unit& u) {
+  const int lane = threadIdx.x & 63;
+  u.head = blockIdx.x % a.hk;
+  int rank = blockIdx.x / a.hk, tiles = 0, most = 0;
+  if (lane < a.batch) tiles = shape_of<SIZE, false>(a, lane, kKeys).tiles;
+  auto sum = [&](int x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    return __builtin_amdgcn_readfirstlane(x);
+  };
+  const int total = sum(tiles);
+  if (rank >= total) return false;
+  const int first = kSlots / 2 / a.hk;
+  if (total * a.hk <= kSlots && rank >= first) rank = total - 1 - (rank - first);
+  // the largest index k that more than `rank` tiles reach: tiles of index k or above
+  int above = 0;
+  for (int bit = static_cast<int>(0x80000000u >> __builtin_clz(total)); bit; bit >>= 1) {
+    const int n = sum(max(tiles - (most + bit), 0));
+    if (n > rank) most += bit;
+    else above = n;
+  }
+  const bool on = tiles > most;
+  const uint64_t mask = __ballot(on);
+  const int order = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+  const int i = __builtin_ctzll(__ballot(on && order == rank - above) | (uint64_t{1} << 63));
+  set_rows<SIZE, false>(a, i, most, u.r);
+  tile_keys(a, u.r, SIZE, u.j0, u.j1);
+  u.piece = 0;
+  u.count = 1;
+  return true;
+}
+
+// The workspace: a counter for every partial result (zero between calls), how many partial results
+// a launch for many rows has and of which tiles they are, then the partial results' maxima and sums
+// [slot][row][2] and their outputs, float32.  An output lies as the matrix unit leaves it, so that
+// whole lines are written: [slot][row / 32][channel / 32][channel % 32 / 8][channel % 8 / 4][row % 32]
+// [channel % 4].
+constexpr int64_t kCounterBytes = FP8_ATTN_COUNTER_BYTES, kHeadBytes = 16 + 16 * kMaxSlots;
+static_assert(kCounterBytes >= 4 * kMaxSlots, "a counter a slot");
+struct Partial {
+  int request, tile, head, count;   // count 0 in all places of a tile but its first
+};
+struct Workspace {
+  int *counters, *used;
+  Partial* partials;
+  float* stats;
+  float* out;
+};
+__device__ __forceinline__ Workspace workspace(const AttnArgs& a, int size) {
+  Workspace w;
+  w.counters = reinterpret_cast<int*>(a.ws);
+  w.used = reinterpret_cast<int*>(a.ws + kCounterBytes);
+  w.partials = reinterpret_cast<Partial*>(a.ws + kCounterBytes + 16);
+  w.stats = reinterpret_cast<float*>(a.ws + kCounterBytes + kHeadBytes);
+  w.out = w.stats + static_cast<int64_t>(kMaxSlots) * size * 2;
+  return w;
+}
+__host__ __device__ constexpr int64_t workspace_bytes(int64_t slots, int size, int head_dim) {
+  return kCounterBytes + kHeadBytes + int64_t{kMaxSlots} * size * 8 + slots * size * head_dim * 4;
+}
+// Where four channels 4 quad .. of a row lie in an output of D channels.
+template <int D>
+__device__ __forceinline__ int64_t partial_at(int row, int quad) {
+  return ((row >> 5) * (D / 32) + (quad >> 3)) * 1024 + ((quad >> 1) & 3) * 256 + (quad & 1) * 128 + (row & 31) * 4;
+}
+
 // The cut for many rows, where the work of tiles differs (a prompt's last rows see the most keys)
 // and the hardware's own order of workgroups balances it: pieces of
-//   max(kMinKeys, work / kUnits)
+//   max(kMinTileKeys, work / kUnits)
 // keys, numbered request by request, the tiles that see the most first.  A full batch of equal
-// lengths stays uncut.
-constexpr int kUnits = 1024;
+// lengths stays uncut.  A second launch joins the partial results: 128 rows of them are too much for
+// one workgroup at the end of the first (measured: 2 tiles a head over 100000 keys 406 us that way).
+constexpr int kUnits = 512;
+constexpr int kMinTileKeys = 512;
 // Units per key head are at most the tiles and this many more, and partial results at most twice it.
 __host__ __device__ constexpr int64_t extra_units(int64_t hk) { return (kUnits + hk - 1) / hk; }
 static_assert(2 * (kUnits + kMaxSplitHeads) <= kMaxSlots, "partial results of the cut for many rows");
@@ -312,10 +386,12 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
   const int unit = block / a.hk;
   Sums sums{lds, lds + kMaxSplitBatch, 0, 0};
   sums.make<SIZE, PAGED>(a, kKeys, [](const Shape& s) { return s.tiles * s.steps; });
-  const int64_t want = (static_cast<int64_t>(sums.total) * a.hk + kUnits - 1) / kUnits;
-  const int most = static_cast<int>(max(want, int64_t{kMinKeys / kKeys}));   // steps a piece
+  const int most = max((sums.total * a.hk + kUnits - 1) / kUnits, kMinTileKeys / kKeys);   // steps a piece
   sums.make<SIZE, PAGED>(a, kKeys, [&](const Shape& s) { return s.tiles * ((s.steps + most - 1) / most); });
-  if (unit >= sums.total) return false;
+  if (unit >= sums.total) {
+    if (block == 0 && threadIdx.x == 0) *workspace(a, SIZE).used = 0;
+    return false;
+  }
   int end;
   const int i = sums.find(a.batch, unit, end);
   const Shape s = shape_of<SIZE, PAGED>(a, i, kKeys);
@@ -325,7 +401,7 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
   const int tile = tiles - 1 - local / pieces;
   u.piece = local % pieces;
   u.slot0 = 0;
-  if (pieces > 1) {
+  if (pieces > 1 || block == 0) {
     sums.make<SIZE, PAGED>(a, kKeys, [&](const Shape& x) {
       const int n = (x.steps + most - 1) / most;
       return n > 1 ? x.tiles * n : 0;
@@ -333,7 +409,8 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
     int slots;
     if (a.batch <= 64) slots = __builtin_amdgcn_readlane(sums.mine, i);
     else slots = __builtin_amdgcn_readfirstlane(sums.ends[i]);
-    u.slot0 = (slots - tiles * pieces + tile * pieces) * a.hk + u.head;
+    if (pieces > 1) u.slot0 = (slots - tiles * pieces + tile * pieces) * a.hk + u.head;
+    if (block == 0 && threadIdx.x == 0) *workspace(a, SIZE).used = sums.total * a.hk;
   }
   if (a.batch > 64) __syncthreads();
   set_rows<SIZE, PAGED>(a, i, tile, u.r);
@@ -342,11 +419,13 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
   const int own = (j1 - j0 + kKeys - 1) / kKeys;
   const int per = max(1, (own + pieces - 1) / pieces);
   u.count = max(1, (own + per - 1) / per);
+  u.slot1 = u.slot0 + a.hk;
+  u.slot_step = a.hk;
+  if (pieces > 1 && threadIdx.x == 0)
+    workspace(a, SIZE).partials[u.slot(u.piece)] = {i, tile, u.head, u.piece == 0 && u.count > 1 ? u.count : 0};
   if (u.piece >= u.count) return false;
   u.j0 = j0 + u.piece * per * kKeys;
   u.j1 = min(j1, u.j0 + per * kKeys);
-  u.slot1 = u.slot0 + a.hk;
-  u.slot_step = a.hk;
   return true;
 }
 
@@ -354,28 +433,6 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
 // steps in one line, an equal stretch for each of kFewGroups workgroups (two to a CU).
 constexpr int kFewGroups = 512;
 static_assert(2 * kFewGroups <= kMaxSlots, "partial results of the cut for few rows");
-
-// The workspace: a counter for every partial result, then the partial results' maxima and sums
-// [slot][row][2], then their outputs, float32.  The counters are zero between calls.  An output lies
-// as the matrix unit leaves it, so that whole lines are written: [slot][row / 32][channel / 32]
-// [channel % 32 / 8][channel % 8 / 4][row % 32][channel % 4].
-constexpr int64_t kCounterBytes = FP8_ATTN_COUNTER_BYTES;
-static_assert(kCounterBytes >= 4 * kMaxSlots, "a counter a slot");
-struct Workspace {
-  int* counters;
-  float* stats;
-  float* out;
-};
-__device__ __forceinline__ Workspace workspace(const AttnArgs& a, int size) {
-  Workspace w;
-  w.counters = reinterpret_cast<int*>(a.ws);
-  w.stats = reinterpret_cast<float*>(a.ws + kCounterBytes);
-  w.out = w.stats + static_cast<int64_t>(kMaxSlots) * size * 2;
-  return w;
-}
-__host__ __device__ constexpr int64_t workspace_bytes(int64_t slots, int size, int head_dim) {
-  return kCounterBytes + int64_t{kMaxSlots} * size * 8 + slots * size * head_dim * 4;
-}
 
 // Partial results pass between workgroups of one launch, whose XCDs' L2 caches do not see each
 // other: they are written and read with agent-scope accesses, which go through to memory, and a
@@ -399,10 +456,10 @@ __device__ __forceinline__ void leave_block(float* to, const v16f& o) {
   }
 }
 
-// A sum of weights and outputs relative to the largest exponent met.
+// A sum of weights and four outputs relative to the largest exponent met.
 struct Joined {
   float m, l, o[4];
-  __device__ __forceinline__ void add(float m2, float l2, const float (&x)[4]) {
+  __device__ __forceinline__ void add(float m2, float l2, const float* x) {
     const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.0f : top;
     const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(m2 - base);
     l = __builtin_fmaf(g, l2, l * f);
@@ -413,11 +470,17 @@ struct Joined {
 };
 
 // After a workgroup's partial result is stored: the workgroup that finds itself the last of its
-// tile joins them all, in their order, so the result does not depend on who that is.  A thread takes
-// four channels of a row; with few rows, several share the row's partial results.  `flag` and `lds`
-// (8 KB) are LDS that nothing else uses any more.
+// tile joins them all, in an order that does not depend on who that is:
+//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// A thread takes four channels of a row, and has eight pieces' reads in flight (they go to memory, at
+// more than a microsecond each); with few rows, several threads share a row's pieces.  `lds` is
+// kJoinBytes of LDS that nothing else uses any more.
+constexpr int kJoinBytes = 16 + 256 * 8 * 4;
 template <int DT, int D, int SIZE>
-__device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, int* flag, float* lds) {
+__device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, char* lds) {
+  constexpr int kPieces = 8;
+  int* const flag = reinterpret_cast<int*>(lds);
+  float* const shared = reinterpret_cast<float*>(lds + 16) + threadIdx.x * 8;
   const Workspace ws = workspace(a, SIZE);
   const Rows& r = u.r;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every thread's stores before the count
@@ -433,45 +496,43 @@ __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, 
   const int rows = min(SIZE, r.rows - r.row0);
   int bits = 0;                       // rows, rounded up to a power of two
   while ((1 << bits) < rows) ++bits;
-  const int items = (D / 4) << bits;
+  const int items = (D / 4) << bits;  // item n: row n % 2^bits, channels 4 (n >> bits) .. + 3
   const int share = items < 256 ? 256 / items : 1;
-  for (int n = threadIdx.x; n < max(items, 256); n += 256) {
-    const int part = n / items, at = n - part * items;
-    const int local = at & ((1 << bits) - 1), quad = at >> bits;   // quad: channels 4 quad .. 4 quad + 3
-    const bool on = local < rows;
-    const int row = on ? local : 0;
-    const int64_t off = ((row >> 5) * (D / 32) + (quad >> 3)) * 1024 + ((quad >> 1) & 3) * 256 + (quad & 1) * 128 + (row & 31) * 4;
+  const int part = share > 1 ? threadIdx.x / items : 0;
+#pragma unroll 1
+  for (int n = threadIdx.x - part * items; n < items; n += 256) {
+    const bool on = (n & ((1 << bits) - 1)) < rows;
+    const int row = on ? n & ((1 << bits) - 1) : 0, quad = n >> bits;
+    const float* stats = ws.stats + row * 2;
+    const float* out = ws.out + partial_at<D>(row, quad);
     Joined j{-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}};
-    for (int i0 = part; i0 < u.count; i0 += 8 * share) {
-      float2 st[8], x0[8], x1[8];
+#pragma unroll 1
+    for (int i0 = part; i0 < u.count; i0 += kPieces * share) {
+      float2 st[kPieces], x[kPieces][2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + k * share;
-        if (i < u.count) {
-          const int64_t slot = u.slot(i);
-          const float* from = ws.out + slot * (SIZE * D) + off;
-          st[k] = pick2(ws.stats + (slot * SIZE + row) * 2);
-          x0[k] = pick2(from);
-          x1[k] = pick2(from + 2);
-        }
+      for (int k = 0; k < kPieces; ++k) {
+        const int64_t slot = u.slot(min(i0 + k * share, u.count - 1));
+        st[k] = pick2(stats + slot * (SIZE * 2));
+        x[k][0] = pick2(out + slot * (SIZE * D));
+        x[k][1] = pick2(out + slot * (SIZE * D) + 2);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i0 + k * share < u.count) j.add(st[k].x, st[k].y, {x0[k].x, x0[k].y, x1[k].x, x1[k].y});
+      for (int k = 0; k < kPieces; ++k) {
+        const float y[4] = {x[k][0].x, x[k][0].y, x[k][1].x, x[k][1].y};
+        if (i0 + k * share < u.count) j.add(st[k].x, st[k].y, y);
+      }
     }
     if (share > 1) {    // one pass only
-      float* to = lds + threadIdx.x * 8;
-      *reinterpret_cast<v4f*>(to) = v4f{j.o[0], j.o[1], j.o[2], j.o[3]};
-      to[4] = j.m;
-      to[5] = j.l;
+      *reinterpret_cast<v4f*>(shared) = v4f{j.o[0], j.o[1], j.o[2], j.o[3]};
+      *reinterpret_cast<float2*>(shared + 4) = make_float2(j.m, j.l);
       __syncthreads();
-      if (part == 0)
-        for (int k = 1; k < share; ++k) {
-          const float* from = to + k * items * 8;
-          j.add(from[4], from[5], {from[0], from[1], from[2], from[3]});
-        }
+      if (part != 0) continue;
+      for (int k = 1; k < share; ++k) {
+        const float* from = shared + k * items * 8;
+        j.add(from[4], from[5], from);
+      }
     }
-    if (!on || part != 0) continue;
+    if (!on) continue;
     const int tok = (r.row0 + row) / a.group;
     const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + u.head * a.group + (r.row0 + row - tok * a.group);
     const bool none = r.pos0 + tok < 0;
@@ -535,6 +596,7 @@ __device__ __forceinline__ v16f mfma_odd(const v8s& v, const v8s& p, v16f o) {
 // Host side: the paged kernels for many rows and for few.
 void launch_attn_tile(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
 void launch_attn_few(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
+void launch_attn_join(int dt, int head_dim, const AttnArgs& a, hipStream_t s);   // after launch_attn_tile's
 
 }  // namespace attn
 }  // namespace fp8amax

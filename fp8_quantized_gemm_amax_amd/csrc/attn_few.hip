@@ -30,6 +30,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   constexpr int kPlanes = !kCodes && D == 128 ? 2 : 1;
   constexpr int kPlaneBytes = kTileKeys * kRowBytes, kTile = kPlanes * kPlaneBytes;
   constexpr int kDma = kTile / 1024;                         // DMA instructions of a tile
+  static_assert(kJoinBytes <= 8 * kTile, "the join's LDS");
   __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * kTile];
   __shared__ __attribute__((aligned(16))) float scales[kCodes ? 4 : 1][2][64];
   __shared__ float stats[2][4][32];
@@ -311,7 +312,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
       if (wave == 0 && half == 0) leave2(ws.stats + (slot * kRows + col) * 2, m, l);
       leave_block(ws.out + slot * (kRows * D) + wave * 1024, o[0]);
     }
-    join_partials<DT, D, kRows>(a, unit, reinterpret_cast<int*>(stats), reinterpret_cast<float*>(lds));
+    join_partials<DT, D, kRows>(a, unit, lds);
     return;
   }
   if (!mine) return;
@@ -331,29 +332,28 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   constexpr int kStep = 4 * kTileKeys;
   Sums sums{ends, ends + kMaxSplitBatch, 0, 0};
   if (split) sums.make<kRows, true>(a, kStep, [](const Shape& s) { return s.tiles * s.steps; });
-  const int64_t total = split ? static_cast<int64_t>(sums.total) * a.hk : gridDim.x;
-  const int64_t each = split ? max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(max(1, kMinKeys / kStep))) : 1;
-  const int64_t to = min(total, (blockIdx.x + 1) * each);
-  for (int64_t from = blockIdx.x * each; from < to;) {
+  const int total = split ? sums.total * a.hk : gridDim.x;
+  const int each = split ? max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), max(1, kMinKeys / kStep)) : 1;
+  const int to = min(total, static_cast<int>(blockIdx.x + 1) * each);
+  for (int from = static_cast<int>(blockIdx.x) * each; from < to;) {
     Unit unit;
     int n = 1;
     if (split) {
-      unit.head = static_cast<int>(from / sums.total);
+      unit.head = from / sums.total;
       int end;
-      const int x = static_cast<int>(from - static_cast<int64_t>(unit.head) * sums.total);
+      const int x = from - unit.head * sums.total;
       const int i = sums.find(a.batch, x, end);
       const Shape s = shape_of<kRows, true>(a, i, kStep);
       const int tiles = __builtin_amdgcn_readfirstlane(s.tiles), steps = __builtin_amdgcn_readfirstlane(s.steps);
       const int low = __builtin_amdgcn_readfirstlane(s.low);
       const int local = x - (end - tiles * steps), tile = local / steps, step = local - tile * steps;
-      n = static_cast<int>(min(to - from, static_cast<int64_t>(steps - step)));
+      n = min(to - from, steps - step);
       set_rows<kRows, true>(a, i, tile, unit.r);
       tile_keys(a, unit.r, kRows, unit.j0, unit.j1);
       unit.j0 = max(unit.j0, low + step * kStep);
       unit.j1 = min(unit.j1, low + (step + n) * kStep);
       // the tile's pieces: a workgroup has at most two partial results, of its first tile and its last
-      const int64_t begin = from - step;
-      const int first = static_cast<int>(begin / each), last = static_cast<int>((begin + steps - 1) / each);
+      const int begin = from - step, first = begin / each, last = (begin + steps - 1) / each;
       unit.piece = static_cast<int>(blockIdx.x) - first;
       unit.count = last - first + 1;
       unit.slot0 = 2 * first + (begin == first * each ? 0 : 1);

@@ -19,6 +19,7 @@ constexpr float kSlack = 8.0f;
 template <int SIZE, bool PAGED>
 __device__ __forceinline__ bool unit_of(const AttnArgs& a, bool split, char* lds, Unit& u) {
   if (PAGED && split) return find_unit<SIZE, PAGED>(a, blockIdx.x, reinterpret_cast<int*>(lds), u);
+  if (!PAGED && a.batch <= 64) return find_ranked<SIZE>(a, u);
   u.head = blockIdx.x % a.hk;
   // heavy tiles first: a prompt's last rows see the most keys
   if (!find_rows(a, gridDim.x / a.hk - 1 - blockIdx.x / a.hk, SIZE, PAGED, u.r)) return false;
@@ -302,11 +303,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     if (store) {
       const Workspace ws = workspace(a, kRows);
       const int64_t slot = unit.slot(unit.piece);
-      if (half == 0) leave2(ws.stats + (slot * kRows + 32 * wave + col) * 2, m, l);
+      if (half == 0) *reinterpret_cast<float2*>(ws.stats + (slot * kRows + 32 * wave + col) * 2) = make_float2(m, l);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) leave_block(ws.out + slot * (kRows * D) + (wave * (D / 32) + i) * 1024, o[i]);
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<v4f*>(ws.out + slot * (kRows * D) + ((wave * (D / 32) + i) * 4 + g) * 256 + lane * 4) =
+              v4f{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
     }
-    join_partials<DT, D, kRows>(a, unit, reinterpret_cast<int*>(lds), reinterpret_cast<float*>(lds + 1024));
     return;
   }
   if (r.row0 + 32 * wave >= r.rows) return;
@@ -333,6 +337,7 @@ void launch(const AttnArgs& a, hipStream_t s) {
   const bool split = SRC != SRC_PACKED && may_split(a.tokens, a.group, a.batch, a.hk, static_cast<int64_t>(a.width) << a.page_shift);
   const int64_t units = (tiles + (split ? extra_units(a.hk) : 0)) * a.hk;
   attn_tile_kernel<DT, D, SRC><<<static_cast<unsigned>(units), 64 * kWaves, 0, s>>>(a, split);
+  if (split) launch_attn_join(DT, D, a, s);
 }
 
 template <int SRC>
