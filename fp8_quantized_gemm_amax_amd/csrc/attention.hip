@@ -28,8 +28,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (slot >= *ws.used) return;
   const Partial p = ws.partials[slot];
   if (p.count <= 1) return;
-  Rows r;
-  set_rows<kSize, true>(a, __builtin_amdgcn_readfirstlane(p.request), __builtin_amdgcn_readfirstlane(p.tile), r);
+  const Rows r = rows_of(a, p.request, load_request<true>(a, p.request), p.tile, kSize);
   const int row = threadIdx.x & 127, quad0 = blockIdx.y * (D / 4 / kQuarters) + (threadIdx.x >> 7);
   if (r.row0 + row >= r.rows) return;
   const int64_t stride = static_cast<int64_t>(a.hk) * kSize;

@@ -191,20 +191,31 @@ __host__ __device__ constexpr bool may_split(int64_t tokens, int64_t group, int6
          tile_bound(tokens, group, batch, 32) * (capacity / kKeys + 1) < (int64_t{1} << 30) / hk;   // steps are counted in int
 }
 
-// Tiles of a request, and steps of `step` keys that its rows see between them.
+// A request's bounds as the kernels use them.
+struct Request {
+  int begin, tokens, len;   // first packed token, new tokens (not negative), keys
+  bool bad;                 // cu_tokens decreases here
+};
+template <bool PAGED>
+__device__ __forceinline__ Request load_request(const AttnArgs& a, int i) {
+  const int lo = a.cu[i], hi = a.cu[i + 1];
+  Request q;
+  q.begin = min(max(lo, 0), a.tokens);
+  q.tokens = max(min(max(hi, 0), a.tokens) - q.begin, 0);
+  q.len = PAGED ? min(max(a.lens[i], 0), a.width << a.page_shift) : q.tokens;
+  q.bad = hi < lo;
+  return q;
+}
+// Its tiles, and steps of `step` keys that its rows see between them.
 struct Shape {
   int tiles, steps, low;   // low: the first key
-  bool bad;                // cu_tokens decreases here
 };
-template <int SIZE, bool PAGED>
-__device__ __forceinline__ Shape shape_of(const AttnArgs& a, int i, int step) {
-  const int begin = min(max(a.cu[i], 0), a.tokens), n = min(max(a.cu[i + 1], 0), a.tokens) - begin;
-  const int len = PAGED ? min(max(a.lens[i], 0), a.width << a.page_shift) : max(n, 0);
+template <int SIZE>
+__device__ __forceinline__ Shape shape_of(const AttnArgs& a, const Request& q, int step) {
   Shape s;
-  s.bad = a.cu[i + 1] < a.cu[i];
-  s.tiles = n > 0 ? static_cast<int>((static_cast<int64_t>(n) * a.group + SIZE - 1) / SIZE) : 0;
-  s.low = a.window > 0 ? max(0, len - n - a.window + 1) & ~(kKeys - 1) : 0;
-  s.steps = max(1, (len - s.low + step - 1) / step);
+  s.tiles = static_cast<int>((static_cast<int64_t>(q.tokens) * a.group + SIZE - 1) / SIZE);
+  s.low = a.window > 0 ? max(0, q.len - q.tokens - a.window + 1) & ~(kKeys - 1) : 0;
+  s.steps = max(1, (q.len - s.low + step - 1) / step);
   return s;
 }
 
@@ -237,23 +248,36 @@ __device__ __forceinline__ int scan256(int x, int* part, int& total) {
 // Inclusive sums over the requests of a number each has: in the lanes of every wave for up to 64
 // requests (no barrier), else in LDS (`ends`, kMaxSplitBatch, and `part`, 4 integers).
 // A batch whose cu_tokens decreases somewhere has a total of 0: nothing is computed for it.
+template <bool PAGED>
 struct Sums {
   int *ends, *part;
   int mine, total;
-  template <int SIZE, bool PAGED, typename F>
-  __device__ __forceinline__ void make(const AttnArgs& a, int step, F number) {
+  Request lane_request;    // up to 64 requests: each lane's, loaded once
+  __device__ __forceinline__ Sums(const AttnArgs& a, int* lds) : ends(lds), part(lds + kMaxSplitBatch), mine(0), total(0), lane_request{0, 0, 0, false} {
+    const int lane = threadIdx.x & 63;
+    if (a.batch <= 64 && lane < a.batch) lane_request = load_request<PAGED>(a, lane);
+  }
+  // Request i (uniform).
+  __device__ __forceinline__ Request request(const AttnArgs& a, int i) const {
+    Request q = lane_request;
+    if (a.batch > 64) q = load_request<PAGED>(a, i);
+    const int from = a.batch > 64 ? 0 : i;
+    return {__builtin_amdgcn_readlane(q.begin, from), __builtin_amdgcn_readlane(q.tokens, from), __builtin_amdgcn_readlane(q.len, from), false};
+  }
+  template <typename F>
+  __device__ __forceinline__ void make(const AttnArgs& a, F number) {
     bool bad = false;
-    auto at = [&](int i) {
-      const Shape s = shape_of<SIZE, PAGED>(a, i, step);
-      bad |= s.bad;
-      return number(s);
-    };
     if (a.batch <= 64) {
       const int lane = threadIdx.x & 63;
-      mine = scan64(lane < a.batch ? at(lane) : 0);
-      total = __any(bad) ? 0 : __builtin_amdgcn_readlane(mine, 63);
+      mine = scan64(lane < a.batch ? number(lane_request) : 0);
+      total = __any(lane_request.bad) ? 0 : __builtin_amdgcn_readlane(mine, 63);
       return;
     }
+    auto at = [&](int i) {
+      const Request q = load_request<PAGED>(a, i);
+      bad |= q.bad;
+      return number(q);
+    };
     int before = 0;
     for (int i0 = 0; i0 < a.batch; i0 += 256) {
       const int i = i0 + threadIdx.x;
@@ -283,15 +307,9 @@ struct Sums {
   }
 };
 
-template <int SIZE, bool PAGED>
-__device__ __forceinline__ void set_rows(const AttnArgs& a, int i, int tile, Rows& r) {
-  r.request = i;
-  r.begin = clamp_cu(a, i);
-  r.tokens = clamp_cu(a, i + 1) - r.begin;
-  r.rows = r.tokens * a.group;
-  r.row0 = tile * SIZE;
-  r.len = PAGED ? min(max(scalar_int(a.lens + i), 0), a.width << a.page_shift) : r.tokens;
-  r.pos0 = r.len - r.tokens;
+// Tile `tile` of request i.
+__device__ __forceinline__ Rows rows_of(const AttnArgs& a, int i, const Request& q, int tile, int size) {
+  return {i, q.begin, q.tokens, q.tokens * a.group, tile * size, q.len, q.len - q.tokens};
 }
 
 // Packed prompts of up to 64 requests: tile `rank` of them all in the order of their index in their
@@ -304,7 +322,8 @@ __device__ __forceinline__ bool find_ranked(const AttnArgs& a, Unit& u) {
   const int lane = threadIdx.x & 63;
   u.head = blockIdx.x % a.hk;
   int rank = blockIdx.x / a.hk, tiles = 0, most = 0;
-  if (lane < a.batch) tiles = shape_of<SIZE, false>(a, lane, kKeys).tiles;
+  const Sums<false> requests(a, nullptr);
+  if (lane < a.batch) tiles = shape_of<SIZE>(a, requests.lane_request, kKeys).tiles;
   auto sum = [&](int x) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
@@ -325,7 +344,7 @@ __device__ __forceinline__ bool find_ranked(const AttnArgs& a, Unit& u) {
   const uint64_t mask = __ballot(on);
   const int order = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
   const int i = __builtin_ctzll(__ballot(on && order == rank - above) | (uint64_t{1} << 63));
-  set_rows<SIZE, false>(a, i, most, u.r);
+  u.r = rows_of(a, i, requests.request(a, i), most, SIZE);
   tile_keys(a, u.r, SIZE, u.j0, u.j1);
   u.piece = 0;
   u.count = 1;
@@ -384,25 +403,32 @@ template <int SIZE, bool PAGED>
 __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds, Unit& u) {
   u.head = block % a.hk;
   const int unit = block / a.hk;
-  Sums sums{lds, lds + kMaxSplitBatch, 0, 0};
-  sums.make<SIZE, PAGED>(a, kKeys, [](const Shape& s) { return s.tiles * s.steps; });
+  Sums<PAGED> sums(a, lds);
+  sums.make(a, [&](const Request& q) {
+    const Shape s = shape_of<SIZE>(a, q, kKeys);
+    return s.tiles * s.steps;
+  });
   const int most = max((sums.total * a.hk + kUnits - 1) / kUnits, kMinTileKeys / kKeys);   // steps a piece
-  sums.make<SIZE, PAGED>(a, kKeys, [&](const Shape& s) { return s.tiles * ((s.steps + most - 1) / most); });
+  sums.make(a, [&](const Request& q) {
+    const Shape s = shape_of<SIZE>(a, q, kKeys);
+    return s.tiles * ((s.steps + most - 1) / most);
+  });
   if (unit >= sums.total) {
     if (block == 0 && threadIdx.x == 0) *workspace(a, SIZE).used = 0;
     return false;
   }
   int end;
   const int i = sums.find(a.batch, unit, end);
-  const Shape s = shape_of<SIZE, PAGED>(a, i, kKeys);
-  const int pieces = __builtin_amdgcn_readfirstlane((s.steps + most - 1) / most);
-  const int tiles = __builtin_amdgcn_readfirstlane(s.tiles);
+  const Request q = sums.request(a, i);
+  const Shape s = shape_of<SIZE>(a, q, kKeys);
+  const int pieces = (s.steps + most - 1) / most, tiles = s.tiles;
   const int local = unit - (end - tiles * pieces);
   const int tile = tiles - 1 - local / pieces;
   u.piece = local % pieces;
   u.slot0 = 0;
   if (pieces > 1 || block == 0) {
-    sums.make<SIZE, PAGED>(a, kKeys, [&](const Shape& x) {
+    sums.make(a, [&](const Request& y) {
+      const Shape x = shape_of<SIZE>(a, y, kKeys);
       const int n = (x.steps + most - 1) / most;
       return n > 1 ? x.tiles * n : 0;
     });
@@ -413,7 +439,7 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
     if (block == 0 && threadIdx.x == 0) *workspace(a, SIZE).used = sums.total * a.hk;
   }
   if (a.batch > 64) __syncthreads();
-  set_rows<SIZE, PAGED>(a, i, tile, u.r);
+  u.r = rows_of(a, i, q, tile, SIZE);
   int j0, j1;
   tile_keys(a, u.r, SIZE, j0, j1);
   const int own = (j1 - j0 + kKeys - 1) / kKeys;

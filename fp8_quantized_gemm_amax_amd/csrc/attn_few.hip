@@ -330,8 +330,12 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   // stretch for each workgroup: a stretch may end one tile, hold others whole and begin the next.
   // Without cuts a workgroup takes a whole tile.
   constexpr int kStep = 4 * kTileKeys;
-  Sums sums{ends, ends + kMaxSplitBatch, 0, 0};
-  if (split) sums.make<kRows, true>(a, kStep, [](const Shape& s) { return s.tiles * s.steps; });
+  Sums<true> sums(a, ends);
+  if (split)
+    sums.make(a, [&](const Request& q) {
+      const Shape s = shape_of<kRows>(a, q, kStep);
+      return s.tiles * s.steps;
+    });
   const int total = split ? sums.total * a.hk : gridDim.x;
   const int each = split ? max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), max(1, kMinKeys / kStep)) : 1;
   const int to = min(total, static_cast<int>(blockIdx.x + 1) * each);
@@ -343,15 +347,14 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
       int end;
       const int x = from - unit.head * sums.total;
       const int i = sums.find(a.batch, x, end);
-      const Shape s = shape_of<kRows, true>(a, i, kStep);
-      const int tiles = __builtin_amdgcn_readfirstlane(s.tiles), steps = __builtin_amdgcn_readfirstlane(s.steps);
-      const int low = __builtin_amdgcn_readfirstlane(s.low);
-      const int local = x - (end - tiles * steps), tile = local / steps, step = local - tile * steps;
+      const Request q = sums.request(a, i);
+      const Shape s = shape_of<kRows>(a, q, kStep);
+      const int steps = s.steps, local = x - (end - s.tiles * steps), tile = local / steps, step = local - tile * steps;
       n = min(to - from, steps - step);
-      set_rows<kRows, true>(a, i, tile, unit.r);
+      unit.r = rows_of(a, i, q, tile, kRows);
       tile_keys(a, unit.r, kRows, unit.j0, unit.j1);
-      unit.j0 = max(unit.j0, low + step * kStep);
-      unit.j1 = min(unit.j1, low + (step + n) * kStep);
+      unit.j0 = max(unit.j0, s.low + step * kStep);
+      unit.j1 = min(unit.j1, s.low + (step + n) * kStep);
       // the tile's pieces: a workgroup has at most two partial results, of its first tile and its last
       const int begin = from - step, first = begin / each, last = (begin + steps - 1) / each;
       unit.piece = static_cast<int>(blockIdx.x) - first;
