@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,9 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemv.hip", "serving_api.hip", "paged.hip", "attention.hip",
            "attn_tile.hip", "attn_few.hip"]
 OBJ_DIR = os.path.join(PKG, "_build")
+# the Python binding of the serving operators: host code against torch's headers
+BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_serving.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -49,19 +53,33 @@ def _run(cmd, verbose):
         raise RuntimeError(f"hipcc failed with exit code {res.returncode}: {' '.join(cmd[-3:])}")
 
 
+def binding_command(out):
+    """Compiles and links the serving binding (no HIP code: the host compiler)."""
+    import torch
+    from torch.utils import cpp_extension
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(), "/opt/rocm/include"]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-Wno-attributes",
+            *[x for i in includes for x in ("-isystem", i)], "-o", out, BINDING_SOURCE, "-L", libs, "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-L/opt/rocm/lib", "-lamdhip64", f"-Wl,-rpath,{libs}"]
+
+
 def build_library(verbose=False):
-    """Compile every HIP source to an object (in parallel), then link LIB_PATH.  Always
-    recompiles."""
+    """Compile every HIP source to an object and the serving binding (in parallel), then link
+    LIB_PATH.  Always recompiles."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     objs = [os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o") for src in SOURCES]
     cmds = [[hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, os.path.join(CSRC, src)]
             for src, obj in zip(SOURCES, objs)]
+    cmds.append(binding_command(BINDING_PATH + ".tmp"))
     workers = max(1, min(len(cmds), int(os.environ.get("MAX_JOBS", os.cpu_count() or 1))))
     with ThreadPoolExecutor(workers) as pool:
         list(pool.map(lambda c: _run(c, verbose), cmds))
     tmp = LIB_PATH + ".tmp"
     _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB_PATH)
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
 
 
