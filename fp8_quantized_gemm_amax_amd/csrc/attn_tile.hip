@@ -34,14 +34,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
   constexpr int kPlanes = D / 64, kTile = kPlanes * kPlane, kSteps = D / 16;
   constexpr bool kPaged = SRC != SRC_PACKED, kCodes = SRC == SRC_E4M3, kRange = kCodes && DT == DT_F16;
   __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];   // K, K, V, V
-  __shared__ __attribute__((aligned(16))) float scales[kCodes ? 2 : 1][2][kKeys];   // of the tile's keys and values
+  __shared__ __attribute__((aligned(16))) float kscale[kCodes ? 4 : 1][kKeys], vscale[kCodes ? 2 : 1][kKeys];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half = lane >> 5, col = lane & 31;
   Unit unit;
   if (!unit_of<kRows, kPaged>(a, split, lds, unit)) return;
   const Rows& r = unit.r;
   const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
 
+  const float c = a.scale * kLog2e;
+  v16f o[D / 32];
+  float m, l;     // running maximum (times c) and this lane's share of the sum
+  int unit_exp;   // kRange: o is in units of 2^unit_exp
+
+  // Over the keys; ODD: again, with the values that are not finite kept apart.
+  auto pass = [&](auto odd_c, const int lane) {
+  constexpr bool ODD = decltype(odd_c)::value;
+  const int half = lane >> 5, col = lane & 31;
   // this wave's rows, and this lane's
   const int w0 = min(r.row0 + 32 * wave, r.rows - 1), w1 = min(w0 + 31, r.rows - 1);
   const int wave_first = r.pos0 + w0 / a.group, wave_last = r.pos0 + w1 / a.group;
@@ -80,42 +88,34 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       for (int x = 0; x < kPlanes; ++x)
         dma16_safe(rs, base + buffer * kTile + x * kPlane + (2 * wave + g) * 1024, off[g] + x * 128);
   };
-  // codes in flight: a lane's D / 4 bytes of one key, of K and V, and one scale of each
-  v4i ck[kPlanes], cv[kPlanes];
-  float sk = 0.0f, sv = 0.0f;
-  auto fetch = [&](int t, int page) {
+  // codes in flight: a lane's D / 4 bytes of one key and one scale
+  struct Codes {
+    v4i c[kPlanes];
+    float s;
+  };
+  auto fetch = [&](const void* p, const float* sp, int t, int page, Codes& to) {
     const int at = t + 16 * wave, have = min(max(r.len - at, 0), 16);
     const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
     const int64_t first = ((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
     const int n = there ? have : 0;
-    auto buffer = [&](const void* p, int64_t bytes, int each) {
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(p)) + bytes * each, 0, n * each, kRsrcWord3);
+    auto buffer = [&](const void* q, int each) {
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(q)) + first * each, 0, n * each, kRsrcWord3);
     };
-    const auto rk = buffer(a.k, first, D), rv = buffer(a.v, first, D);
+    const auto rc = buffer(p, D);
 #pragma unroll
-    for (int x = 0; x < kPlanes; ++x) {
-      ck[x] = __builtin_amdgcn_raw_buffer_load_b128(rk, lane * (D / 4) + 16 * x, 0, 0);
-      cv[x] = __builtin_amdgcn_raw_buffer_load_b128(rv, lane * (D / 4) + 16 * x, 0, 0);
-    }
-    sk = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(a.ks, first, 4), (lane & 15) * 4, 0, 0));
-    sv = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(a.vs, first, 4), (lane & 15) * 4, 0, 0));
+    for (int x = 0; x < kPlanes; ++x) to.c[x] = __builtin_amdgcn_raw_buffer_load_b128(rc, lane * (D / 4) + 16 * x, 0, 0);
+    to.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(sp, 4), (lane & 15) * 4, 0, 0));
   };
-  auto put = [&](int buffer) {
+  auto put = [&](const Codes& from, int buffer, float* to_scale) {
     const int key = 16 * wave + (lane >> 2);
 #pragma unroll
     for (int x = 0; x < kPlanes; ++x) {
       const int c = (lane & 3) * (D / 32) + 2 * x;       // first of the two chunks of eight channels
-      char* to = lds + (c >> 3) * kPlane + key * 128;
-      const int c0 = ((c & 7) ^ gemm::swz(key & 15)) << 4, c1 = (((c & 7) + 1) ^ gemm::swz(key & 15)) << 4;
-      *reinterpret_cast<v4u*>(to + buffer * kTile + c0) = codes8<DT>(ck[x][0], ck[x][1]);
-      *reinterpret_cast<v4u*>(to + buffer * kTile + c1) = codes8<DT>(ck[x][2], ck[x][3]);
-      *reinterpret_cast<v4u*>(to + (2 + buffer) * kTile + c0) = codes8<DT>(cv[x][0], cv[x][1]);
-      *reinterpret_cast<v4u*>(to + (2 + buffer) * kTile + c1) = codes8<DT>(cv[x][2], cv[x][3]);
+      char* to = lds + buffer * kTile + (c >> 3) * kPlane + key * 128;
+      *reinterpret_cast<v4u*>(to + (((c & 7) ^ gemm::swz(key & 15)) << 4)) = codes8<DT>(from.c[x][0], from.c[x][1]);
+      *reinterpret_cast<v4u*>(to + (((c & 7) + 1) ^ gemm::swz(key & 15)) * 16) = codes8<DT>(from.c[x][2], from.c[x][3]);
     }
-    if (lane < 16) {
-      scales[kCodes ? buffer : 0][0][16 * wave + lane] = sk;
-      scales[kCodes ? buffer : 0][1][16 * wave + lane] = sv;
-    }
+    if (lane < 16) to_scale[16 * wave + lane] = from.s;
   };
 
   // LDS addresses of this lane's operands
@@ -125,170 +125,282 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
   const uint32_t va0 = vr * 128 + ((vc ^ gemm::swz(vr)) << 4) + vb;
   const uint32_t va1 = (vr + 8) * 128 + ((vc ^ gemm::swz(vr + 8)) << 4) + vb;
 
-  const float c = a.scale * kLog2e;
-  v16f o[D / 32];
-  float m, l;     // running maximum (times c) and this lane's share of the sum
-  int unit_exp;   // kRange: o is in units of 2^unit_exp
+  // Scores of 32 of a tile's keys: A operands of steps 4 q .. 4 q + 3, and their products.
+  auto read_k = [&](int buffer, int w, v8s (&k)[kSteps / 2]) {
+#pragma unroll
+    for (int i = 0; i < kSteps / 2; ++i) {
+      const int x = (w & 1) * (kSteps / 2) + i;
+      k[i] = *reinterpret_cast<const v8s*>(lds + buffer * kTile + (x / 4) * kPlane + (w / 2) * 4096 + (ka ^ ((2 * x % 8) << 4)));
+    }
+  };
+  auto score = [&](int w, const v8s (&k)[kSteps / 2], v16f (&s)[2]) {
+    if ((w & 1) == 0) s[w / 2] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSteps / 2; ++i) s[w / 2] = mfma<DT>(k[i], q[(w & 1) * (kSteps / 2) + i], s[w / 2]);
+  };
+  auto read_v1 = [&](int buffer, int w, int i) -> v8s {      // 16 keys, channels 32 i ..
+    const uint32_t flip = (i & 1) << 6;
+    const char* at = lds + (2 + buffer) * kTile + (i / 2) * kPlane + w * 2048;
+    const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va0 ^ flip)));
+    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va1 ^ flip)));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto read_v = [&](int buffer, int w, v8s (&v)[D / 32]) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) v[i] = read_v1(buffer, w, i);
+  };
 
-  // Over the keys once; ODD: again, with the values that are not finite kept apart.
-  auto walk = [&](auto odd_c) {
+  // The steps from a tile's scores to its weights: the keys' scales; the mask; the running maximum
+  // and what it rescales; (kRange) the unit of o and the factor to it; 16 keys' weights for the
+  // product with their values, and their share of the sum.
+  auto scale_scores = [&](v16f (&s)[2], const float* scale) {
+    if constexpr (kCodes) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const v4f x = *reinterpret_cast<const v4f*>(scale + 32 * u + 8 * g + 4 * half);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][4 * g + i] *= x[i];
+        }
+    }
+  };
+  auto mask_scores = [&](v16f (&s)[2], int t) {
+    if (t + kKeys - 1 > wave_first || (a.window > 0 && t < wave_last - a.window + 1)) {
+      const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = 32 * u + 8 * (i / 4) + i % 4;
+          s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
+        }
+    }
+  };
+  auto follow_maximum = [&](v16f (&s)[2], auto& o) {
+    constexpr int kBlocks = sizeof(o) / sizeof(v16f);
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+    top = max_halves(top) * c;
+    if (__any(top > m + kSlack)) {
+      const float m1 = fmaxf(m, top);
+      const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+      m = m1;
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[i][x] *= keep;
+    }
+  };
+  auto follow_scales = [&](const float* scale, auto& o) -> float {
+    constexpr int kBlocks = sizeof(o) / sizeof(v16f);
+    float unit_inv = 1.0f;
+    if constexpr (kRange) {
+      // A weight's share of its value's scale, in units of a power of two at least the largest
+      // scale met, so that no product leaves fp16's range.
+      float most = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const v4f x = *reinterpret_cast<const v4f*>(scale + 32 * u + 8 * g + 4 * half);
+          most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
+        }
+      most = max_halves(most);
+      const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
+      if (e > unit_exp) {      // the same in every lane: the scales are
+        const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
+        unit_exp = e;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[i][x] *= keep;
+      }
+      unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
+    }
+    return unit_inv;
+  };
+  auto weigh = [&](auto odd_c, const v16f (&s)[2], int w, float mb, float unit_inv, const float* scale) -> v8s {
     constexpr bool ODD = decltype(odd_c)::value;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w / 2][8 * (w & 1) + i], c, -mb));
+      l += x[i];
+    }
+    if constexpr (kCodes) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const v4f y = *reinterpret_cast<const v4f*>(scale + 16 * w + 8 * g + 4 * half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float z = x[4 * g + i] * (kRange ? y[i] * unit_inv : y[i]);
+          x[4 * g + i] = ODD && x[4 * g + i] == 0.0f ? 0.0f : z;
+        }
+      }
+    }
+    return __builtin_bit_cast(v8s, v4u{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
+  };
+
+  // Over the keys once.  Tile i's
+  // weights are formed while the matrix unit multiplies tile i + 1's keys and the weights that are
+  // ready with tile i's values: K runs one tile ahead of V.
+  auto walk = [&]() {
     m = -INFINITY;
     l = 0.0f;
     unit_exp = -200;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
-    int page = page_of(j0);
-    if (j0 < j1) {
-      if constexpr (kCodes) {
-        fetch(j0, page);
-        put(0);
-        fetch(j0 + kKeys, page_of(j0 + kKeys));
-      } else {
-        bring(a.k, a.kts, a.khs, koff, j0, page, 0);
-        bring(a.v, a.vts, a.vhs, voff, j0, page, 2);
-      }
+    if (j0 >= j1) return;
+    v16f s0[2], s1[2];
+    Codes ck, cv;
+    int page = page_of(j0), page1 = page_of(j0 + kKeys), page2 = page_of(j0 + 2 * kKeys);
+    if constexpr (kCodes) {
+      Codes first;
+      fetch(a.k, a.ks, j0, page, first);
+      fetch(a.k, a.ks, j0 + kKeys, page1, ck);
+      fetch(a.v, a.vs, j0, page, cv);
+      put(first, 0, kscale[0]);
+      put(ck, 1, kscale[kCodes ? 1 : 0]);
+      put(cv, 2, vscale[0]);
+      fetch(a.k, a.ks, j0 + 2 * kKeys, page2, ck);
+      fetch(a.v, a.vs, j0 + kKeys, page1, cv);
+    } else {
+      bring(a.k, a.kts, a.khs, koff, j0, page, 0);
+      bring(a.k, a.kts, a.khs, koff, j0 + kKeys, page1, 1);
+      bring(a.v, a.vts, a.vhs, voff, j0, page, 2);
+      wait_vmcnt<4 * kPlanes>();      // the first K tile: the next one's and V's DMAs came after it
     }
-    page = page_of(j0 + (kCodes ? 2 : 1) * kKeys);
-    int buf = 0;
-    for (int t = j0; t < j1; t += kKeys, buf ^= 1) {
+    wait_lds_reads();
+    stage_barrier();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      v8s k[kSteps / 2];
+      read_k(0, w, k);
+      score(w, k, s0);
+    }
+    int t = j0, tile = 0;
+    auto step = [&](auto parity, v16f (&s)[2], v16f (&next)[2]) {
+      constexpr int B = decltype(parity)::value;      // tile i's buffer
       wait_lds_reads();
       if constexpr (!kCodes) wait_vmcnt<0>();
       stage_barrier();
-      if constexpr (!kCodes) {
-        if (t + kKeys < j1) {
-          bring(a.k, a.kts, a.khs, koff, t + kKeys, page, buf ^ 1);
-          bring(a.v, a.vts, a.vhs, voff, t + kKeys, page, 2 + (buf ^ 1));
-          page = page_of(t + 2 * kKeys);
-        }
-      } else {
-        if (t + kKeys < j1) {
-          put(buf ^ 1);
-          fetch(t + 2 * kKeys, page);
-          page = page_of(t + 3 * kKeys);
-        }
-      }
-      if (t > wave_last) continue;      // this wave sees none of them (uniform; the barriers stay common)
-      const char* kt = lds + buf * kTile;
-      v16f s[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        s[u] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const v8s k = *reinterpret_cast<const v8s*>(kt + (i / 4) * kPlane + u * 4096 + (ka ^ ((2 * i % 8) << 4)));
-          s[u] = mfma<DT>(k, q[i], s[u]);
-        }
-      }
+      page = page1;
+      page1 = page2;
+      page2 = page_of(t + 3 * kKeys);
       if constexpr (kCodes) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const v4f x = *reinterpret_cast<const v4f*>(&scales[buf][0][32 * u + 8 * g + 4 * half]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[u][4 * g + i] *= x[i];
-          }
+        put(ck, B, kscale[kCodes ? (tile + 2) & 3 : 0]);
+        put(cv, 2 + (B ^ 1), vscale[kCodes ? B ^ 1 : 0]);
+        fetch(a.k, a.ks, t + 3 * kKeys, page2, ck);
+        fetch(a.v, a.vs, t + 2 * kKeys, page1, cv);
+      } else if (t + kKeys < j1) {
+        bring(a.k, a.kts, a.khs, koff, t + 2 * kKeys, page1, B);
+        bring(a.v, a.vts, a.vhs, voff, t + kKeys, page, 2 + (B ^ 1));
       }
-      if (t + kKeys - 1 > wave_first || (a.window > 0 && t < wave_last - a.window + 1)) {
-        const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = 32 * u + 8 * (i / 4) + i % 4;
-            s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
-          }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-      top = max_halves(top) * c;
-      if (__any(top > m + kSlack)) {
-        const float m1 = fmaxf(m, top);
-        const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
-        m = m1;
-        l *= keep;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) o[i][x] *= keep;
-      }
+      v8s k[2][kSteps / 2], v[2][D / 32];
+      read_k(B ^ 1, 0, k[0]);
+      scale_scores(s, kscale[kCodes ? tile & 3 : 0]);
+      mask_scores(s, t);
+      follow_maximum(s, o);
       const float mb = m == -INFINITY ? 0.0f : m;
+      const float unit_inv = follow_scales(vscale[kCodes ? B : 0], o);
+      v8s p[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int w = 0; w < 4; ++w) {      // 16 keys
+        if (w < 3) read_k(B ^ 1, w + 1, k[(w + 1) & 1]);
+        read_v(B, w, v[w & 1]);
+        p[w & 1] = weigh(std::false_type{}, s, w, mb, unit_inv, vscale[kCodes ? B : 0]);
+        score(w, k[w & 1], next);
+        if (w > 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], c, -mb));
-          l += s[u][i];
-        }
-      if constexpr (kCodes) {
-        // a weight's share of its value's scale; for fp16, in units of a power of two at least the
-        // largest scale met, so that no product leaves fp16's range
-        float unit_inv = 1.0f;
-        if constexpr (kRange) {
-          float most = 0.0f;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const v4f x = *reinterpret_cast<const v4f*>(&scales[buf][1][32 * u + 8 * g + 4 * half]);
-              most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
-            }
-          most = max_halves(most);
-          const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
-          if (e > unit_exp) {      // the same in every lane: the scales are
-            const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
-            unit_exp = e;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-              for (int x = 0; x < 16; ++x) o[i][x] *= keep;
-          }
-          unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
+          for (int i = 0; i < D / 32; ++i)
+            o[i] = mfma<DT>(v[(w + 1) & 1][i], p[(w + 1) & 1], o[i]);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const v4f x = *reinterpret_cast<const v4f*>(&scales[buf][1][32 * u + 8 * g + 4 * half]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float y = s[u][4 * g + i] * (kRange ? x[i] * unit_inv : x[i]);
-              s[u][4 * g + i] = ODD && s[u][4 * g + i] == 0.0f ? 0.0f : y;
-            }
-          }
+        for (int n = 0; n < kSteps / 2 + (w > 0 ? D / 32 : 0); ++n) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // MFMA
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);    // LDS reads
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    // VALU
+          __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);    // exponentials
+        }
       }
-      v8s p[4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        v4u x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = pack2<DT>(s[w / 2][8 * (w & 1) + 2 * i], s[w / 2][8 * (w & 1) + 2 * i + 1]);
-        p[w] = __builtin_bit_cast(v8s, x);
-      }
-      const char* vt = lds + (2 + buf) * kTile;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t flip = (i & 1) << 6;
-          const char* at = vt + (i / 2) * kPlane + w * 2048;
-          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va0 ^ flip)));
-          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va1 ^ flip)));
-          const v8s v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-          if constexpr (ODD) o[i] = mfma_odd<DT>(v, p[w], o[i]);
-          else o[i] = mfma<DT>(v, p[w], o[i]);
-        }
+      for (int i = 0; i < D / 32; ++i) o[i] = mfma<DT>(v[1][i], p[1], o[i]);
+      t += kKeys;
+      ++tile;
+    };
+    while (true) {
+      step(std::integral_constant<int, 0>{}, s0, s1);
+      if (t >= j1) break;
+      step(std::integral_constant<int, 1>{}, s1, s0);
+      if (t >= j1) break;
     }
   };
-  walk(std::false_type{});
+  // Once more, with the values that are not finite kept apart: 32 channels at a time and one tile
+  // after the other (few registers, so that the code above keeps its own).
+  auto walk_odd = [&]() {
+#pragma unroll 1
+    for (int x = 0; x < D / 32; ++x) {
+      v16f part[1];
+      part[0] = 0.0f;
+      m = -INFINITY;
+      l = 0.0f;
+      unit_exp = -200;
+#pragma unroll 1
+      for (int t = j0; t < j1; t += kKeys) {
+        const int page = page_of(t);
+        wait_lds_reads();
+        stage_barrier();
+        if constexpr (kCodes) {
+          Codes codes;
+          fetch(a.k, a.ks, t, page, codes);
+          put(codes, 0, kscale[0]);
+          fetch(a.v, a.vs, t, page, codes);
+          put(codes, 2, vscale[0]);
+        } else {
+          bring(a.k, a.kts, a.khs, koff, t, page, 0);
+          bring(a.v, a.vts, a.vhs, voff, t, page, 2);
+          wait_vmcnt<0>();
+        }
+        wait_lds_reads();
+        stage_barrier();
+        v16f s[2];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          v8s k[kSteps / 2];
+          read_k(0, w, k);
+          score(w, k, s);
+        }
+        scale_scores(s, kscale[0]);
+        mask_scores(s, t);
+        follow_maximum(s, part);
+        const float mb = m == -INFINITY ? 0.0f : m, unit_inv = follow_scales(vscale[0], part);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) part[0] = mfma_odd<DT>(read_v1(0, w, x), weigh(std::true_type{}, s, w, mb, unit_inv, vscale[0]), part[0]);
+      }
+#pragma unroll
+      for (int y = 0; y < D / 32; ++y)
+        if (y == x) o[y] = part[0];
+    }
+  };
+  if constexpr (ODD) walk_odd();
+  else walk();
+  };   // pass
+  pass(std::false_type{}, lane);
   bool fine = true;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int x = 0; x < 16; ++x) fine &= __builtin_isfinite(o[i][x]);
-  if (__syncthreads_or(!fine)) walk(std::true_type{});
+  if (__syncthreads_or(!fine)) {
+    int again = lane;      // nothing of the first pass is kept for it in registers
+    asm volatile("" : "+v"(again));
+    pass(std::true_type{}, again);
+  }
+  const int half = lane >> 5, col = lane & 31;
+  const int row = min(r.row0 + 32 * wave + col, r.rows - 1), tok = row / a.group, pos = r.pos0 + tok;
 
   l = add_halves(l);
   if constexpr (kRange) {
