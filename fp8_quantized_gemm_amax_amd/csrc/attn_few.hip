@@ -86,7 +86,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   auto bring_scales = [&](const float* p, int t, const int (&pages)[kGroups], uint32_t to) {
     int page = pages[0];
 #pragma unroll
-    for (int g = 1; g < kGroups; ++g) page = lane >> 4 == g ? pages[g] : page;
+    for (int g = 1; g < kGroups; ++g) {   // as a value of its own: a choice of addresses would put the array into memory
+      const int other = __builtin_amdgcn_readfirstlane(pages[g]);
+      page = lane >> 4 == g ? other : page;
+    }
     const int at = t + lane;
     const int64_t x = ((static_cast<int64_t>(page) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
     dma4_lane(p + x, to, at < r.len && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages));
