@@ -79,8 +79,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     const int at = t + 16 * wave;
     return at < r.len ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
   };
-  auto bring = [&](const void* p, int64_t ts, int64_t hs, const uint32_t (&off)[2], int t, int page, int buffer) {
-    v4i rs = key_rows<SRC, D>(a, r, p, ts, hs, h, t + 16 * wave, 16, page);
+  // Where the wave's 16 keys of the tile at key t lie: their first row, and how many there are.
+  struct Place {
+    int64_t row;
+    int n;
+  };
+  auto place = [&](int t, int page) -> Place {
+    const int at = t + 16 * wave, have = min(max(r.len - at, 0), 16);
+    if constexpr (!kPaged) return {r.begin + at, have};
+    const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
+    return {((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1)), there ? have : 0};
+  };
+  auto bring = [&](const void* p, int64_t ts, int64_t hs, const uint32_t (&off)[2], const Place& at, int buffer) {
+    const char* from = static_cast<const char*>(p) + (kPaged ? at.row * D : at.row * ts + h * hs) * 2;
+    v4i rs = make_rsrc(from, at.n > 0 ? static_cast<uint32_t>((at.n - 1) * (kPaged ? D : ts) * 2 + D * 2) : 0u);
     settle(rs);
 #pragma unroll
     for (int g = 0; g < 2; ++g)
@@ -93,13 +105,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     v4i c[kPlanes];
     float s;
   };
-  auto fetch = [&](const void* p, const float* sp, int t, int page, Codes& to) {
-    const int at = t + 16 * wave, have = min(max(r.len - at, 0), 16);
-    const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
-    const int64_t first = ((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
-    const int n = there ? have : 0;
+  auto fetch = [&](const void* p, const float* sp, const Place& at, Codes& to) {
     auto buffer = [&](const void* q, int each) {
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(q)) + first * each, 0, n * each, kRsrcWord3);
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(q)) + at.row * each, 0, at.n * each, kRsrcWord3);
     };
     const auto rc = buffer(p, D);
 #pragma unroll
@@ -256,21 +264,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     if (j0 >= j1) return;
     v16f s0[2], s1[2];
     Codes ck, cv;
-    int page = page_of(j0), page1 = page_of(j0 + kKeys), page2 = page_of(j0 + 2 * kKeys);
+    const Place at0 = place(j0, page_of(j0));
+    Place at1 = place(j0 + kKeys, page_of(j0 + kKeys));   // of the tile whose V comes next
+    int page = page_of(j0 + 2 * kKeys);                   // of the tile whose K comes next
     if constexpr (kCodes) {
       Codes first;
-      fetch(a.k, a.ks, j0, page, first);
-      fetch(a.k, a.ks, j0 + kKeys, page1, ck);
-      fetch(a.v, a.vs, j0, page, cv);
+      fetch(a.k, a.ks, at0, first);
+      fetch(a.k, a.ks, at1, ck);
+      fetch(a.v, a.vs, at0, cv);
       put(first, 0, kscale[0]);
       put(ck, 1, kscale[kCodes ? 1 : 0]);
       put(cv, 2, vscale[0]);
-      fetch(a.k, a.ks, j0 + 2 * kKeys, page2, ck);
-      fetch(a.v, a.vs, j0 + kKeys, page1, cv);
+      const Place at2 = place(j0 + 2 * kKeys, page);
+      fetch(a.k, a.ks, at2, ck);
+      fetch(a.v, a.vs, at1, cv);
+      at1 = at2;
+      page = page_of(j0 + 3 * kKeys);
     } else {
-      bring(a.k, a.kts, a.khs, koff, j0, page, 0);
-      bring(a.k, a.kts, a.khs, koff, j0 + kKeys, page1, 1);
-      bring(a.v, a.vts, a.vhs, voff, j0, page, 2);
+      bring(a.k, a.kts, a.khs, koff, at0, 0);
+      bring(a.k, a.kts, a.khs, koff, at1, 1);
+      bring(a.v, a.vts, a.vhs, voff, at0, 2);
       wait_vmcnt<4 * kPlanes>();      // the first K tile: the next one's and V's DMAs came after it
     }
     wait_lds_reads();
@@ -287,17 +300,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       wait_lds_reads();
       if constexpr (!kCodes) wait_vmcnt<0>();
       stage_barrier();
-      page = page1;
-      page1 = page2;
-      page2 = page_of(t + 3 * kKeys);
       if constexpr (kCodes) {
         put(ck, B, kscale[kCodes ? (tile + 2) & 3 : 0]);
         put(cv, 2 + (B ^ 1), vscale[kCodes ? B ^ 1 : 0]);
-        fetch(a.k, a.ks, t + 3 * kKeys, page2, ck);
-        fetch(a.v, a.vs, t + 2 * kKeys, page1, cv);
+        const Place at = place(t + 3 * kKeys, page);
+        fetch(a.k, a.ks, at, ck);
+        fetch(a.v, a.vs, at1, cv);
+        at1 = at;
+        page = page_of(t + 4 * kKeys);
       } else if (t + kKeys < j1) {
-        bring(a.k, a.kts, a.khs, koff, t + 2 * kKeys, page1, B);
-        bring(a.v, a.vts, a.vhs, voff, t + kKeys, page, 2 + (B ^ 1));
+        const Place at = place(t + 2 * kKeys, page);
+        bring(a.k, a.kts, a.khs, koff, at, B);
+        bring(a.v, a.vts, a.vhs, voff, at1, 2 + (B ^ 1));
+        at1 = at;
+        page = page_of(t + 3 * kKeys);
       }
       v8s k[2][kSteps / 2], v[2][D / 32];
       read_k(B ^ 1, 0, k[0]);
@@ -350,18 +366,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       unit_exp = -200;
 #pragma unroll 1
       for (int t = j0; t < j1; t += kKeys) {
-        const int page = page_of(t);
+        const Place at = place(t, page_of(t));
         wait_lds_reads();
         stage_barrier();
         if constexpr (kCodes) {
           Codes codes;
-          fetch(a.k, a.ks, t, page, codes);
+          fetch(a.k, a.ks, at, codes);
           put(codes, 0, kscale[0]);
-          fetch(a.v, a.vs, t, page, codes);
+          fetch(a.v, a.vs, at, codes);
           put(codes, 2, vscale[0]);
         } else {
-          bring(a.k, a.kts, a.khs, koff, t, page, 0);
-          bring(a.v, a.vts, a.vhs, voff, t, page, 2);
+          bring(a.k, a.kts, a.khs, koff, at, 0);
+          bring(a.v, a.vts, a.vhs, voff, at, 2);
           wait_vmcnt<0>();
         }
         wait_lds_reads();
