@@ -59,29 +59,29 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
   __shared__ int64_t part[kPlanThreads / 64][2];
   int64_t base[2] = {0, 0}, lost = 0;
   const bool first = blockIdx.x == 0;
-  for (int i0 = 0; i0 < a.batch; i0 += kPlanThreads) {
-    const int i = i0 + threadIdx.x;
-    int64_t na = 0, np = 0;
-    if (i < a.batch) {
-      const int64_t c = max(a.cached[i], 0), n = max(a.added[i], 0);
-      na = n;
-      const int had = pages_for(c, a.page_shift, a.width);
-      np = pages_for(c + n, a.page_shift, a.width) - had;
-      if (first) {
-        a.lens[i] = static_cast<int>(min(c + n, int64_t{0x7fffffff}));
-        const int64_t one = int64_t{1} << a.page_shift;   // entries the table does not have
-        lost += max(int64_t{0}, ((c + n + one - 1) >> a.page_shift) - max((c + one - 1) >> a.page_shift, int64_t{a.width}));
-      }
+  // Each thread sums a run of requests of its own, one scan over the threads puts the runs in place.
+  const int run = (a.batch + kPlanThreads - 1) / kPlanThreads;
+  const int begin = min(static_cast<int>(threadIdx.x) * run, a.batch), end = min(begin + run, a.batch);
+  int64_t na = 0, np = 0;
+  for (int i = begin; i < end; ++i) {
+    const int64_t c = max(a.cached[i], 0), n = max(a.added[i], 0);
+    na += n;
+    np += pages_for(c + n, a.page_shift, a.width) - pages_for(c, a.page_shift, a.width);
+    cu[i] = static_cast<int>(min(na, int64_t{0x7fffffff}));
+    pg[i] = static_cast<int>(min(np, int64_t{0x7fffffff}));
+    if (first) {
+      a.lens[i] = static_cast<int>(min(c + n, int64_t{0x7fffffff}));
+      const int64_t one = int64_t{1} << a.page_shift;   // entries the table does not have
+      lost += max(int64_t{0}, ((c + n + one - 1) >> a.page_shift) - max((c + one - 1) >> a.page_shift, int64_t{a.width}));
     }
-    int64_t total[2];
-    scan2(na, np, part, total);
-    if (i < a.batch) {
-      cu[i] = static_cast<int>(min(base[0] + na, int64_t{0x7fffffff}));
-      pg[i] = static_cast<int>(min(base[1] + np, int64_t{0x7fffffff}));
-      if (first) a.cu[i + 1] = cu[i];
-    }
-    base[0] += total[0];
-    base[1] += total[1];
+  }
+  const int64_t own_a = na, own_p = np;
+  scan2(na, np, part, base);
+  const int64_t before_a = na - own_a, before_p = np - own_p;
+  for (int i = begin; i < end; ++i) {
+    cu[i] = static_cast<int>(min(before_a + cu[i], int64_t{0x7fffffff}));
+    pg[i] = static_cast<int>(min(before_p + pg[i], int64_t{0x7fffffff}));
+    if (first) a.cu[i + 1] = cu[i];
   }
   __syncthreads();
   const int taken = max(*a.taken_in, 0);
