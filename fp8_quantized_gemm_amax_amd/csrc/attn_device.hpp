@@ -138,21 +138,15 @@ __device__ __forceinline__ bool find_rows(const AttnArgs& a, int j, int size, bo
   return true;
 }
 
-// Base of the next n <= 16 keys from key `at` on (uniform, at a multiple of 8 inside one page),
-// as a buffer whose reads past the request's keys, or of a page that is not there, give zeros.
+// The 16 keys from key `at` on (uniform, a multiple of 16, so inside one page) as a buffer whose reads
+// past the request's keys, or of a page that is not there, give zeros.
 template <int SRC, int D>
-__device__ __forceinline__ v4i key_rows(const AttnArgs& a, const Rows& r, const void* base, int64_t ts, int64_t hs,
-                                        int h, int at, int n, int page) {
+__device__ __forceinline__ v4i key_rows(const AttnArgs& a, const Rows& r, const void* base, int h, int at, int page) {
   constexpr int kElem = SRC == SRC_E4M3 ? 1 : 2;
-  const int have = min(max(r.len - at, 0), n);
-  if constexpr (SRC == SRC_PACKED) {
-    const char* p = static_cast<const char*>(base) + ((r.begin + at) * ts + h * hs) * 2;
-    return make_rsrc(p, have > 0 ? static_cast<uint32_t>((have - 1) * ts * 2 + D * 2) : 0u);
-  } else {
-    const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
-    const int64_t row = ((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
-    return make_rsrc(static_cast<const char*>(base) + row * (D * kElem), there ? static_cast<uint32_t>(have * D * kElem) : 0u);
-  }
+  const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
+  const int64_t row = ((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+  const int have = there ? min(max(r.len - at, 0), 16) : 0;
+  return make_rsrc(static_cast<const char*>(base) + row * (D * kElem), static_cast<uint32_t>(have * D * kElem));
 }
 
 // ------------------------------------------------------------------------------------------

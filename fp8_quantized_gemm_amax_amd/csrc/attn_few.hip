@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   auto bring = [&](const void* p, int t, const int (&pages)[kGroups], uint32_t to) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      v4i rs = key_rows<SRC, D>(a, r, p, 0, 0, h, t + 16 * g, 16, pages[g]);
+      v4i rs = key_rows<SRC, D>(a, r, p, h, t + 16 * g, pages[g]);
       settle(rs);
 #pragma unroll
       for (int x = 0; x < kPlanes; ++x)

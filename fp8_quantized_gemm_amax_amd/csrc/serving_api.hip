@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxInt = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
+constexpr int64_t kMaxKeys = int64_t{1} << 30;     // of a request: key numbers and their sums stay below 2^31
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool valid_dt(fp8_dtype_t dt) { return dt == FP8_BF16 || dt == FP8_F16; }
@@ -45,7 +46,8 @@ fp8_status_t check_heads(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, 
   return FP8_OK;
 }
 
-int window_of(int64_t window) { return window > kMaxInt ? 0 : static_cast<int>(window); }
+// A window that no request can fill is none.
+int window_of(int64_t window) { return window >= kMaxKeys ? 0 : static_cast<int>(window); }
 
 }  // namespace
 
@@ -140,7 +142,7 @@ fp8_status_t fp8_attn_prompt(const void* q, const void* k, const void* v, fp8_dt
 int64_t fp8_attn_paged_workspace(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int32_t head_dim,
                                  int64_t width, int32_t page_size, int64_t max_new) {
   if (check_heads(tokens, batch, q_heads, kv_heads, head_dim, 1.0f, 0) != FP8_OK || !valid_page(page_size) ||
-      width < 1 || width > kMaxInt / page_size || max_new < 0)
+      width < 1 || width > kMaxKeys / page_size || max_new < 0)
     return 0;
   return fp8amax::attn_paged_workspace(tokens, batch, q_heads, kv_heads, head_dim, width * page_size, max_new);
 }
@@ -157,7 +159,7 @@ fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const
   if (max_new < 0 || width < 1) return FP8_ERR_BAD_SHAPE;
   if (!valid_dt(dt) || !valid_format(format)) return FP8_ERR_BAD_DTYPE;
   if ((st = check_cache(pages, kv_heads, head_dim, page_size)) != FP8_OK) return st;
-  if (width > kMaxInt / page_size || (batch > 0 && width > kMaxElems / batch)) return FP8_ERR_TOO_LARGE;
+  if (width > kMaxKeys / page_size || (batch > 0 && width > kMaxElems / batch)) return FP8_ERR_TOO_LARGE;
   if ((st = check_strides(tokens, q_heads, q_token_stride, q_head_stride)) != FP8_OK) return st;
   if (tokens == 0 || batch == 0) return FP8_OK;
   const bool e4m3 = format == FP8_KV_E4M3;

@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/Exceptions.h>
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 
 #include <cmath>
 #include <map>
@@ -202,6 +203,7 @@ PyObject* paged_plan(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     on(cached, {{&added, "added"}, {&tab, "block_table"}, {&free, "free_pages"}, {&taken, "taken"}, {&o[0], names[0]}, {&o[1], names[1]},
                 {&o[2], names[2]}, {&o[3], names[3]}, {&o[4], names[4]}, {&o[5], names[5]}});
   }
+  const c10::DeviceGuard guard(cached.device());   // the launch goes to the tensors' GPU
   const fp8_status_t code = plan_fn(ptr<int32_t>(cached), ptr<int32_t>(added), batch, static_cast<int32_t>(page), ptr<int32_t>(tab), tab.size(1),
                                     ptr<int32_t>(free), free.size(0), ptr<int32_t>(taken), tokens, ptr<int32_t>(o[0]), ptr<int32_t>(o[1]),
                                     ptr<int32_t>(o[2]), ptr<int64_t>(o[3]), ptr<int32_t>(o[4]), ptr<int32_t>(o[5]), stream_of(a[8]));
@@ -235,6 +237,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     TORCH_CHECK_VALUE(!t->defined() || (!overlaps(*t, k) && !overlaps(*t, v)), "a cache overlaps k or v");
   on(k, {{&v, "v"}, {&slots, "slots"}});
   on_cache(k, c);
+  const c10::DeviceGuard guard(k.device());   // the launch goes to the tensors' GPU
   return status(append_fn(k.data_ptr(), v.data_ptr(), dt, k.size(0), heads, static_cast<int32_t>(dim), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                           ptr<int64_t>(slots), c.k.size(0), static_cast<int32_t>(page), c.format, c.k.data_ptr(), c.v.data_ptr(), ptr<float>(c.ks),
                           ptr<float>(c.vs), stream_of(a[7])));
@@ -289,6 +292,7 @@ PyObject* attn_prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const at::Tensor out = output(a[6], q, {&q, &k, &v, &cu});
   if (a[6] != Py_None) on(q, {{&k, "k"}, {&v, "v"}, {&cu, "cu_tokens"}, {&out, "out"}});
   const at::Tensor lse = s.lse ? at::empty({tokens, hq}, q.options().dtype(at::kFloat)) : at::Tensor();
+  const c10::DeviceGuard guard(q.device());   // the launch goes to the tensors' GPU
   const fp8_status_t code = prompt_fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, tokens, ptr<int32_t>(cu), cu.size(0) - 1, hq, k.size(1),
                                       static_cast<int32_t>(dim), q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1), s.scale,
                                       s.window, out.data_ptr(), ptr<float>(lse), stream_of(a[8]));
@@ -333,6 +337,7 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     TORCH_CHECK_VALUE(ws.dim() == 1 && ws.is_contiguous(), "workspace must be a contiguous vector");
     on(q, {{&ws, "workspace"}});
   }
+  const c10::DeviceGuard guard(q.device());   // the launch goes to the tensors' GPU
   const fp8_status_t code = paged_fn(q.data_ptr(), dt, tokens, ptr<int32_t>(cu), batch, hq, hk, static_cast<int32_t>(dim), q.stride(0), q.stride(1), c.format,
                                      c.k.data_ptr(), c.v.data_ptr(), ptr<float>(c.ks), ptr<float>(c.vs), pages, static_cast<int32_t>(page),
                                      ptr<int32_t>(tab), width, ptr<int32_t>(lens), s.scale, s.window, most, out.data_ptr(), ptr<float>(lse), ws.data_ptr(),

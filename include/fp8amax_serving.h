@@ -24,7 +24,8 @@
  * Packed sequences.  The tokens of a step's requests lie one after the other; request r's are
  * [cu_tokens[r], cu_tokens[r + 1]) (int32 [batch + 1] on the device, non-decreasing from 0).
  * Values outside [0, tokens] are clamped and a request whose end precedes its start is empty,
- * so any values give in-bounds accesses.  Output rows that no request covers are not written.
+ * so any values give in-bounds accesses; what is computed where they decrease is not specified.
+ * Output rows that no request covers are not written.
  *
  * Strides.  q, k and v are [tokens, heads, head_dim] with the last index contiguous; the token
  * and head strides are given in elements, non-negative multiples of 8 (so that a fused
@@ -88,7 +89,8 @@ fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t
  *   lse_i = log sum_j exp(softmax_scale * q_i . k_j)
  *   out : [tokens, q_heads, head_dim] of dt, dense.  lse : NULL or float32 [tokens, q_heads].
  *   The token strides of k and v are at least head_dim (with more than one token) and at most 2^20.
- *   softmax_scale : finite and > 0.  window : 0 (none) or the number of keys a query sees.
+ *   softmax_scale : finite and > 0.
+ *   window : 0 (none; 2^30 or more is none too) or the number of keys a query sees at most.
  * Scores, the running maximum and sum, and the output accumulate in float32; the weights are
  * rounded to dt for the product with v, and the result once to dt.
  */
@@ -104,7 +106,7 @@ fp8_status_t fp8_attn_prompt(const void* q, const void* k, const void* v, fp8_dt
  * a request of seq_lens[r] tokens in the cache (the new ones among them) are its last n, so
  * query i of them sits at position seq_lens[r] - n + i and sees the keys up to there.  A query
  * at a negative position (seq_lens[r] < n) sees none: its output is 0 and its lse -inf.
- *   seq_lens : int32 [batch], clamped to [0, width * page_size].
+ *   seq_lens : int32 [batch], clamped to [0, width * page_size], which is at most 2^30.
  *   max_new  : the largest number of new tokens of a request, 0 if unknown; it chooses the
  *              kernel and has no effect on what is computed.
  *   workspace : workspace_bytes of device memory, 16-byte aligned, of at least

@@ -317,6 +317,111 @@ def test_lengths_beyond_their_tensors_stay_inside():
     check_prompt(q, q2, q, [4, 6], out2, None, "bf16", 1 / 8, 0)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_cache_beyond_32_bit_offsets(e4m3):
+    """Pages whose bytes lie past 4 GiB (and elements past 2^31) of the cache: appended to and read."""
+    hk, dim, page = 8, 128, 1024
+    per = hk * page * dim * (1 if e4m3 else 2)
+    pages = (1 << 32) // per + 40 + ((1 << 31) // per if e4m3 else 0)
+    shape = (pages, hk, page, dim)
+    kind = torch.uint8 if e4m3 else torch.bfloat16
+    kc, vc = (torch.empty(shape, dtype=kind, device=DEV) for _ in "kv")
+    ks, vs = (torch.empty(shape[:3], device=DEV) for _ in "kv") if e4m3 else (None, None)
+    n = 1500
+    x = normal((n, 2 * hk, dim), "bf16", 41)
+    k, v = x[:, :hk], x[:, hk:]
+    table = i32([[pages - 1, pages - 37]])
+    t = torch.arange(n, device=DEV)
+    fp8.fp8_kv_append(k, v, table[0, t // page].long() * page + t % page, kc, vc, ks, vs)
+    for new in (1, 30):
+        q = normal((new, 16, dim), "bf16", 42 + new)
+        out = fp8.fp8_attn_paged(q, kc, vc, table, i32([n]), i32([0, new]), ks, vs, max_new=new)
+        kk, vv = f64_of(k), f64_of(v)
+        if e4m3:
+            kk, vv = (decode_e4m3(quantize_rowwise(bits_of(y).reshape(-1, dim), "bf16")[0]).astype(np.float64).reshape(n, hk, dim)
+                      * quantize_rowwise(bits_of(y).reshape(-1, dim), "bf16")[1].astype(np.float64).reshape(n, hk, 1) for y in (k, v))
+        ref = attention_ref(f64_of(q), kk, vv, n - new, 1 / math.sqrt(dim), 0)
+        check_rows(out, None, ref, "bf16", n, dim, float(np.abs(vv).max()), f"{new} new")
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 50, 90]])
+def test_decreasing_cu_tokens_leave_the_workspace_fit(new):
+    """What decreasing cu_tokens compute is not specified; the calls after them are right."""
+    cache = Cache([600, 3000, 900], 2, 128, 16, "bf16", False, 51)
+    q = normal((sum(new), 8, 128), "bf16", 52)
+    args = (cache.k, cache.v, cache.dev_table, cache.dev_lens)
+    want = fp8.fp8_attn_paged(q, *args, cu_of(new), max_new=max(new))
+    for cu in ([0, sum(new), 0, sum(new)], [sum(new), 2, 1, 0], [5, -3, 1 << 30, 7]):
+        fp8.fp8_attn_paged(q, *args, i32(cu), max_new=max(new))
+        fp8.fp8_attn_prompt(q, q[:, :2], q[:, 2:4], i32(cu))
+        assert torch.equal(fp8.fp8_attn_paged(q, *args, cu_of(new), max_new=max(new)), want)
+    check_paged(q, cache, new, want, None, "bf16", 1 / math.sqrt(128), 0)
+
+
+def test_workspace_of_the_caller():
+    """One workspace, zero in its counters only, serves calls of both kernels and of different sizes."""
+    cases = []
+    for seed, (lens, new, hk) in enumerate([([5000, 40], [1, 1], 4), ([3000], [100], 2), ([900, 8000, 7], [1, 1, 1], 1)]):
+        cache = Cache(lens, hk, 64, 32, "f16", False, 60 + seed)
+        q = normal((sum(new), hk * 4, 64), "f16", 70 + seed)
+        args = (q, cache.k, cache.v, cache.dev_table, cache.dev_lens, cu_of(new))
+        need = fp8.fp8_attn_paged_workspace(sum(new), len(new), hk * 4, hk, 64, cache.dev_table.shape[1], 32, max(new))
+        cases.append((args, max(new), need))
+    ws = torch.full((max(n for _, _, n in cases),), 0x5A, dtype=torch.uint8, device=DEV)
+    ws[:16384] = 0
+    for args, most, need in cases * 2:
+        assert need > 0
+        got = fp8.fp8_attn_paged(*args, max_new=most, workspace=ws)
+        assert torch.equal(got, fp8.fp8_attn_paged(*args, max_new=most))
+        with pytest.raises(fp8.Fp8Error, match="BAD_SHAPE"):
+            fp8.fp8_attn_paged(*args, max_new=most, workspace=ws[: need - 1])
+    assert not ws[:16384].any()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams keep apart (each stream has its own workspace)."""
+    cache = Cache([6000, 100], 4, 128, 16, "bf16", True, 81)
+    qs = [normal((2, 16, 128), "bf16", 82 + i) for i in range(2)]
+    args = (cache.k, cache.v, cache.dev_table, cache.dev_lens, cu_of([1, 1]), cache.ks, cache.vs)
+    want = [fp8.fp8_attn_paged(q, *args, max_new=1) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fp8.fp8_attn_paged(qs[i], *args, max_new=1))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o_, w in zip(got, want) for o in o_)
+
+
+@pytest.mark.parametrize("status,call", [
+    ("BAD_SHAPE", lambda c, q: fp8.fp8_attn_paged(q, c.k, c.v, c.dev_table, c.dev_lens, cu_of([1]), window=-1)),
+    ("BAD_SHAPE", lambda c, q: fp8.fp8_attn_paged(q, c.k, c.v, c.dev_table, c.dev_lens, cu_of([1]), softmax_scale=0.0)),
+    ("BAD_SHAPE", lambda c, q: fp8.fp8_attn_paged(q[:, :3], c.k, c.v, c.dev_table, c.dev_lens, cu_of([1]))),
+    ("BAD_SHAPE", lambda c, q: fp8.fp8_attn_paged(q, c.k[:, :, :12].contiguous(), c.v[:, :, :12].contiguous(), c.dev_table, c.dev_lens, cu_of([1]))),
+    ("BAD_SHAPE", lambda c, q: fp8.fp8_attn_prompt(q[..., :32].contiguous(), q[:, :2, :32].contiguous(), q[:, :2, :32].contiguous(), cu_of([1]))),
+    ("BAD_SHAPE", lambda c, q: fp8.fp8_paged_plan(i32([0]), i32([1]), i32([[0]]), i32([0]), i32([0]), 1, 24)),
+    ("TOO_LARGE", lambda c, q: fp8.fp8_paged_plan(i32([0] * 20000), i32([1] * 20000), i32([[0]] * 20000), i32([0]), i32([0]), 1, 16)),
+    ("BAD_SHAPE", lambda c, q: fp8.fp8_kv_append(q[:, :2, :32].contiguous(), q[:, :2, :32].contiguous(), torch.zeros(1, dtype=torch.int64, device=DEV),
+                                                 c.k[..., :32].contiguous(), c.v[..., :32].contiguous())),
+])
+def test_refused_sizes_are_errors(status, call):
+    cache = Cache([40], 2, 64, 16, "bf16", False, 91)
+    with pytest.raises(fp8.Fp8Error, match=status):
+        call(cache, normal((1, 4, 64), "bf16", 92))
+
+
+def test_empty_batches():
+    cache = Cache([40], 2, 64, 16, "bf16", False, 93)
+    none = normal((0, 4, 64), "bf16", 94)
+    assert fp8.fp8_attn_paged(none, cache.k, cache.v, cache.dev_table, cache.dev_lens, i32([0, 0])).shape == (0, 4, 64)
+    out, lse = fp8.fp8_attn_prompt(none, none[:, :2], none[:, 2:], i32([0]), return_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    fp8.fp8_kv_append(none[:, :2], none[:, 2:], torch.zeros(0, dtype=torch.int64, device=DEV), cache.k, cache.v)
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------------------- streams, graphs
 
 def step_inputs():
