@@ -3,16 +3,24 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "attn_device.hpp"
 
 namespace fp8amax {
 namespace attn {
 namespace {
 
-// Whether a batch goes to the kernel for few rows: where every request has at most 32 rows a key
-// head.  Without max_new, by the average.
-bool few_rows(int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
-  return (max_new > 0 ? max_new : (tokens + batch - 1) / (batch > 0 ? batch : 1)) * group <= 32;
+// Whether a batch goes to the kernel for few rows: where its requests have at most 32 rows a key head on
+// average (64 over an e4m3 cache, which the kernel for many rows has to widen on the way), and none, as
+// far as max_new says, has more than 512, since that one's keys are read once for every 32 rows.
+// Kernel for many rows against the one for few, in us, 24 to 32 requests over up to 4000 keys, 128
+// channels, by average rows a request:
+//   16 bits  19 rows 48.7 : 44.6    31 rows 49.3 : 51.0    39 rows (500 keys) 17.6 : 27.7    73 rows 157 : 280
+//   e4m3     15 rows 52.2 : 32.0    32 rows 54.3 : 37.5    56 rows 68.3 : 43.4    61 rows 59.8 : 50.7
+//            73 rows 195 : 184      80 rows 65.4 : 66.3
+bool few_rows(bool e4m3, int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
+  return std::min(max_new, tokens) * group <= 512 && tokens * group <= (e4m3 ? 64 : 32) * batch;
 }
 
 // Joins the partial results of the launch for many rows, of 128 rows each: a thread takes one row and
@@ -91,7 +99,7 @@ void launch_attn_join(int dt, int head_dim, const AttnArgs& a, hipStream_t s) {
 }  // namespace attn
 
 void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnArgs& a, hipStream_t s) {
-  if (attn::few_rows(max_new, a.group, a.tokens, a.batch)) attn::launch_attn_few(dt, head_dim, e4m3, a, s);
+  if (attn::few_rows(e4m3, max_new, a.group, a.tokens, a.batch)) attn::launch_attn_few(dt, head_dim, e4m3, a, s);
   else attn::launch_attn_tile(dt, head_dim, e4m3, a, s);
 }
 
@@ -99,8 +107,12 @@ int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t 
                              int64_t max_new) {
   using namespace attn;
   if (!may_split(tokens, hq / hk, batch, hk, capacity)) return 0;
-  const bool few = few_rows(max_new, hq / hk, tokens, batch);
-  return workspace_bytes(few ? 2 * kFewGroups : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
+  auto bytes = [&](bool few) {
+    return workspace_bytes(few ? 2 * kFewGroups : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
+  };
+  // Enough for either format of the cache.
+  return std::max(bytes(few_rows(false, max_new, hq / hk, tokens, batch)),
+                  bytes(few_rows(true, max_new, hq / hk, tokens, batch)));
 }
 
 }  // namespace fp8amax

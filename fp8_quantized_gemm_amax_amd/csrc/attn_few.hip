@@ -56,278 +56,278 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
     off[g] = i * (kCodes ? D : 2 * D) + chunk_of(lane & (kRowBytes / 16 - 1), i) * 16;
   }
   auto run = [&](const Unit& unit) {
-  const Rows& r = unit.r;
-  const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
-  const int last_row = min(r.row0 + 31, r.rows - 1);
-  const int first_pos = r.pos0 + r.row0 / a.group, last_pos = r.pos0 + last_row / a.group;
-  const int row = min(r.row0 + col, last_row), tok = row / a.group, pos = r.pos0 + tok;
-  const int low = a.window > 0 ? pos - a.window + 1 : 0;
-  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (r.begin + tok) * a.qts + (h * a.group + row - tok * a.group) * a.qhs;
-  v8s q[kSteps];
+    const Rows& r = unit.r;
+    const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
+    const int last_row = min(r.row0 + 31, r.rows - 1);
+    const int first_pos = r.pos0 + r.row0 / a.group, last_pos = r.pos0 + last_row / a.group;
+    const int row = min(r.row0 + col, last_row), tok = row / a.group, pos = r.pos0 + tok;
+    const int low = a.window > 0 ? pos - a.window + 1 : 0;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (r.begin + tok) * a.qts + (h * a.group + row - tok * a.group) * a.qhs;
+    v8s q[kSteps];
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)   // codes are read 16 channels at a time: their order over two steps
-    q[s] = *reinterpret_cast<const v8s*>(qp + (kCodes ? 32 * (s / 2) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half));
+    for (int s = 0; s < kSteps; ++s)   // codes are read 16 channels at a time: their order over two steps
+      q[s] = *reinterpret_cast<const v8s*>(qp + (kCodes ? 32 * (s / 2) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half));
 
-  auto page_of = [&](int at) -> int {
-    return at < j1 ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
-  };
-  auto bring = [&](const void* p, int t, const int (&pages)[kGroups], uint32_t to) {
+    auto page_of = [&](int at) -> int {
+      return at < j1 ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
+    };
+    auto bring = [&](const void* p, int t, const int (&pages)[kGroups], uint32_t to) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      v4i rs = key_rows<SRC, D>(a, r, p, h, t + 16 * g, pages[g]);
-      settle(rs);
+      for (int g = 0; g < kGroups; ++g) {
+        v4i rs = key_rows<SRC, D>(a, r, p, h, t + 16 * g, pages[g]);
+        settle(rs);
 #pragma unroll
-      for (int x = 0; x < kPlanes; ++x)
+        for (int x = 0; x < kPlanes; ++x)
 #pragma unroll
-        for (int y = 0; y < kRowBytes / 64; ++y)
-          dma16_safe(rs, to + x * kPlaneBytes + g * 16 * kRowBytes + y * 1024, off[y] + x * 128);
-    }
-  };
-  auto bring_scales = [&](const float* p, int t, const int (&pages)[kGroups], uint32_t to) {
-    int page = pages[0];
+          for (int y = 0; y < kRowBytes / 64; ++y)
+            dma16_safe(rs, to + x * kPlaneBytes + g * 16 * kRowBytes + y * 1024, off[y] + x * 128);
+      }
+    };
+    auto bring_scales = [&](const float* p, int t, const int (&pages)[kGroups], uint32_t to) {
+      int page = pages[0];
 #pragma unroll
-    for (int g = 1; g < kGroups; ++g) {   // as a value of its own: a choice of addresses would put the array into memory
-      const int other = __builtin_amdgcn_readfirstlane(pages[g]);
-      page = lane >> 4 == g ? other : page;
-    }
-    const int at = t + lane;
-    const int64_t x = ((static_cast<int64_t>(page) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
-    dma4_lane(p + x, to, at < r.len && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages));
-  };
+      for (int g = 1; g < kGroups; ++g) {   // as a value of its own: a choice of addresses would put the array into memory
+        const int other = __builtin_amdgcn_readfirstlane(pages[g]);
+        page = lane >> 4 == g ? other : page;
+      }
+      const int at = t + lane;
+      const int64_t x = ((static_cast<int64_t>(page) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+      dma4_lane(p + x, to, at < r.len && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages));
+    };
 
-  // this lane's operands in LDS
-  const int vr = kCodes ? 4 * half + ((lane >> 1) & 3) + 8 * ((lane >> 3) & 1) : 4 * half + ((lane & 15) >> 2);
-  const int vdsub = (lane >> 4) & 1;
+    // this lane's operands in LDS
+    const int vr = kCodes ? 4 * half + ((lane >> 1) & 3) + 8 * ((lane >> 3) & 1) : 4 * half + ((lane & 15) >> 2);
+    const int vdsub = (lane >> 4) & 1;
 
-  const float c = a.scale * kLog2e;
-  v16f o[D / 32];
-  float m, l;
-  int unit_exp;
-  auto walk = [&](auto odd_c) {
-    constexpr bool ODD = decltype(odd_c)::value;
-    m = -INFINITY;
-    l = 0.0f;
-    unit_exp = -200;
+    const float c = a.scale * kLog2e;
+    v16f o[D / 32];
+    float m, l;
+    int unit_exp;
+    auto walk = [&](auto odd_c) {
+      constexpr bool ODD = decltype(odd_c)::value;
+      m = -INFINITY;
+      l = 0.0f;
+      unit_exp = -200;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
-    int pages[kGroups];
-    int t = j0 + wave * kTileKeys;
+      for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
+      int pages[kGroups];
+      int t = j0 + wave * kTileKeys;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t + 16 * g);
-    if (t < j1) {
-      if constexpr (kCodes) bring_scales(a.ks, t, pages, lds_addr(my_ks));
-      bring(a.k, t, pages, kbase);
-      if constexpr (kCodes) bring_scales(a.vs, t, pages, lds_addr(my_vs));
-      bring(a.v, t, pages, vbase);
-    }
-    for (; t < j1; t += 4 * kTileKeys) {
-      const int t1 = t + 4 * kTileKeys;
+      for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t + 16 * g);
+      if (t < j1) {
+        if constexpr (kCodes) bring_scales(a.ks, t, pages, lds_addr(my_ks));
+        bring(a.k, t, pages, kbase);
+        if constexpr (kCodes) bring_scales(a.vs, t, pages, lds_addr(my_vs));
+        bring(a.v, t, pages, vbase);
+      }
+      for (; t < j1; t += 4 * kTileKeys) {
+        const int t1 = t + 4 * kTileKeys;
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t1 + 16 * g);
-      wait_vmcnt<kDma>();      // K is there: at least the DMAs of V came after it
-      asm volatile("" ::: "memory");
-      v16f s[kSub];
+        for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t1 + 16 * g);
+        wait_vmcnt<kDma>();      // K is there: at least the DMAs of V came after it
+        asm volatile("" ::: "memory");
+        v16f s[kSub];
 #pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        s[u] = 0.0f;
-        const int i = 32 * u + col;
-        if constexpr (kCodes) {
+        for (int u = 0; u < kSub; ++u) {
+          s[u] = 0.0f;
+          const int i = 32 * u + col;
+          if constexpr (kCodes) {
 #pragma unroll
-          for (int x = 0; x < kSteps / 2; ++x) {
-            const v4u w = *reinterpret_cast<const v4u*>(kt + i * kRowBytes + (chunk_of(2 * x + half, i) << 4));
-            s[u] = mfma<DT>(__builtin_bit_cast(v8s, codes8<DT>(w[0], w[1])), q[2 * x], s[u]);
-            s[u] = mfma<DT>(__builtin_bit_cast(v8s, codes8<DT>(w[2], w[3])), q[2 * x + 1], s[u]);
-          }
+            for (int x = 0; x < kSteps / 2; ++x) {
+              const v4u w = *reinterpret_cast<const v4u*>(kt + i * kRowBytes + (chunk_of(2 * x + half, i) << 4));
+              s[u] = mfma<DT>(__builtin_bit_cast(v8s, codes8<DT>(w[0], w[1])), q[2 * x], s[u]);
+              s[u] = mfma<DT>(__builtin_bit_cast(v8s, codes8<DT>(w[2], w[3])), q[2 * x + 1], s[u]);
+            }
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const v4f x = *reinterpret_cast<const v4f*>(my_ks + 32 * u + 8 * g + 4 * half);
+            for (int g = 0; g < 4; ++g) {
+              const v4f x = *reinterpret_cast<const v4f*>(my_ks + 32 * u + 8 * g + 4 * half);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) s[u][4 * g + y] *= x[y];
-          }
-        } else {
+              for (int y = 0; y < 4; ++y) s[u][4 * g + y] *= x[y];
+            }
+          } else {
 #pragma unroll
-          for (int x = 0; x < kSteps; ++x) {
-            const v8s k = *reinterpret_cast<const v8s*>(kt + (x / 4) * kPlaneBytes + i * 128 + (chunk_of(2 * (x & 3) + half, i) << 4));
-            s[u] = mfma<DT>(k, q[x], s[u]);
+            for (int x = 0; x < kSteps; ++x) {
+              const v8s k = *reinterpret_cast<const v8s*>(kt + (x / 4) * kPlaneBytes + i * 128 + (chunk_of(2 * (x & 3) + half, i) << 4));
+              s[u] = mfma<DT>(k, q[x], s[u]);
+            }
           }
         }
-      }
-      wait_lds_reads();
-      if (t1 < j1) {
-        if constexpr (kCodes) bring_scales(a.ks, t1, pages, lds_addr(my_ks));
-        bring(a.k, t1, pages, kbase);
-      }
-      if (t + kTileKeys - 1 > first_pos || (a.window > 0 && t < last_pos - a.window + 1)) {
-        const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
+        wait_lds_reads();
+        if (t1 < j1) {
+          if constexpr (kCodes) bring_scales(a.ks, t1, pages, lds_addr(my_ks));
+          bring(a.k, t1, pages, kbase);
+        }
+        if (t + kTileKeys - 1 > first_pos || (a.window > 0 && t < last_pos - a.window + 1)) {
+          const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int key = 32 * u + 8 * (i / 4) + i % 4;
+              s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
+            }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 16 * kSub; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+        top = max_halves(top) * c;
+        if (__any(top > m)) {
+          const float m1 = fmaxf(m, top);
+          const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+          m = m1;
+          l *= keep;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[i][x] *= keep;
+        }
+        const float mb = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int key = 32 * u + 8 * (i / 4) + i % 4;
-            s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
+            s[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], c, -mb));
+            l += s[u][i];
           }
-      }
-      float top = s[0][0];
+        // V is there: at least the DMAs of the next K came after it, if there is one
+        if (t1 < j1) wait_vmcnt<kDma>();
+        else wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
+        if constexpr (kCodes) {
+          float unit_inv = 1.0f;
+          if constexpr (kRange) {
+            float most = 0.0f;
 #pragma unroll
-      for (int i = 1; i < 16 * kSub; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-      top = max_halves(top) * c;
-      if (__any(top > m)) {
-        const float m1 = fmaxf(m, top);
-        const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
-        m = m1;
-        l *= keep;
+            for (int u = 0; u < kSub; ++u)
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
+              for (int g = 0; g < 4; ++g) {
+                const v4f x = *reinterpret_cast<const v4f*>(my_vs + 32 * u + 8 * g + 4 * half);
+                most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
+              }
+            most = max_halves(most);
+            const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
+            if (e > unit_exp) {
+              const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
+              unit_exp = e;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[i][x] *= keep;
-      }
-      const float mb = m == -INFINITY ? 0.0f : m;
+              for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int u = 0; u < kSub; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], c, -mb));
-          l += s[u][i];
-        }
-      // V is there: at least the DMAs of the next K came after it, if there is one
-      if (t1 < j1) wait_vmcnt<kDma>();
-      else wait_vmcnt<0>();
-      asm volatile("" ::: "memory");
-      if constexpr (kCodes) {
-        float unit_inv = 1.0f;
-        if constexpr (kRange) {
-          float most = 0.0f;
+                for (int x = 0; x < 16; ++x) o[i][x] *= keep;
+            }
+            unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
+          }
 #pragma unroll
           for (int u = 0; u < kSub; ++u)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const v4f x = *reinterpret_cast<const v4f*>(my_vs + 32 * u + 8 * g + 4 * half);
-              most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float z = s[u][4 * g + y] * (kRange ? x[y] * unit_inv : x[y]);
+                s[u][4 * g + y] = ODD && s[u][4 * g + y] == 0.0f ? 0.0f : z;
+              }
             }
-          most = max_halves(most);
-          const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
-          if (e > unit_exp) {
-            const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
-            unit_exp = e;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-              for (int x = 0; x < 16; ++x) o[i][x] *= keep;
-          }
-          unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
         }
 #pragma unroll
-        for (int u = 0; u < kSub; ++u)
+        for (int w = 0; w < kTileKeys / 16; ++w) {
+          v4u x;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const v4f x = *reinterpret_cast<const v4f*>(my_vs + 32 * u + 8 * g + 4 * half);
+          for (int i = 0; i < 4; ++i) x[i] = pack2<DT>(s[w / 2][8 * (w & 1) + 2 * i], s[w / 2][8 * (w & 1) + 2 * i + 1]);
+          const v8s p = __builtin_bit_cast(v8s, x);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float z = s[u][4 * g + y] * (kRange ? x[y] * unit_inv : x[y]);
-              s[u][4 * g + y] = ODD && s[u][4 * g + y] == 0.0f ? 0.0f : z;
+          for (int i = 0; i < D / 32; ++i) {
+            v8s v;
+            if constexpr (kCodes) {
+              typedef int v2i __attribute__((ext_vector_type(2)));
+              const int key = 16 * w + vr;
+              const char* at = vt + key * kRowBytes + (chunk_of(2 * i + vdsub, key) << 4) + (lane & 1) * 8;
+              const v2i y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)at);
+              v = __builtin_bit_cast(v8s, codes8<DT>(y[0], y[1]));
+            } else {
+              const int chunk = (i & 1) * 4 + vdsub * 2 + ((lane & 3) >> 1);
+              const char* at = vt + (i / 2) * kPlaneBytes + (lane & 1) * 8;
+              const int k0 = 16 * w + vr, k1 = k0 + 8;
+              const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k0 * 128 + (chunk_of(chunk, k0) << 4)));
+              const v4s z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k1 * 128 + (chunk_of(chunk, k1) << 4)));
+              v = __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7);
             }
+            if constexpr (ODD) o[i] = mfma_odd<DT>(v, p, o[i]);
+            else o[i] = mfma<DT>(v, p, o[i]);
           }
-      }
-#pragma unroll
-      for (int w = 0; w < kTileKeys / 16; ++w) {
-        v4u x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = pack2<DT>(s[w / 2][8 * (w & 1) + 2 * i], s[w / 2][8 * (w & 1) + 2 * i + 1]);
-        const v8s p = __builtin_bit_cast(v8s, x);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          v8s v;
-          if constexpr (kCodes) {
-            typedef int v2i __attribute__((ext_vector_type(2)));
-            const int key = 16 * w + vr;
-            const char* at = vt + key * kRowBytes + (chunk_of(2 * i + vdsub, key) << 4) + (lane & 1) * 8;
-            const v2i y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)at);
-            v = __builtin_bit_cast(v8s, codes8<DT>(y[0], y[1]));
-          } else {
-            const int chunk = (i & 1) * 4 + vdsub * 2 + ((lane & 3) >> 1);
-            const char* at = vt + (i / 2) * kPlaneBytes + (lane & 1) * 8;
-            const int k0 = 16 * w + vr, k1 = k0 + 8;
-            const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k0 * 128 + (chunk_of(chunk, k0) << 4)));
-            const v4s z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k1 * 128 + (chunk_of(chunk, k1) << 4)));
-            v = __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7);
-          }
-          if constexpr (ODD) o[i] = mfma_odd<DT>(v, p, o[i]);
-          else o[i] = mfma<DT>(v, p, o[i]);
+        }
+        wait_lds_reads();
+        if (t1 < j1) {
+          if constexpr (kCodes) bring_scales(a.vs, t1, pages, lds_addr(my_vs));
+          bring(a.v, t1, pages, vbase);
         }
       }
-      wait_lds_reads();
-      if (t1 < j1) {
-        if constexpr (kCodes) bring_scales(a.vs, t1, pages, lds_addr(my_vs));
-        bring(a.v, t1, pages, vbase);
+      l = add_halves(l);
+      if constexpr (kRange) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[i][x] = __builtin_ldexpf(o[i][x], unit_exp);
       }
-    }
-    l = add_halves(l);
-    if constexpr (kRange) {
+      // join the four waves: wave w adds up channels 32 w .. 32 w + 31 and keeps them in o[0]
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-        for (int x = 0; x < 16; ++x) o[i][x] = __builtin_ldexpf(o[i][x], unit_exp);
-    }
-    // join the four waves: wave w adds up channels 32 w .. 32 w + 31 and keeps them in o[0]
-    __syncthreads();
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<v4f*>(lds + (wave * (D / 32) + i) * 4096 + g * 1024 + lane * 16) =
+              v4f{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
+      if (half == 0) {
+        stats[0][wave][col] = m;
+        stats[1][wave][col] = l;
+      }
+      __syncthreads();
+      float mw[4];
+      m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, mw[w] = stats[0][w][col]);
+      l = 0.0f;
+      o[0] = 0.0f;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<v4f*>(lds + (wave * (D / 32) + i) * 4096 + g * 1024 + lane * 16) =
-            v4f{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
-    if (half == 0) {
-      stats[0][wave][col] = m;
-      stats[1][wave][col] = l;
-    }
-    __syncthreads();
-    float mw[4];
-    m = -INFINITY;
+      for (int w = 0; w < 4; ++w) {
+        const float f = mw[w] == m ? 1.0f : __builtin_amdgcn_exp2f(mw[w] - m);
+        l = __builtin_fmaf(f, stats[1][w][col], l);
+        if (wave < D / 32) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, mw[w] = stats[0][w][col]);
-    l = 0.0f;
-    o[0] = 0.0f;
+          for (int g = 0; g < 4; ++g) {
+            const v4f x = *reinterpret_cast<const v4f*>(lds + (w * (D / 32) + wave) * 4096 + g * 1024 + lane * 16);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = mw[w] == m ? 1.0f : __builtin_amdgcn_exp2f(mw[w] - m);
-      l = __builtin_fmaf(f, stats[1][w][col], l);
-      if (wave < D / 32) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const v4f x = *reinterpret_cast<const v4f*>(lds + (w * (D / 32) + wave) * 4096 + g * 1024 + lane * 16);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) o[0][4 * g + y] = __builtin_fmaf(f, x[y], o[0][4 * g + y]);
+            for (int y = 0; y < 4; ++y) o[0][4 * g + y] = __builtin_fmaf(f, x[y], o[0][4 * g + y]);
+          }
         }
       }
-    }
-  };
-  walk(std::false_type{});
-  bool fine = true;
+    };
+    walk(std::false_type{});
+    bool fine = true;
 #pragma unroll
-  for (int x = 0; x < 16; ++x) fine &= __builtin_isfinite(o[0][x]);
-  if (__syncthreads_or(!fine)) walk(std::true_type{});
+    for (int x = 0; x < 16; ++x) fine &= __builtin_isfinite(o[0][x]);
+    if (__syncthreads_or(!fine)) walk(std::true_type{});
 
-  const bool mine = wave < D / 32 && r.row0 + col < r.rows;
-  if (unit.count > 1) {
-    if (mine) {
-      const Workspace ws = workspace(a, kRows);
-      const int64_t slot = unit.slot(unit.piece);
-      if (wave == 0 && half == 0) leave2(ws.stats + (slot * kRows + col) * 2, m, l);
-      leave_block(ws.out + slot * (kRows * D) + wave * 1024, o[0]);
+    const bool mine = wave < D / 32 && r.row0 + col < r.rows;
+    if (unit.count > 1) {
+      if (mine) {
+        const Workspace ws = workspace(a, kRows);
+        const int64_t slot = unit.slot(unit.piece);
+        if (wave == 0 && half == 0) leave2(ws.stats + (slot * kRows + col) * 2, m, l);
+        leave_block(ws.out + slot * (kRows * D) + wave * 1024, o[0]);
+      }
+      join_partials<DT, D, kRows>(a, unit, lds);
+      return;
     }
-    join_partials<DT, D, kRows>(a, unit, lds);
-    return;
-  }
-  if (!mine) return;
-  const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + h * a.group + (row - tok * a.group);
-  const float inv = pos < 0 ? 0.0f : 1.0f / l;
-  if (a.lse && wave == 0 && half == 0) a.lse[out_row] = pos < 0 ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
-  uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * D + 32 * wave + 4 * half;
+    if (!mine) return;
+    const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + h * a.group + (row - tok * a.group);
+    const float inv = pos < 0 ? 0.0f : 1.0f / l;
+    if (a.lse && wave == 0 && half == 0) a.lse[out_row] = pos < 0 ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * D + 32 * wave + 4 * half;
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    *reinterpret_cast<uint2*>(out + 8 * g) = make_uint2(pack2<DT>(o[0][4 * g] * inv, o[0][4 * g + 1] * inv),
-                                                        pack2<DT>(o[0][4 * g + 2] * inv, o[0][4 * g + 3] * inv));
-  };   // run
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<uint2*>(out + 8 * g) = make_uint2(pack2<DT>(o[0][4 * g] * inv, o[0][4 * g + 1] * inv),
+                                                          pack2<DT>(o[0][4 * g + 2] * inv, o[0][4 * g + 3] * inv));
+  };
 
   // The work of the batch as one line of steps, head by head, request by request, cut into one equal
   // stretch for each workgroup: a stretch may end one tile, hold others whole and begin the next.

@@ -48,362 +48,362 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 
   // Over the keys; ODD: again, with the values that are not finite kept apart.
   auto pass = [&](auto odd_c, const int lane) {
-  constexpr bool ODD = decltype(odd_c)::value;
-  const int half = lane >> 5, col = lane & 31;
-  // this wave's rows, and this lane's
-  const int w0 = min(r.row0 + 32 * wave, r.rows - 1), w1 = min(w0 + 31, r.rows - 1);
-  const int wave_first = r.pos0 + w0 / a.group, wave_last = r.pos0 + w1 / a.group;
-  const int row = min(r.row0 + 32 * wave + col, r.rows - 1);
-  const int tok = row / a.group, pos = r.pos0 + tok;
-  const int low = a.window > 0 ? pos - a.window + 1 : 0;
-  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (r.begin + tok) * a.qts + (h * a.group + row - tok * a.group) * a.qhs;
-  v8s q[kSteps];
+    constexpr bool ODD = decltype(odd_c)::value;
+    const int half = lane >> 5, col = lane & 31;
+    // this wave's rows, and this lane's
+    const int w0 = min(r.row0 + 32 * wave, r.rows - 1), w1 = min(w0 + 31, r.rows - 1);
+    const int wave_first = r.pos0 + w0 / a.group, wave_last = r.pos0 + w1 / a.group;
+    const int row = min(r.row0 + 32 * wave + col, r.rows - 1);
+    const int tok = row / a.group, pos = r.pos0 + tok;
+    const int low = a.window > 0 ? pos - a.window + 1 : 0;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (r.begin + tok) * a.qts + (h * a.group + row - tok * a.group) * a.qhs;
+    v8s q[kSteps];
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const v8s*>(qp + 16 * s + 8 * half);
+    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const v8s*>(qp + 16 * s + 8 * half);
 
-  // A tile into LDS: this wave brings keys 16 wave .. 16 wave + 15, 16-bit ones by DMA, codes
-  // through registers, where they are converted (exactly) once for all four waves.
-  const uint32_t base = lds_addr(lds);
-  uint32_t koff[2], voff[2];
-  if constexpr (!kCodes) {
-    const uint32_t kb = kPaged ? D * 2 : static_cast<uint32_t>(a.kts * 2), vb = kPaged ? D * 2 : static_cast<uint32_t>(a.vts * 2);
+    // A tile into LDS: this wave brings keys 16 wave .. 16 wave + 15, 16-bit ones by DMA, codes
+    // through registers, where they are converted (exactly) once for all four waves.
+    const uint32_t base = lds_addr(lds);
+    uint32_t koff[2], voff[2];
+    if constexpr (!kCodes) {
+      const uint32_t kb = kPaged ? D * 2 : static_cast<uint32_t>(a.kts * 2), vb = kPaged ? D * 2 : static_cast<uint32_t>(a.vts * 2);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const uint32_t c = gemm::dma_chunk(lane, g) * 16;
-      koff[g] = (8 * g + (lane >> 3)) * kb + c;
-      voff[g] = (8 * g + (lane >> 3)) * vb + c;
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t c = gemm::dma_chunk(lane, g) * 16;
+        koff[g] = (8 * g + (lane >> 3)) * kb + c;
+        voff[g] = (8 * g + (lane >> 3)) * vb + c;
+      }
     }
-  }
-  auto page_of = [&](int t) -> int {
-    if constexpr (!kPaged) return 0;
-    const int at = t + 16 * wave;
-    return at < r.len ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
-  };
-  // Where the wave's 16 keys of the tile at key t lie: their first row, and how many there are.
-  struct Place {
-    int64_t row;
-    int n;
-  };
-  auto place = [&](int t, int page) -> Place {
-    const int at = t + 16 * wave, have = min(max(r.len - at, 0), 16);
-    if constexpr (!kPaged) return {r.begin + at, have};
-    const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
-    return {((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1)), there ? have : 0};
-  };
-  auto bring = [&](const void* p, int64_t ts, int64_t hs, const uint32_t (&off)[2], const Place& at, int buffer) {
-    const char* from = static_cast<const char*>(p) + (kPaged ? at.row * D : at.row * ts + h * hs) * 2;
-    v4i rs = make_rsrc(from, at.n > 0 ? static_cast<uint32_t>((at.n - 1) * (kPaged ? D : ts) * 2 + D * 2) : 0u);
-    settle(rs);
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int x = 0; x < kPlanes; ++x)
-        dma16_safe(rs, base + buffer * kTile + x * kPlane + (2 * wave + g) * 1024, off[g] + x * 128);
-  };
-  // codes in flight: a lane's D / 4 bytes of one key and one scale
-  struct Codes {
-    v4i c[kPlanes];
-    float s;
-  };
-  auto fetch = [&](const void* p, const float* sp, const Place& at, Codes& to) {
-    auto buffer = [&](const void* q, int each) {
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(q)) + at.row * each, 0, at.n * each, kRsrcWord3);
+    auto page_of = [&](int t) -> int {
+      if constexpr (!kPaged) return 0;
+      const int at = t + 16 * wave;
+      return at < r.len ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
     };
-    const auto rc = buffer(p, D);
+    // Where the wave's 16 keys of the tile at key t lie: their first row, and how many there are.
+    struct Place {
+      int64_t row;
+      int n;
+    };
+    auto place = [&](int t, int page) -> Place {
+      const int at = t + 16 * wave, have = min(max(r.len - at, 0), 16);
+      if constexpr (!kPaged) return {r.begin + at, have};
+      const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
+      return {((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1)), there ? have : 0};
+    };
+    auto bring = [&](const void* p, int64_t ts, int64_t hs, const uint32_t (&off)[2], const Place& at, int buffer) {
+      const char* from = static_cast<const char*>(p) + (kPaged ? at.row * D : at.row * ts + h * hs) * 2;
+      v4i rs = make_rsrc(from, at.n > 0 ? static_cast<uint32_t>((at.n - 1) * (kPaged ? D : ts) * 2 + D * 2) : 0u);
+      settle(rs);
 #pragma unroll
-    for (int x = 0; x < kPlanes; ++x) to.c[x] = __builtin_amdgcn_raw_buffer_load_b128(rc, lane * (D / 4) + 16 * x, 0, 0);
-    to.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(sp, 4), (lane & 15) * 4, 0, 0));
-  };
-  auto put = [&](const Codes& from, int buffer, float* to_scale) {
-    const int key = 16 * wave + (lane >> 2);
+      for (int g = 0; g < 2; ++g)
 #pragma unroll
-    for (int x = 0; x < kPlanes; ++x) {
-      const int c = (lane & 3) * (D / 32) + 2 * x;       // first of the two chunks of eight channels
-      char* to = lds + buffer * kTile + (c >> 3) * kPlane + key * 128;
-      *reinterpret_cast<v4u*>(to + (((c & 7) ^ gemm::swz(key & 15)) << 4)) = codes8<DT>(from.c[x][0], from.c[x][1]);
-      *reinterpret_cast<v4u*>(to + (((c & 7) + 1) ^ gemm::swz(key & 15)) * 16) = codes8<DT>(from.c[x][2], from.c[x][3]);
-    }
-    if (lane < 16) to_scale[16 * wave + lane] = from.s;
-  };
+        for (int x = 0; x < kPlanes; ++x)
+          dma16_safe(rs, base + buffer * kTile + x * kPlane + (2 * wave + g) * 1024, off[g] + x * 128);
+    };
+    // codes in flight: a lane's D / 4 bytes of one key and one scale
+    struct Codes {
+      v4i c[kPlanes];
+      float s;
+    };
+    auto fetch = [&](const void* p, const float* sp, const Place& at, Codes& to) {
+      auto buffer = [&](const void* q, int each) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(q)) + at.row * each, 0, at.n * each, kRsrcWord3);
+      };
+      const auto rc = buffer(p, D);
+#pragma unroll
+      for (int x = 0; x < kPlanes; ++x) to.c[x] = __builtin_amdgcn_raw_buffer_load_b128(rc, lane * (D / 4) + 16 * x, 0, 0);
+      to.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(sp, 4), (lane & 15) * 4, 0, 0));
+    };
+    auto put = [&](const Codes& from, int buffer, float* to_scale) {
+      const int key = 16 * wave + (lane >> 2);
+#pragma unroll
+      for (int x = 0; x < kPlanes; ++x) {
+        const int c = (lane & 3) * (D / 32) + 2 * x;       // first of the two chunks of eight channels
+        char* to = lds + buffer * kTile + (c >> 3) * kPlane + key * 128;
+        *reinterpret_cast<v4u*>(to + (((c & 7) ^ gemm::swz(key & 15)) << 4)) = codes8<DT>(from.c[x][0], from.c[x][1]);
+        *reinterpret_cast<v4u*>(to + (((c & 7) + 1) ^ gemm::swz(key & 15)) * 16) = codes8<DT>(from.c[x][2], from.c[x][3]);
+      }
+      if (lane < 16) to_scale[16 * wave + lane] = from.s;
+    };
 
-  // LDS addresses of this lane's operands
-  const uint32_t ka = (lane & 31) * 128 + ((half ^ gemm::swz(lane & 15)) << 4);      // ^ (2 s % 8) * 16
-  const int vr = 4 * half + ((lane & 15) >> 2);                                      // + 16 s (+ 8)
-  const uint32_t vc = (((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)), vb = (lane & 1) * 8;   // chunk (^ 4: odd 32 channels)
-  const uint32_t va0 = vr * 128 + ((vc ^ gemm::swz(vr)) << 4) + vb;
-  const uint32_t va1 = (vr + 8) * 128 + ((vc ^ gemm::swz(vr + 8)) << 4) + vb;
+    // LDS addresses of this lane's operands
+    const uint32_t ka = (lane & 31) * 128 + ((half ^ gemm::swz(lane & 15)) << 4);      // ^ (2 s % 8) * 16
+    const int vr = 4 * half + ((lane & 15) >> 2);                                      // + 16 s (+ 8)
+    const uint32_t vc = (((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)), vb = (lane & 1) * 8;   // chunk (^ 4: odd 32 channels)
+    const uint32_t va0 = vr * 128 + ((vc ^ gemm::swz(vr)) << 4) + vb;
+    const uint32_t va1 = (vr + 8) * 128 + ((vc ^ gemm::swz(vr + 8)) << 4) + vb;
 
-  // Scores of 32 of a tile's keys: A operands of steps 4 q .. 4 q + 3, and their products.
-  auto read_k = [&](int buffer, int w, v8s (&k)[kSteps / 2]) {
+    // Scores of 32 of a tile's keys: A operands of steps 4 q .. 4 q + 3, and their products.
+    auto read_k = [&](int buffer, int w, v8s (&k)[kSteps / 2]) {
 #pragma unroll
-    for (int i = 0; i < kSteps / 2; ++i) {
-      const int x = (w & 1) * (kSteps / 2) + i;
-      k[i] = *reinterpret_cast<const v8s*>(lds + buffer * kTile + (x / 4) * kPlane + (w / 2) * 4096 + (ka ^ ((2 * x % 8) << 4)));
-    }
-  };
-  auto score = [&](int w, const v8s (&k)[kSteps / 2], v16f (&s)[2]) {
-    if ((w & 1) == 0) s[w / 2] = 0.0f;
+      for (int i = 0; i < kSteps / 2; ++i) {
+        const int x = (w & 1) * (kSteps / 2) + i;
+        k[i] = *reinterpret_cast<const v8s*>(lds + buffer * kTile + (x / 4) * kPlane + (w / 2) * 4096 + (ka ^ ((2 * x % 8) << 4)));
+      }
+    };
+    auto score = [&](int w, const v8s (&k)[kSteps / 2], v16f (&s)[2]) {
+      if ((w & 1) == 0) s[w / 2] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSteps / 2; ++i) s[w / 2] = mfma<DT>(k[i], q[(w & 1) * (kSteps / 2) + i], s[w / 2]);
-  };
-  auto read_v1 = [&](int buffer, int w, int i) -> v8s {      // 16 keys, channels 32 i ..
-    const uint32_t flip = (i & 1) << 6;
-    const char* at = lds + (2 + buffer) * kTile + (i / 2) * kPlane + w * 2048;
-    const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va0 ^ flip)));
-    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va1 ^ flip)));
-    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  auto read_v = [&](int buffer, int w, v8s (&v)[D / 32]) {
+      for (int i = 0; i < kSteps / 2; ++i) s[w / 2] = mfma<DT>(k[i], q[(w & 1) * (kSteps / 2) + i], s[w / 2]);
+    };
+    auto read_v1 = [&](int buffer, int w, int i) -> v8s {      // 16 keys, channels 32 i ..
+      const uint32_t flip = (i & 1) << 6;
+      const char* at = lds + (2 + buffer) * kTile + (i / 2) * kPlane + w * 2048;
+      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va0 ^ flip)));
+      const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + (va1 ^ flip)));
+      return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto read_v = [&](int buffer, int w, v8s (&v)[D / 32]) {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) v[i] = read_v1(buffer, w, i);
-  };
+      for (int i = 0; i < D / 32; ++i) v[i] = read_v1(buffer, w, i);
+    };
 
-  // The steps from a tile's scores to its weights: the keys' scales; the mask; the running maximum
-  // and what it rescales; (kRange) the unit of o and the factor to it; 16 keys' weights for the
-  // product with their values, and their share of the sum.
-  auto scale_scores = [&](v16f (&s)[2], const float* scale) {
-    if constexpr (kCodes) {
+    // The steps from a tile's scores to its weights: the keys' scales; the mask; the running maximum
+    // and what it rescales; (kRange) the unit of o and the factor to it; 16 keys' weights for the
+    // product with their values, and their share of the sum.
+    auto scale_scores = [&](v16f (&s)[2], const float* scale) {
+      if constexpr (kCodes) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const v4f x = *reinterpret_cast<const v4f*>(scale + 32 * u + 8 * g + 4 * half);
+          for (int g = 0; g < 4; ++g) {
+            const v4f x = *reinterpret_cast<const v4f*>(scale + 32 * u + 8 * g + 4 * half);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[u][4 * g + i] *= x[i];
-        }
-    }
-  };
-  auto mask_scores = [&](v16f (&s)[2], int t) {
-    if (t + kKeys - 1 > wave_first || (a.window > 0 && t < wave_last - a.window + 1)) {
-      const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
+            for (int i = 0; i < 4; ++i) s[u][4 * g + i] *= x[i];
+          }
+      }
+    };
+    auto mask_scores = [&](v16f (&s)[2], int t) {
+      if (t + kKeys - 1 > wave_first || (a.window > 0 && t < wave_last - a.window + 1)) {
+        const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = 32 * u + 8 * (i / 4) + i % 4;
-          s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
-        }
-    }
-  };
-  auto follow_maximum = [&](v16f (&s)[2], auto& o) {
-    constexpr int kBlocks = sizeof(o) / sizeof(v16f);
-    float top = s[0][0];
+          for (int i = 0; i < 16; ++i) {
+            const int key = 32 * u + 8 * (i / 4) + i % 4;
+            s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
+          }
+      }
+    };
+    auto follow_maximum = [&](v16f (&s)[2], auto& o) {
+      constexpr int kBlocks = sizeof(o) / sizeof(v16f);
+      float top = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-    top = max_halves(top) * c;
-    if (__any(top > m + kSlack)) {
-      const float m1 = fmaxf(m, top);
-      const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
-      m = m1;
-      l *= keep;
-#pragma unroll
-      for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) o[i][x] *= keep;
-    }
-  };
-  auto follow_scales = [&](const float* scale, auto& o) -> float {
-    constexpr int kBlocks = sizeof(o) / sizeof(v16f);
-    float unit_inv = 1.0f;
-    if constexpr (kRange) {
-      // A weight's share of its value's scale, in units of a power of two at least the largest
-      // scale met, so that no product leaves fp16's range.
-      float most = 0.0f;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const v4f x = *reinterpret_cast<const v4f*>(scale + 32 * u + 8 * g + 4 * half);
-          most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
-        }
-      most = max_halves(most);
-      const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
-      if (e > unit_exp) {      // the same in every lane: the scales are
-        const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
-        unit_exp = e;
+      for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+      top = max_halves(top) * c;
+      if (__any(top > m + kSlack)) {
+        const float m1 = fmaxf(m, top);
+        const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+        m = m1;
+        l *= keep;
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
           for (int x = 0; x < 16; ++x) o[i][x] *= keep;
       }
-      unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
-    }
-    return unit_inv;
-  };
-  auto weigh = [&](auto odd_c, const v16f (&s)[2], int w, float mb, float unit_inv, const float* scale) -> v8s {
-    constexpr bool ODD = decltype(odd_c)::value;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w / 2][8 * (w & 1) + i], c, -mb));
-      l += x[i];
-    }
-    if constexpr (kCodes) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const v4f y = *reinterpret_cast<const v4f*>(scale + 16 * w + 8 * g + 4 * half);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float z = x[4 * g + i] * (kRange ? y[i] * unit_inv : y[i]);
-          x[4 * g + i] = ODD && x[4 * g + i] == 0.0f ? 0.0f : z;
-        }
-      }
-    }
-    return __builtin_bit_cast(v8s, v4u{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
-  };
-
-  // Over the keys once.  Tile i's
-  // weights are formed while the matrix unit multiplies tile i + 1's keys and the weights that are
-  // ready with tile i's values: K runs one tile ahead of V.
-  auto walk = [&]() {
-    m = -INFINITY;
-    l = 0.0f;
-    unit_exp = -200;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
-    if (j0 >= j1) return;
-    v16f s0[2], s1[2];
-    Codes ck, cv;
-    const Place at0 = place(j0, page_of(j0));
-    Place at1 = place(j0 + kKeys, page_of(j0 + kKeys));   // of the tile whose V comes next
-    int page = page_of(j0 + 2 * kKeys);                   // of the tile whose K comes next
-    if constexpr (kCodes) {
-      Codes first;
-      fetch(a.k, a.ks, at0, first);
-      fetch(a.k, a.ks, at1, ck);
-      fetch(a.v, a.vs, at0, cv);
-      put(first, 0, kscale[0]);
-      put(ck, 1, kscale[kCodes ? 1 : 0]);
-      put(cv, 2, vscale[0]);
-      const Place at2 = place(j0 + 2 * kKeys, page);
-      fetch(a.k, a.ks, at2, ck);
-      fetch(a.v, a.vs, at1, cv);
-      at1 = at2;
-      page = page_of(j0 + 3 * kKeys);
-    } else {
-      bring(a.k, a.kts, a.khs, koff, at0, 0);
-      bring(a.k, a.kts, a.khs, koff, at1, 1);
-      bring(a.v, a.vts, a.vhs, voff, at0, 2);
-      wait_vmcnt<4 * kPlanes>();      // the first K tile: the next one's and V's DMAs came after it
-    }
-    wait_lds_reads();
-    stage_barrier();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      v8s k[kSteps / 2];
-      read_k(0, w, k);
-      score(w, k, s0);
-    }
-    int t = j0, tile = 0;
-    auto step = [&](auto parity, v16f (&s)[2], v16f (&next)[2]) {
-      constexpr int B = decltype(parity)::value;      // tile i's buffer
-      wait_lds_reads();
-      if constexpr (!kCodes) wait_vmcnt<0>();
-      stage_barrier();
-      if constexpr (kCodes) {
-        put(ck, B, kscale[kCodes ? (tile + 2) & 3 : 0]);
-        put(cv, 2 + (B ^ 1), vscale[kCodes ? B ^ 1 : 0]);
-        const Place at = place(t + 3 * kKeys, page);
-        fetch(a.k, a.ks, at, ck);
-        fetch(a.v, a.vs, at1, cv);
-        at1 = at;
-        page = page_of(t + 4 * kKeys);
-      } else if (t + kKeys < j1) {
-        const Place at = place(t + 2 * kKeys, page);
-        bring(a.k, a.kts, a.khs, koff, at, B);
-        bring(a.v, a.vts, a.vhs, voff, at1, 2 + (B ^ 1));
-        at1 = at;
-        page = page_of(t + 3 * kKeys);
-      }
-      v8s k[2][kSteps / 2], v[2][D / 32];
-      read_k(B ^ 1, 0, k[0]);
-      scale_scores(s, kscale[kCodes ? tile & 3 : 0]);
-      mask_scores(s, t);
-      follow_maximum(s, o);
-      const float mb = m == -INFINITY ? 0.0f : m;
-      const float unit_inv = follow_scales(vscale[kCodes ? B : 0], o);
-      v8s p[2];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {      // 16 keys
-        if (w < 3) read_k(B ^ 1, w + 1, k[(w + 1) & 1]);
-        read_v(B, w, v[w & 1]);
-        p[w & 1] = weigh(std::false_type{}, s, w, mb, unit_inv, vscale[kCodes ? B : 0]);
-        score(w, k[w & 1], next);
-        if (w > 0) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            o[i] = mfma<DT>(v[(w + 1) & 1][i], p[(w + 1) & 1], o[i]);
-        }
-#pragma unroll
-        for (int n = 0; n < kSteps / 2 + (w > 0 ? D / 32 : 0); ++n) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // MFMA
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);    // LDS reads
-          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    // VALU
-          __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);    // exponentials
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = mfma<DT>(v[1][i], p[1], o[i]);
-      t += kKeys;
-      ++tile;
     };
-    while (true) {
-      step(std::integral_constant<int, 0>{}, s0, s1);
-      if (t >= j1) break;
-      step(std::integral_constant<int, 1>{}, s1, s0);
-      if (t >= j1) break;
-    }
-  };
-  // Once more, with the values that are not finite kept apart: 32 channels at a time and one tile
-  // after the other (few registers, so that the code above keeps its own).
-  auto walk_odd = [&]() {
-#pragma unroll 1
-    for (int x = 0; x < D / 32; ++x) {
-      v16f part[1];
-      part[0] = 0.0f;
+    auto follow_scales = [&](const float* scale, auto& o) -> float {
+      constexpr int kBlocks = sizeof(o) / sizeof(v16f);
+      float unit_inv = 1.0f;
+      if constexpr (kRange) {
+        // A weight's share of its value's scale, in units of a power of two at least the largest
+        // scale met, so that no product leaves fp16's range.
+        float most = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const v4f x = *reinterpret_cast<const v4f*>(scale + 32 * u + 8 * g + 4 * half);
+            most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
+          }
+        most = max_halves(most);
+        const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
+        if (e > unit_exp) {      // the same in every lane: the scales are
+          const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
+          unit_exp = e;
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[i][x] *= keep;
+        }
+        unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
+      }
+      return unit_inv;
+    };
+    auto weigh = [&](auto odd_c, const v16f (&s)[2], int w, float mb, float unit_inv, const float* scale) -> v8s {
+      constexpr bool ODD = decltype(odd_c)::value;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w / 2][8 * (w & 1) + i], c, -mb));
+        l += x[i];
+      }
+      if constexpr (kCodes) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const v4f y = *reinterpret_cast<const v4f*>(scale + 16 * w + 8 * g + 4 * half);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float z = x[4 * g + i] * (kRange ? y[i] * unit_inv : y[i]);
+            x[4 * g + i] = ODD && x[4 * g + i] == 0.0f ? 0.0f : z;
+          }
+        }
+      }
+      return __builtin_bit_cast(v8s, v4u{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
+    };
+
+    // Over the keys once.  Tile i's
+    // weights are formed while the matrix unit multiplies tile i + 1's keys and the weights that are
+    // ready with tile i's values: K runs one tile ahead of V.
+    auto walk = [&]() {
       m = -INFINITY;
       l = 0.0f;
       unit_exp = -200;
-#pragma unroll 1
-      for (int t = j0; t < j1; t += kKeys) {
-        const Place at = place(t, page_of(t));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
+      if (j0 >= j1) return;
+      v16f s0[2], s1[2];
+      Codes ck, cv;
+      const Place at0 = place(j0, page_of(j0));
+      Place at1 = place(j0 + kKeys, page_of(j0 + kKeys));   // of the tile whose V comes next
+      int page = page_of(j0 + 2 * kKeys);                   // of the tile whose K comes next
+      if constexpr (kCodes) {
+        Codes first;
+        fetch(a.k, a.ks, at0, first);
+        fetch(a.k, a.ks, at1, ck);
+        fetch(a.v, a.vs, at0, cv);
+        put(first, 0, kscale[0]);
+        put(ck, 1, kscale[kCodes ? 1 : 0]);
+        put(cv, 2, vscale[0]);
+        const Place at2 = place(j0 + 2 * kKeys, page);
+        fetch(a.k, a.ks, at2, ck);
+        fetch(a.v, a.vs, at1, cv);
+        at1 = at2;
+        page = page_of(j0 + 3 * kKeys);
+      } else {
+        bring(a.k, a.kts, a.khs, koff, at0, 0);
+        bring(a.k, a.kts, a.khs, koff, at1, 1);
+        bring(a.v, a.vts, a.vhs, voff, at0, 2);
+        wait_vmcnt<4 * kPlanes>();      // the first K tile: the next one's and V's DMAs came after it
+      }
+      wait_lds_reads();
+      stage_barrier();
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v8s k[kSteps / 2];
+        read_k(0, w, k);
+        score(w, k, s0);
+      }
+      int t = j0, tile = 0;
+      auto step = [&](auto parity, v16f (&s)[2], v16f (&next)[2]) {
+        constexpr int B = decltype(parity)::value;      // tile i's buffer
         wait_lds_reads();
+        if constexpr (!kCodes) wait_vmcnt<0>();
         stage_barrier();
         if constexpr (kCodes) {
-          Codes codes;
-          fetch(a.k, a.ks, at, codes);
-          put(codes, 0, kscale[0]);
-          fetch(a.v, a.vs, at, codes);
-          put(codes, 2, vscale[0]);
-        } else {
-          bring(a.k, a.kts, a.khs, koff, at, 0);
-          bring(a.v, a.vts, a.vhs, voff, at, 2);
-          wait_vmcnt<0>();
+          put(ck, B, kscale[kCodes ? (tile + 2) & 3 : 0]);
+          put(cv, 2 + (B ^ 1), vscale[kCodes ? B ^ 1 : 0]);
+          const Place at = place(t + 3 * kKeys, page);
+          fetch(a.k, a.ks, at, ck);
+          fetch(a.v, a.vs, at1, cv);
+          at1 = at;
+          page = page_of(t + 4 * kKeys);
+        } else if (t + kKeys < j1) {
+          const Place at = place(t + 2 * kKeys, page);
+          bring(a.k, a.kts, a.khs, koff, at, B);
+          bring(a.v, a.vts, a.vhs, voff, at1, 2 + (B ^ 1));
+          at1 = at;
+          page = page_of(t + 3 * kKeys);
         }
-        wait_lds_reads();
-        stage_barrier();
-        v16f s[2];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          v8s k[kSteps / 2];
-          read_k(0, w, k);
-          score(w, k, s);
-        }
-        scale_scores(s, kscale[0]);
+        v8s k[2][kSteps / 2], v[2][D / 32];
+        read_k(B ^ 1, 0, k[0]);
+        scale_scores(s, kscale[kCodes ? tile & 3 : 0]);
         mask_scores(s, t);
-        follow_maximum(s, part);
-        const float mb = m == -INFINITY ? 0.0f : m, unit_inv = follow_scales(vscale[0], part);
+        follow_maximum(s, o);
+        const float mb = m == -INFINITY ? 0.0f : m;
+        const float unit_inv = follow_scales(vscale[kCodes ? B : 0], o);
+        v8s p[2];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) part[0] = mfma_odd<DT>(read_v1(0, w, x), weigh(std::true_type{}, s, w, mb, unit_inv, vscale[0]), part[0]);
+        for (int w = 0; w < 4; ++w) {      // 16 keys
+          if (w < 3) read_k(B ^ 1, w + 1, k[(w + 1) & 1]);
+          read_v(B, w, v[w & 1]);
+          p[w & 1] = weigh(std::false_type{}, s, w, mb, unit_inv, vscale[kCodes ? B : 0]);
+          score(w, k[w & 1], next);
+          if (w > 0) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              o[i] = mfma<DT>(v[(w + 1) & 1][i], p[(w + 1) & 1], o[i]);
+          }
+#pragma unroll
+          for (int n = 0; n < kSteps / 2 + (w > 0 ? D / 32 : 0); ++n) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);    // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    // VALU
+            __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);    // exponentials
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = mfma<DT>(v[1][i], p[1], o[i]);
+        t += kKeys;
+        ++tile;
+      };
+      while (true) {
+        step(std::integral_constant<int, 0>{}, s0, s1);
+        if (t >= j1) break;
+        step(std::integral_constant<int, 1>{}, s1, s0);
+        if (t >= j1) break;
       }
+    };
+    // Once more, with the values that are not finite kept apart: 32 channels at a time and one tile
+    // after the other (few registers, so that the code above keeps its own).
+    auto walk_odd = [&]() {
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        v16f part[1];
+        part[0] = 0.0f;
+        m = -INFINITY;
+        l = 0.0f;
+        unit_exp = -200;
+#pragma unroll 1
+        for (int t = j0; t < j1; t += kKeys) {
+          const Place at = place(t, page_of(t));
+          wait_lds_reads();
+          stage_barrier();
+          if constexpr (kCodes) {
+            Codes codes;
+            fetch(a.k, a.ks, at, codes);
+            put(codes, 0, kscale[0]);
+            fetch(a.v, a.vs, at, codes);
+            put(codes, 2, vscale[0]);
+          } else {
+            bring(a.k, a.kts, a.khs, koff, at, 0);
+            bring(a.v, a.vts, a.vhs, voff, at, 2);
+            wait_vmcnt<0>();
+          }
+          wait_lds_reads();
+          stage_barrier();
+          v16f s[2];
 #pragma unroll
-      for (int y = 0; y < D / 32; ++y)
-        if (y == x) o[y] = part[0];
-    }
+          for (int w = 0; w < 4; ++w) {
+            v8s k[kSteps / 2];
+            read_k(0, w, k);
+            score(w, k, s);
+          }
+          scale_scores(s, kscale[0]);
+          mask_scores(s, t);
+          follow_maximum(s, part);
+          const float mb = m == -INFINITY ? 0.0f : m, unit_inv = follow_scales(vscale[0], part);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) part[0] = mfma_odd<DT>(read_v1(0, w, x), weigh(std::true_type{}, s, w, mb, unit_inv, vscale[0]), part[0]);
+        }
+#pragma unroll
+        for (int y = 0; y < D / 32; ++y)
+          if (y == x) o[y] = part[0];
+      }
+    };
+    if constexpr (ODD) walk_odd();
+    else walk();
   };
-  if constexpr (ODD) walk_odd();
-  else walk();
-  };   // pass
   pass(std::false_type{}, lane);
   bool fine = true;
 #pragma unroll

@@ -245,6 +245,16 @@ def test_paged_long(dtype, e4m3):
     run_paged([5000], [2], 2, 2, 64, 16, dtype, e4m3)
 
 
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("dim,window", [(64, 0), (128, 0), (64, 300)])
+@pytest.mark.parametrize("many", [False, True])
+def test_paged_mixed(many, dim, window, dtype, e4m3):
+    """Single tokens next to chunks of several tiles of rows; in one wave's lanes and over 64 requests."""
+    lens = [3000, 1, 900, 40, 128, 2000, 17, 1, 64, 333, 1500, 256] * (7 if many else 1)
+    new = [100, 1, 1, 1, 1, 3, 1, 1, 0, 1, 17, 1] * (7 if many else 1)
+    run_paged(lens, new, 8, 2, dim, 16, dtype, e4m3, window=window)   # 43 rows a request on average, 400 at most
+
+
 @pytest.mark.parametrize("max_new", [0, 1, 64, 4096])
 def test_paged_hint_changes_no_meaning(max_new):
     run_paged([100, 300, 64], [1, 130, 0], 8, 2, 128, 16, "bf16", False, max_new=max_new)
