@@ -385,7 +385,11 @@ __device__ __forceinline__ int64_t partial_at(int row, int quad) {
 // keys, numbered request by request, the tiles that see the most first.  A full batch of equal
 // lengths stays uncut.  A second launch joins the partial results: 128 rows of them are too much for
 // one workgroup at the end of the first (measured: 2 tiles a head over 100000 keys 406 us that way).
-constexpr int kUnits = 512;
+// One unit a CU rather than the two that fit, since a partial result of 128 rows is 64 KB to write and
+// to read: 512 and 256 units take 569 and 535 us for 4 x 1024 tokens over up to 16000 keys, 111 and 101
+// for 16 over 100000, 54 and 50 for 16 x 64 over up to 4096; 192 take 528, 111 and 53.  Pieces of at
+// least 512 keys: 24 mixed requests of up to 2000 keys, e4m3, 31 us; with 256 35, with 1024 38.
+constexpr int kUnits = 256;
 constexpr int kMinTileKeys = 512;
 // Units per key head are at most the tiles and this many more, and partial results at most twice it.
 __host__ __device__ constexpr int64_t extra_units(int64_t hk) { return (kUnits + hk - 1) / hk; }
