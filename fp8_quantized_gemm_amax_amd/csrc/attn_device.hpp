@@ -156,7 +156,7 @@ __device__ __forceinline__ v4i key_rows(const AttnArgs& a, const Rows& r, const 
 // cut is made there: every workgroup sums the batch's work (three integers a request).
 constexpr int kMaxSplitBatch = 1024;   // above, there is enough to do without cuts
 constexpr int kMaxSplitHeads = 1024;
-constexpr int kMinKeys = 256;          // no piece below: a piece's start and end cost about that
+constexpr int kMinKeys = 256;          // no piece below (one request of 701 keys, 32 heads: 128, 256, 512 keys 11.2, 11.3, 17.3 us)
 constexpr int kMaxSlots = 4096;        // partial results of a launch
 
 struct Unit {
@@ -309,7 +309,8 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int i, const Request&
 // Packed prompts of up to 64 requests: tile `rank` of them all in the order of their index in their
 // request, the last first, so that the tiles that see the most keys start first whatever request
 // they are of (hardware starts workgroups in order).  Up to kSlots workgroups are all on the card at
-// once, two to a CU: there the second of a CU is the lightest left, not the next.
+// once, two to a CU: there the second of a CU is the lightest left, not the next.  12 prompts of up to
+// 2048 tokens: 68.4 us so, 73.2 in the order of the requests.
 constexpr int kSlots = 512;
 template <int SIZE>
 __device__ __forceinline__ bool find_ranked(const AttnArgs& a, Unit& u) {
@@ -454,7 +455,9 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
 }
 
 // The cut for few rows, where the keys are read once and every step costs the same: the batch's
-// steps in one line, an equal stretch for each of kFewGroups workgroups (two to a CU).
+// steps in one line, an equal stretch for each of kFewGroups workgroups (two to a CU: with 256, 512
+// and 1024 the 64-request e4m3 batch takes 91.5, 75.6 and 83.7 us, 4 requests of up to 131072 keys 174,
+// 182 and 192).
 constexpr int kFewGroups = 512;
 static_assert(2 * kFewGroups <= kMaxSlots, "partial results of the cut for few rows");
 

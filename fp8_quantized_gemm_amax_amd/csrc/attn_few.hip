@@ -1,7 +1,17 @@
-// attn_few.hip - attention over a paged cache for at most 32 packed rows a request and key head
-// (single tokens, short drafts): the keys are the work.  A workgroup of four waves takes one unit of
-// keys; each wave walks over its own tiles of them, through its own LDS without a barrier, for all
-// rows, and the four results are joined in LDS at the end.
+// attn_few.hip - attention over a paged cache for few packed rows a request and key head (single
+// tokens, short drafts, and such next to some chunks), 32 rows at a time: the keys are the work.
+//   m' = max(m, max_j s_j), l' = 2^(m - m') l + sum_j 2^(s_j - m'), o' = 2^(m - m') o + sum_j 2^(s_j - m') v_j
+// over tiles of keys, s_j = scale log2(e) q.k_j, and out = o / l, all float32; a weight is rounded to
+// 16 bits for its product with v.  A workgroup of four waves takes one unit of keys; each wave walks
+// over its own tiles of them, through its own LDS without a barrier, for all rows, and the four
+// results are joined in LDS at the end.  K of the next tile is under way while V of this one is
+// multiplied, V while the next scores are: 16 KB a wave, two workgroups a CU, so 128 KB of reads in
+// flight a CU.
+// Long caches are bound by HBM: 4 requests of up to 131072 keys, 8 heads of 128 in bf16, 977 MB,
+// take 181 us (5.4 TB/s; a copy of 2 GiB reaches 4.8, reads and writes together); 64 e4m3 requests of
+// up to 8192 keys, 322 MB, 74 us (4.4 TB/s).  Short ones are bound by a chain of dependent reads of 1
+// to 2 us each (lengths, table, K and V, partial results): one request of 701 keys, 32 heads of 128,
+// 11.5 MB, takes 11.5 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
