@@ -398,11 +398,11 @@ static_assert(2 * (kUnits + kMaxSplitHeads) <= kMaxSlots, "partial results of th
 
 // Unit `block` of the launch (block = unit * hk + head).  `lds`: 4 * (kMaxSplitBatch + 4) bytes, free
 // again on return.  False where there is none.
-template <int SIZE, bool PAGED>
+template <int SIZE>
 __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds, Unit& u) {
   u.head = block % a.hk;
   const int unit = block / a.hk;
-  Sums<PAGED> sums(a, lds);
+  Sums<true> sums(a, lds);
   sums.make(a, [&](const Request& q) {
     const Shape s = shape_of<SIZE>(a, q, kKeys);
     return s.tiles * s.steps;

@@ -35,8 +35,11 @@ constexpr float kSlack = 8.0f;
 // The workgroup's unit: cut from the batch's work (find_unit) or a whole tile of rows.
 template <int SIZE, bool PAGED>
 __device__ __forceinline__ bool unit_of(const AttnArgs& a, bool split, char* lds, Unit& u) {
-  if (PAGED && split) return find_unit<SIZE, PAGED>(a, blockIdx.x, reinterpret_cast<int*>(lds), u);
-  if (!PAGED && a.batch <= 64) return find_ranked<SIZE>(a, u);
+  if constexpr (PAGED) {
+    if (split) return find_unit<SIZE>(a, blockIdx.x, reinterpret_cast<int*>(lds), u);
+  } else {
+    if (a.batch <= 64) return find_ranked<SIZE>(a, u);
+  }
   u.head = blockIdx.x % a.hk;
   // heavy tiles first: a prompt's last rows see the most keys
   if (!find_rows(a, gridDim.x / a.hk - 1 - blockIdx.x / a.hk, SIZE, PAGED, u.r)) return false;
