@@ -99,14 +99,6 @@ __device__ __forceinline__ float add_halves(float x) {
   return __uint_as_float(a) + __uint_as_float(b);
 }
 
-// LDS DMA as dma16, with the wait states that the compiler does not insert for inline asm: one
-// between the write of m0 and the load (here), and five between a vector instruction's write of
-// the buffer's scalars (readfirstlane) and the load (settle, once per buffer).
-__device__ __forceinline__ void settle(v4i& rsrc) { asm volatile("s_nop 4" : "+s"(rsrc)); }
-__device__ __forceinline__ void dma16_safe(const v4i& rsrc, uint32_t lds, uint32_t voff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
-}
-
 // One request's part of a tile of rows (all uniform).
 struct Rows {
   int request, begin, tokens;   // its first packed token and its number of new tokens

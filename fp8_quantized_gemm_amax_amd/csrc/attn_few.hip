@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
         for (int x = 0; x < kPlanes; ++x)
 #pragma unroll
           for (int y = 0; y < kRowBytes / 64; ++y)
-            dma16_safe(rs, to + x * kPlaneBytes + g * 16 * kRowBytes + y * 1024, off[y] + x * 128);
+            dma16(rs, to + x * kPlaneBytes + g * 16 * kRowBytes + y * 1024, off[y] + x * 128);
       }
     };
     auto bring_scales = [&](const float* p, int t, const int (&pages)[kGroups], uint32_t to) {

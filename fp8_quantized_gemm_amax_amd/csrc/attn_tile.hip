@@ -118,7 +118,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int x = 0; x < kPlanes; ++x)
-          dma16_safe(rs, base + buffer * kTile + x * kPlane + (2 * wave + g) * 1024, off[g] + x * 128);
+          dma16(rs, base + buffer * kTile + x * kPlane + (2 * wave + g) * 1024, off[g] + x * 128);
     };
     // codes in flight: a lane's D / 4 bytes of one key and one scale
     struct Codes {

@@ -32,12 +32,17 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // written by an outstanding load and wait for every DMA in flight before each LDS read;
 // the kernel orders them itself (wait_vmcnt + barrier).  The instruction has no
 // destination registers, and its address operands are read when it issues.
+// The compiler inserts no wait states for inline asm.  The load needs one after the write of
+// m0, which the compiler may place directly before it: the s_nop.  It needs five after a
+// vector instruction's write of the buffer's scalars (make_rsrc's readfirstlane); a kernel
+// that forms a buffer right before its loads calls settle once for it.
 __device__ __forceinline__ void dma16(const v4i& rsrc, uint32_t lds, uint32_t voff) {
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void dma4(const v4i& rsrc, uint32_t lds, uint32_t voff) {
-  asm volatile("buffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
 }
+__device__ __forceinline__ void settle(v4i& rsrc) { asm volatile("s_nop 4" : "+s"(rsrc)); }
 
 // s_waitcnt with only the vector-memory counter constrained (gfx9 encoding: vmcnt in bits
 // 3:0 and 15:14, expcnt and lgkmcnt left at their maxima).
