@@ -30,9 +30,10 @@ constexpr int kRows = 32;
 // request of 500: 10.9 and 11.4.  At 768: 16 e4m3 requests of up to 700 keys, cut 11.9, whole 14.5.
 constexpr int kWholeKeys = 512;
 
-// One dword from `p` into LDS at lds + lane * 4, where `on` holds for the lane.
-__device__ __forceinline__ void dma4_lane(const float* p, uint32_t lds, bool on) {
-  if (on) asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+// One dword from `p` into LDS at to + lane where `on` holds for the lane, 0 where it does not.
+__device__ __forceinline__ void dma4_lane(const float* p, float* to, bool on) {
+  if (on) asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds_addr(to)) : "memory");
+  else to[threadIdx.x & 63] = 0.0f;
 }
 
 template <int DT, int D, int SRC>
@@ -56,10 +57,6 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   const uint32_t kbase = lds_addr(kt), vbase = kbase + kTile;
   float* const my_ks = scales[kCodes ? wave : 0][0];
   float* const my_vs = scales[kCodes ? wave : 0][1];
-  if constexpr (kCodes) {   // a lane without a key leaves its place as it was
-    my_ks[lane] = my_vs[lane] = 0.0f;
-    wait_lds_reads();
-  }
 
   // Chunk of 16 bytes at position x of key row i in LDS; rows of 64 bytes hold four.
   auto chunk_of = [](int x, int i) { return kRowBytes == 128 ? x ^ gemm::swz(i & 15) : x ^ ((i >> 1) & 3); };
@@ -97,7 +94,8 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
             dma16(rs, to + x * kPlaneBytes + g * 16 * kRowBytes + y * 1024, off[y] + x * 128);
       }
     };
-    auto bring_scales = [&](const float* p, int t, const int (&pages)[kGroups], uint32_t to) {
+    // The scales of a tile's keys; 0 where there is no key or its page is not in the cache, whose codes read as 0 too.
+    auto bring_scales = [&](const float* p, int t, const int (&pages)[kGroups], float* to) {
       int page = pages[0];
 #pragma unroll
       for (int g = 1; g < kGroups; ++g) {   // as a value of its own: a choice of addresses would put the array into memory
@@ -129,9 +127,9 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t + 16 * g);
       if (t < j1) {
-        if constexpr (kCodes) bring_scales(a.ks, t, pages, lds_addr(my_ks));
+        if constexpr (kCodes) bring_scales(a.ks, t, pages, my_ks);
         bring(a.k, t, pages, kbase);
-        if constexpr (kCodes) bring_scales(a.vs, t, pages, lds_addr(my_vs));
+        if constexpr (kCodes) bring_scales(a.vs, t, pages, my_vs);
         bring(a.v, t, pages, vbase);
       }
       for (; t < j1; t += 4 * kTileKeys) {
@@ -168,7 +166,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
         }
         wait_lds_reads();
         if (t1 < j1) {
-          if constexpr (kCodes) bring_scales(a.ks, t1, pages, lds_addr(my_ks));
+          if constexpr (kCodes) bring_scales(a.ks, t1, pages, my_ks);
           bring(a.k, t1, pages, kbase);
         }
         if (t + kTileKeys - 1 > first_pos || (a.window > 0 && t < last_pos - a.window + 1)) {
@@ -271,7 +269,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
         }
         wait_lds_reads();
         if (t1 < j1) {
-          if constexpr (kCodes) bring_scales(a.vs, t1, pages, lds_addr(my_vs));
+          if constexpr (kCodes) bring_scales(a.vs, t1, pages, my_vs);
           bring(a.v, t1, pages, vbase);
         }
       }
