@@ -67,6 +67,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else return __builtin_bit_cast(uint32_t, v2h{static_cast<_Float16>(lo), static_cast<_Float16>(hi)});
 }
 
+template <int DT>
+__device__ __forceinline__ v8s pack8(const float (&x)[8]) {
+  return __builtin_bit_cast(v8s, v4u{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
+}
+
 // Eight e4m3 codes as 16-bit values (exact: both types hold every code).
 template <int DT>
 __device__ __forceinline__ v4u codes8(uint32_t lo, uint32_t hi) {
@@ -80,6 +85,28 @@ __device__ __forceinline__ v4u codes8(uint32_t lo, uint32_t hi) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true)),
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false)),
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true))};
+}
+
+// fp16 queries over an e4m3 cache.  A weight times its value's scale can lie far outside fp16's range,
+// next to another key's above all, so the scale is split into 2^e and the rest: the power of two goes
+// to the codes, where it is exact for -14 <= e <= 7 (every code times it is an fp16 number), and the
+// rest, 1 to 2 for a scale in that range, to the weight.  So the values are what an fp16 cache would
+// hold, no key's scale touches another's product, and a rest or a product beyond fp16 shows as an
+// output that is not finite.
+constexpr bool splits_scale(int dt, bool codes) { return codes && dt == DT_F16; }
+struct SplitScale {
+  float power, rest;
+};
+__device__ __forceinline__ SplitScale split_scale(float scale) {
+  const uint32_t e = min(max((__float_as_uint(scale) >> 23) & 0xff, 127u - 14), 127u + 7);
+  return {__uint_as_float(e << 23), scale * __uint_as_float((254 - e) << 23)};
+}
+// Eight e4m3 codes times a power of two as fp16 values.
+__device__ __forceinline__ v4u codes8_times(uint32_t lo, uint32_t hi, float power) {
+  return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, power, false)),
+             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, power, true)),
+             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, false)),
+             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, true))};
 }
 
 // {a of lane l % 32, b of lane l % 32} in the low and high half, and the same of lanes 32-63.
@@ -596,15 +623,49 @@ struct Odd {
   }
 };
 
-template <int DT>
-__device__ __forceinline__ v16f mfma_odd(const v8s& v, const v8s& p, v16f o) {
+// Eight fp16 values of few bits (codes times powers of two) as bf16.
+__device__ __forceinline__ v8s as_bf16(const v8s& x) {
+  const v8h h = __builtin_bit_cast(v8h, x);
+  v8bf r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = static_cast<__bf16>(static_cast<float>(h[i]));
+  return __builtin_bit_cast(v8s, r);
+}
+
+// The product of eight keys' values v with their weights z, of type DT.  SPLIT (fp16): weights beyond
+// fp16's range are taken out of it, and multiplied as two bf16, their rounding and what it left.
+template <int DT, bool SPLIT>
+__device__ __forceinline__ v16f mfma_odd(const v8s& v, const float (&z)[8], v16f o) {
+  float x[8];
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool in = !SPLIT || z[i] < 65520.0f;     // rounds to an fp16 number; false for NaN
+    x[i] = in ? z[i] : 0.0f;
+    any |= !in;
+  }
+  const v8s p = pack8<DT>(x);
   o = mfma<DT>(Odd<DT>::without(v), p, o);
-  const v8s w = Odd<DT>::seen(p);
+  v8s seen = Odd<DT>::seen(p);
+  if (SPLIT && __any(any)) {
+    float big[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) big[i] = z[i] < 65520.0f ? 0.0f : z[i];
+    const v8s w = as_bf16(Odd<DT>::without(v)), near = pack8<DT_BF16>(big);
+    seen |= Odd<DT>::seen(near);
+    o = mfma<DT_BF16>(w, near, o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = static_cast<float>(__builtin_bit_cast(v8bf, near)[i]);
+      big[i] = __builtin_isfinite(y) ? big[i] - y : 0.0f;
+    }
+    o = mfma<DT_BF16>(w, pack8<DT_BF16>(big), o);
+  }
 #pragma unroll 1
   for (int kind = 0; kind < 3; ++kind) {
     v16f n;
     n = 0.0f;
-    n = mfma<DT>(Odd<DT>::is(v, kind), w, n);
+    n = mfma<DT>(Odd<DT>::is(v, kind), seen, n);
     const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __uint_as_float(kCanonicalNaN);
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] += n[i] > 0.0f ? add : 0.0f;

@@ -38,7 +38,7 @@ __device__ __forceinline__ void dma4_lane(const float* p, float* to, bool on) {
 
 template <int DT, int D, int SRC>
 __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split) {
-  constexpr bool kCodes = SRC == SRC_E4M3, kRange = kCodes && DT == DT_F16;
+  constexpr bool kCodes = SRC == SRC_E4M3, kSplit = splits_scale(DT, kCodes);
   constexpr int kTileKeys = !kCodes && D == 128 ? 32 : 64;   // keys a wave takes at a time: 8 KB of K (4: codes of 64 channels)
   constexpr int kSub = kTileKeys / 32, kGroups = kTileKeys / 16, kSteps = D / 16;
   constexpr int kRowBytes = kCodes && D == 64 ? 64 : 128;    // of a key in a plane
@@ -48,6 +48,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
   static_assert(kJoinBytes <= 8 * kTile, "the join's LDS");
   __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * kTile];
   __shared__ __attribute__((aligned(16))) float scales[kCodes ? 4 : 1][2][64];
+  __shared__ __attribute__((aligned(16))) _Float16 powers[kSplit ? 4 : 1][64];
   __shared__ float stats[2][4][32];
   __shared__ int ends[kMaxSplitBatch + 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -114,12 +115,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
     const float c = a.scale * kLog2e;
     v16f o[D / 32];
     float m, l;
-    int unit_exp;
     auto walk = [&](auto odd_c) {
       constexpr bool ODD = decltype(odd_c)::value;
       m = -INFINITY;
       l = 0.0f;
-      unit_exp = -200;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
       int pages[kGroups];
@@ -136,7 +135,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
         const int t1 = t + 4 * kTileKeys;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) pages[g] = page_of(t1 + 16 * g);
-        wait_vmcnt<kDma>();      // K is there: at least the DMAs of V came after it
+        wait_vmcnt<kDma>();      // K and the scales are there: at least the DMAs of V came after them
         asm volatile("" ::: "memory");
         v16f s[kSub];
 #pragma unroll
@@ -168,6 +167,11 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
         if (t1 < j1) {
           if constexpr (kCodes) bring_scales(a.ks, t1, pages, my_ks);
           bring(a.k, t1, pages, kbase);
+        }
+        if constexpr (kSplit) {
+          const SplitScale y = split_scale(my_vs[lane]);
+          my_vs[lane] = y.rest;
+          powers[wave][lane] = static_cast<_Float16>(y.power);
         }
         if (t + kTileKeys - 1 > first_pos || (a.window > 0 && t < last_pos - a.window + 1)) {
           const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
@@ -205,47 +209,26 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
         if (t1 < j1) wait_vmcnt<kDma>();
         else wait_vmcnt<0>();
         asm volatile("" ::: "memory");
-        if constexpr (kCodes) {
-          float unit_inv = 1.0f;
-          if constexpr (kRange) {
-            float most = 0.0f;
-#pragma unroll
-            for (int u = 0; u < kSub; ++u)
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const v4f x = *reinterpret_cast<const v4f*>(my_vs + 32 * u + 8 * g + 4 * half);
-                most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
-              }
-            most = max_halves(most);
-            const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
-            if (e > unit_exp) {
-              const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
-              unit_exp = e;
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[i][x] *= keep;
-            }
-            unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
-          }
-#pragma unroll
-          for (int u = 0; u < kSub; ++u)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const v4f x = *reinterpret_cast<const v4f*>(my_vs + 32 * u + 8 * g + 4 * half);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float z = s[u][4 * g + y] * (kRange ? x[y] * unit_inv : x[y]);
-                s[u][4 * g + y] = ODD && s[u][4 * g + y] == 0.0f ? 0.0f : z;
-              }
-            }
-        }
 #pragma unroll
         for (int w = 0; w < kTileKeys / 16; ++w) {
-          v4u x;
+          float z[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = pack2<DT>(s[w / 2][8 * (w & 1) + 2 * i], s[w / 2][8 * (w & 1) + 2 * i + 1]);
-          const v8s p = __builtin_bit_cast(v8s, x);
+          for (int i = 0; i < 8; ++i) z[i] = s[w / 2][8 * (w & 1) + i];
+          if constexpr (kCodes) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const v4f x = *reinterpret_cast<const v4f*>(my_vs + 16 * w + 8 * g + 4 * half);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) z[4 * g + y] = ODD && z[4 * g + y] == 0.0f ? 0.0f : z[4 * g + y] * x[y];
+            }
+          }
+          const v8s p = pack8<DT>(z);
+          v8h power;
+          if constexpr (kSplit) {
+            typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+            power = __builtin_shufflevector(*reinterpret_cast<const v4h*>(powers[wave] + 16 * w + 4 * half),
+                                            *reinterpret_cast<const v4h*>(powers[wave] + 16 * w + 4 * half + 8), 0, 1, 2, 3, 4, 5, 6, 7);
+          }
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             v8s v;
@@ -255,6 +238,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
               const char* at = vt + key * kRowBytes + (chunk_of(2 * i + vdsub, key) << 4) + (lane & 1) * 8;
               const v2i y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)at);
               v = __builtin_bit_cast(v8s, codes8<DT>(y[0], y[1]));
+              if constexpr (kSplit) v = __builtin_bit_cast(v8s, __builtin_bit_cast(v8h, v) * power);
             } else {
               const int chunk = (i & 1) * 4 + vdsub * 2 + ((lane & 3) >> 1);
               const char* at = vt + (i / 2) * kPlaneBytes + (lane & 1) * 8;
@@ -263,7 +247,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
               const v4s z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k1 * 128 + (chunk_of(chunk, k1) << 4)));
               v = __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7);
             }
-            if constexpr (ODD) o[i] = mfma_odd<DT>(v, p, o[i]);
+            if constexpr (ODD) o[i] = mfma_odd<DT, kSplit>(v, z, o[i]);
             else o[i] = mfma<DT>(v, p, o[i]);
           }
         }
@@ -274,12 +258,6 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
         }
       }
       l = add_halves(l);
-      if constexpr (kRange) {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) o[i][x] = __builtin_ldexpf(o[i][x], unit_exp);
-      }
       // join the four waves: wave w adds up channels 32 w .. 32 w + 31 and keeps them in o[0]
       __syncthreads();
 #pragma unroll

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool unit_of(const AttnArgs& a, bool split, char* lds
 template <int DT, int D, int SRC>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, bool split) {
   constexpr int kPlanes = D / 64, kTile = kPlanes * kPlane, kSteps = D / 16;
-  constexpr bool kPaged = SRC != SRC_PACKED, kCodes = SRC == SRC_E4M3, kRange = kCodes && DT == DT_F16;
+  constexpr bool kPaged = SRC != SRC_PACKED, kCodes = SRC == SRC_E4M3, kSplit = splits_scale(DT, kCodes);
   __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];   // K, K, V, V
   __shared__ __attribute__((aligned(16))) float kscale[kCodes ? 4 : 1][kKeys], vscale[kCodes ? 2 : 1][kKeys];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -64,7 +64,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
   const float c = a.scale * kLog2e;
   v16f o[D / 32];
   float m, l;     // running maximum (times c) and this lane's share of the sum
-  int unit_exp;   // kRange: o is in units of 2^unit_exp
 
   // Over the keys; ODD: again, with the values that are not finite kept apart.
   auto pass = [&](auto odd_c, const int lane) {
@@ -134,16 +133,27 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       for (int x = 0; x < kPlanes; ++x) to.c[x] = __builtin_amdgcn_raw_buffer_load_b128(rc, lane * (D / 4) + 16 * x, 0, 0);
       to.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(sp, 4), (lane & 15) * 4, 0, 0));
     };
-    auto put = [&](const Codes& from, int buffer, float* to_scale) {
+    auto put = [&](auto value, const Codes& from, int buffer, float* to_scale) {
+      constexpr bool SPLIT = kSplit && decltype(value)::value;   // a value's power of two goes to its codes
       const int key = 16 * wave + (lane >> 2);
+      float power = 1.0f, scale = from.s;
+      if constexpr (SPLIT) {
+        const SplitScale y = split_scale(scale);
+        scale = y.rest;
+        power = __shfl(y.power, lane >> 2);
+      }
+      auto widen = [&](uint32_t lo, uint32_t hi) -> v4u {
+        if constexpr (SPLIT) return codes8_times(lo, hi, power);
+        else return codes8<DT>(lo, hi);
+      };
 #pragma unroll
       for (int x = 0; x < kPlanes; ++x) {
         const int c = (lane & 3) * (D / 32) + 2 * x;       // first of the two chunks of eight channels
         char* to = lds + buffer * kTile + (c >> 3) * kPlane + key * 128;
-        *reinterpret_cast<v4u*>(to + (((c & 7) ^ gemm::swz(key & 15)) << 4)) = codes8<DT>(from.c[x][0], from.c[x][1]);
-        *reinterpret_cast<v4u*>(to + (((c & 7) + 1) ^ gemm::swz(key & 15)) * 16) = codes8<DT>(from.c[x][2], from.c[x][3]);
+        *reinterpret_cast<v4u*>(to + (((c & 7) ^ gemm::swz(key & 15)) << 4)) = widen(from.c[x][0], from.c[x][1]);
+        *reinterpret_cast<v4u*>(to + (((c & 7) + 1) ^ gemm::swz(key & 15)) * 16) = widen(from.c[x][2], from.c[x][3]);
       }
-      if (lane < 16) to_scale[16 * wave + lane] = from.s;
+      if (lane < 16) to_scale[16 * wave + lane] = scale;
     };
 
     // LDS addresses of this lane's operands
@@ -179,8 +189,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     };
 
     // The steps from a tile's scores to its weights: the keys' scales; the mask; the running maximum
-    // and what it rescales; (kRange) the unit of o and the factor to it; 16 keys' weights for the
-    // product with their values, and their share of the sum.
+    // and what it rescales; 16 keys' weights for the product with their values, and their share of
+    // the sum.
     auto scale_scores = [&](v16f (&s)[2], const float* scale) {
       if constexpr (kCodes) {
 #pragma unroll
@@ -222,37 +232,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           for (int x = 0; x < 16; ++x) o[i][x] *= keep;
       }
     };
-    auto follow_scales = [&](const float* scale, auto& o) -> float {
-      constexpr int kBlocks = sizeof(o) / sizeof(v16f);
-      float unit_inv = 1.0f;
-      if constexpr (kRange) {
-        // A weight's share of its value's scale, in units of a power of two at least the largest
-        // scale met, so that no product leaves fp16's range.
-        float most = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const v4f x = *reinterpret_cast<const v4f*>(scale + 32 * u + 8 * g + 4 * half);
-            most = fmaxf(fmaxf(fmaxf(most, x[0]), fmaxf(x[1], x[2])), x[3]);
-          }
-        most = max_halves(most);
-        const int e = min(max(__builtin_amdgcn_frexp_expf(most), -120), 120);
-        if (e > unit_exp) {      // the same in every lane: the scales are
-          const float keep = __builtin_ldexpf(1.0f, max(unit_exp - e, -200));
-          unit_exp = e;
-#pragma unroll
-          for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[i][x] *= keep;
-        }
-        unit_inv = __builtin_ldexpf(1.0f, -unit_exp);
-      }
-      return unit_inv;
-    };
-    auto weigh = [&](auto odd_c, const v16f (&s)[2], int w, float mb, float unit_inv, const float* scale) -> v8s {
+    auto weigh = [&](auto odd_c, const v16f (&s)[2], int w, float mb, const float* scale, float (&x)[8]) {
       constexpr bool ODD = decltype(odd_c)::value;
-      float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w / 2][8 * (w & 1) + i], c, -mb));
@@ -264,12 +245,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           const v4f y = *reinterpret_cast<const v4f*>(scale + 16 * w + 8 * g + 4 * half);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float z = x[4 * g + i] * (kRange ? y[i] * unit_inv : y[i]);
+            const float z = x[4 * g + i] * y[i];
             x[4 * g + i] = ODD && x[4 * g + i] == 0.0f ? 0.0f : z;
           }
         }
       }
-      return __builtin_bit_cast(v8s, v4u{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
     };
 
     // Over the keys once.  Tile i's weights are formed while the matrix unit multiplies tile i + 1's
@@ -277,7 +257,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     auto walk = [&]() {
       m = -INFINITY;
       l = 0.0f;
-      unit_exp = -200;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
       if (j0 >= j1) return;
@@ -291,9 +270,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
         fetch(a.k, a.ks, at0, first);
         fetch(a.k, a.ks, at1, ck);
         fetch(a.v, a.vs, at0, cv);
-        put(first, 0, kscale[0]);
-        put(ck, 1, kscale[kCodes ? 1 : 0]);
-        put(cv, 2, vscale[0]);
+        put(std::false_type{}, first, 0, kscale[0]);
+        put(std::false_type{}, ck, 1, kscale[kCodes ? 1 : 0]);
+        put(std::true_type{}, cv, 2, vscale[0]);
         const Place at2 = place(j0 + 2 * kKeys, page);
         fetch(a.k, a.ks, at2, ck);
         fetch(a.v, a.vs, at1, cv);
@@ -320,8 +299,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
         if constexpr (!kCodes) wait_vmcnt<0>();
         stage_barrier();
         if constexpr (kCodes) {
-          put(ck, B, kscale[kCodes ? (tile + 2) & 3 : 0]);
-          put(cv, 2 + (B ^ 1), vscale[kCodes ? B ^ 1 : 0]);
+          put(std::false_type{}, ck, B, kscale[kCodes ? (tile + 2) & 3 : 0]);
+          put(std::true_type{}, cv, 2 + (B ^ 1), vscale[kCodes ? B ^ 1 : 0]);
           const Place at = place(t + 3 * kKeys, page);
           fetch(a.k, a.ks, at, ck);
           fetch(a.v, a.vs, at1, cv);
@@ -340,13 +319,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
         mask_scores(s, t);
         follow_maximum(s, o);
         const float mb = m == -INFINITY ? 0.0f : m;
-        const float unit_inv = follow_scales(vscale[kCodes ? B : 0], o);
         v8s p[2];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {      // 16 keys
           if (w < 3) read_k(B ^ 1, w + 1, k[(w + 1) & 1]);
           read_v(B, w, v[w & 1]);
-          p[w & 1] = weigh(std::false_type{}, s, w, mb, unit_inv, vscale[kCodes ? B : 0]);
+          float z[8];
+          weigh(std::false_type{}, s, w, mb, vscale[kCodes ? B : 0], z);
+          p[w & 1] = pack8<DT>(z);
           score(w, k[w & 1], next);
           if (w > 0) {
 #pragma unroll
@@ -382,8 +362,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
         part[0] = 0.0f;
         m = -INFINITY;
         l = 0.0f;
-        unit_exp = -200;
-#pragma unroll 1
+  #pragma unroll 1
         for (int t = j0; t < j1; t += kKeys) {
           const Place at = place(t, page_of(t));
           wait_lds_reads();
@@ -391,9 +370,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           if constexpr (kCodes) {
             Codes codes;
             fetch(a.k, a.ks, at, codes);
-            put(codes, 0, kscale[0]);
+            put(std::false_type{}, codes, 0, kscale[0]);
             fetch(a.v, a.vs, at, codes);
-            put(codes, 2, vscale[0]);
+            put(std::true_type{}, codes, 2, vscale[0]);
           } else {
             bring(a.k, a.kts, a.khs, koff, at, 0);
             bring(a.v, a.vts, a.vhs, voff, at, 2);
@@ -411,9 +390,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           scale_scores(s, kscale[0]);
           mask_scores(s, t);
           follow_maximum(s, part);
-          const float mb = m == -INFINITY ? 0.0f : m, unit_inv = follow_scales(vscale[0], part);
+          const float mb = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) part[0] = mfma_odd<DT>(read_v1(0, w, x), weigh(std::true_type{}, s, w, mb, unit_inv, vscale[0]), part[0]);
+          for (int w = 0; w < 4; ++w) {
+            float z[8];
+            weigh(std::true_type{}, s, w, mb, vscale[0], z);
+            part[0] = mfma_odd<DT, kSplit>(read_v1(0, w, x), z, part[0]);
+          }
         }
 #pragma unroll
         for (int y = 0; y < D / 32; ++y)
@@ -438,12 +421,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
   const int row = min(r.row0 + 32 * wave + col, r.rows - 1), tok = row / a.group, pos = r.pos0 + tok;
 
   l = add_halves(l);
-  if constexpr (kRange) {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) o[i][x] = __builtin_ldexpf(o[i][x], unit_exp);
-  }
   const int64_t out_row = static_cast<int64_t>(r.begin + tok) * a.hq + h * a.group + (row - tok * a.group);
   const bool store = r.row0 + 32 * wave + col < r.rows;
   if (kPaged && unit.count > 1) {      // a partial result: maximum, sum and output as they are

@@ -92,7 +92,9 @@ fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t
  *   softmax_scale : finite and > 0.
  *   window : 0 (none; 2^30 or more is none too) or the number of keys a query sees at most.
  * Scores, the running maximum and sum, and the output accumulate in float32; the weights are
- * rounded to dt for the product with v, and the result once to dt.
+ * rounded to dt for the product with v, and the result once to dt.  Over a cache in FP8_KV_E4M3 a
+ * key's scale multiplies its score in float32, and a value's scale its weight before that rounding;
+ * with fp16 the scale's power of two, from 2^-14 to 2^7, multiplies the codes instead, exactly.
  */
 fp8_status_t fp8_attn_prompt(const void* q, const void* k, const void* v, fp8_dtype_t dt, int64_t tokens,
                              const int32_t* cu_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads,

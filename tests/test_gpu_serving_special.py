@@ -82,3 +82,98 @@ def test_requests_whose_value_scales_lie_far_apart(dim, dtype):
         alone = fp8.fp8_attn_paged(q[r:r + 1], *args, cache.dev_table[r:r + 1, :13].contiguous(), cache.dev_lens[r:r + 1], cu_of([1]),
                                    cache.ks, cache.vs, max_new=1)
         assert torch.equal(out[r:r + 1], alone), r
+
+
+# ------------------------------------------------------------- fp16 queries over e4m3 value scales
+
+def few_or_many(many):
+    """New tokens of one request: rows that go to the kernel for few (4 a token and key head) and for many."""
+    return 90 if many else 6
+
+
+def paged(cache, q, new, **kw):
+    return fp8.fp8_attn_paged(q, cache.k, cache.v, cache.dev_table, cache.dev_lens, cu_of(new), cache.ks, cache.vs, max_new=max(new), **kw)
+
+
+def check_request(cache, q, out, dim, window=0, dtype="f16"):
+    """One request's rows, each against the values it sees.  The weights carry 16 bits in float32's range, so nothing in
+    the bound goes by the largest value (vmax 0)."""
+    kk, vv = cache.request("k", 0), cache.request("v", 0)
+    ref = attention_ref(f64_of(q), kk, vv, len(kk) - len(q), 1 / math.sqrt(dim), window)
+    check_rows(out, None, ref, dtype, len(kk), dim, 0.0, "request", rel=False)
+    for i in range(len(q)):      # row by row as well, since their sizes may differ; 2^-25: half the spacing of fp16's smallest
+        w = ref[0][i]
+        assert np.linalg.norm(f64_of(out[i]) - w) <= 2 * 2.0 ** -11 * np.linalg.norm(w) + math.sqrt(w.size) * 2.0 ** -25, i
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("length", [130, 1500])
+def test_a_late_value_of_large_scale_reaches_only_its_rows(length, many, dim):
+    """The last new token's value scale is 2^18 times the others': the rows before it keep their bits and their exactness."""
+    new = few_or_many(many)
+    cache = Cache([length], 2, dim, 16, "f16", True, 11)
+    cache.vs *= 2.0 ** -10
+    q = normal((new, 8, dim), "f16", 12)
+    before = paged(cache, q, [new])
+    set_row(cache, "v", 0, length - 1, scale=cache.vs[int(cache.table[0, (length - 1) // 16]), :, (length - 1) % 16] * 2.0 ** 18)
+    reread(cache)
+    out = paged(cache, q, [new])
+    assert torch.equal(out[:-1], before[:-1])
+    check_request(cache, q, out, dim)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 24, float("inf"), float("nan")])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
+def test_a_value_before_the_window_does_not_matter(many, dim, scale):
+    """A key that no row's window reaches, in a tile that some of their keys share."""
+    new, window = few_or_many(many), 40
+    cache = Cache([230], 2, dim, 16, "f16", True, 13)
+    cache.vs *= 2.0 ** -14
+    reread(cache)
+    q = normal((new, 8, dim), "f16", 14)
+    before = paged(cache, q, [new], window=window)
+    set_row(cache, "v", 0, 230 - new - window, scale=scale)
+    assert torch.equal(paged(cache, q, [new], window=window), before)
+    check_request(cache, q, before, dim, window)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("zero", [False, True])
+def test_a_seen_value_of_large_scale_and_no_weight(zero, many, dim):
+    """Seen by every row: a value row of zeros, whose scale is 1, among values of scale 2^-14; or a value whose scale is
+    2^20 times the others' under a key whose weight all but vanishes."""
+    new = few_or_many(many)
+    cache = Cache([150], 2, dim, 16, "f16", True, 15)
+    cache.vs *= 2.0 ** -14
+    q = normal((new, 8, dim), "f16", 16, 0.1)
+    if zero:
+        set_row(cache, "v", 0, 7, codes=0, scale=1.0)
+    else:   # a key against the queries' common part: score about -25
+        q = q + torch.ones(dim, dtype=q.dtype, device=DEV)
+        set_row(cache, "k", 0, 7, codes=0xB8, scale=25.0 / math.sqrt(dim))      # 0xB8: -1
+        set_row(cache, "v", 0, 7, scale=2.0 ** 6)
+    reread(cache)
+    check_request(cache, q, paged(cache, q, [new]), dim)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("length", [130, 1500])
+def test_value_scales_beyond_fp16(length, many, dim):
+    """Scales up to 2^24 whose codes are small enough for fp16 outputs (a cache that bf16 rows were appended to): at two
+    places that every row sees, and at the last token, which reaches only its own row."""
+    new = few_or_many(many)
+    cache = Cache([length], 2, dim, 16, "f16", True, 17)
+    q = normal((new, 8, dim), "f16", 18)
+    small = torch.arange(dim, device=DEV).remainder(8).to(torch.uint8) | torch.arange(dim, device=DEV).remainder(3).eq(0).to(torch.uint8) * 0x80
+    set_row(cache, "v", 0, 7, codes=small, scale=2.0 ** 21)          # codes of up to 7 / 512
+    set_row(cache, "v", 0, 33, codes=small.flip(0), scale=2.0 ** 22)
+    before = paged(cache, q, [new])
+    set_row(cache, "v", 0, length - 1, codes=small, scale=2.0 ** 24)
+    reread(cache)
+    out = paged(cache, q, [new])
+    assert torch.equal(out[:-1], before[:-1])
+    check_request(cache, q, out, dim)
