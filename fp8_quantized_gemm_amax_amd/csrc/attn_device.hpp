@@ -593,8 +593,8 @@ __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, 
 // Values that are not finite.  The product with v multiplies a masked key's value by a weight of
 // zero, which is right unless that value is infinite or NaN.  A workgroup with a result that is not
 // finite goes over its keys once more: such values enter the product as zeros, so rows that do not
-// see them get the bits they would have had, and rows whose weight for them is not zero get what
-// they hold added afterwards.
+// see them get the bits they would have had, and rows that see them, however small the weight, get
+// what they hold added afterwards.
 template <int DT>
 struct Odd {
   static constexpr short kExp = DT == DT_BF16 ? 0x7f80 : 0x7c00;
@@ -615,10 +615,11 @@ struct Odd {
     for (int i = 0; i < 8; ++i) r[i] = (x[i] & kExp) == kExp ? 0 : x[i];
     return r;
   }
-  static __device__ __forceinline__ v8s seen(const v8s& p) {
+  // 1 where bit i of `seen` is set.
+  static __device__ __forceinline__ v8s ones(uint32_t seen) {
     v8s r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = (p[i] & 0x7fff) ? kOne : 0;
+    for (int i = 0; i < 8; ++i) r[i] = seen >> i & 1 ? kOne : 0;
     return r;
   }
 };
@@ -632,27 +633,25 @@ __device__ __forceinline__ v8s as_bf16(const v8s& x) {
   return __builtin_bit_cast(v8s, r);
 }
 
-// The product of eight keys' values v with their weights z, of type DT.  SPLIT (fp16): weights beyond
+// The product of eight keys' values v with their weights z, of type DT; bit i of `seen`: the row sees
+// key i (a weight is 0 where it does not).  SPLIT (fp16): weights beyond
 // fp16's range are taken out of it, and multiplied as two bf16, their rounding and what it left.
 template <int DT, bool SPLIT>
-__device__ __forceinline__ v16f mfma_odd(const v8s& v, const float (&z)[8], v16f o) {
+__device__ __forceinline__ v16f mfma_odd(const v8s& v, const float (&z)[8], uint32_t seen, v16f o) {
   float x[8];
   bool any = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const bool in = !SPLIT || z[i] < 65520.0f;     // rounds to an fp16 number; false for NaN
+    const bool in = !SPLIT || __builtin_fabsf(z[i]) < 65520.0f;     // rounds to an fp16 number; false for NaN
     x[i] = in ? z[i] : 0.0f;
     any |= !in;
   }
-  const v8s p = pack8<DT>(x);
-  o = mfma<DT>(Odd<DT>::without(v), p, o);
-  v8s seen = Odd<DT>::seen(p);
+  o = mfma<DT>(Odd<DT>::without(v), pack8<DT>(x), o);
   if (SPLIT && __any(any)) {
     float big[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) big[i] = z[i] < 65520.0f ? 0.0f : z[i];
+    for (int i = 0; i < 8; ++i) big[i] = __builtin_fabsf(z[i]) < 65520.0f ? 0.0f : z[i];
     const v8s w = as_bf16(Odd<DT>::without(v)), near = pack8<DT_BF16>(big);
-    seen |= Odd<DT>::seen(near);
     o = mfma<DT_BF16>(w, near, o);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -661,11 +660,12 @@ __device__ __forceinline__ v16f mfma_odd(const v8s& v, const float (&z)[8], v16f
     }
     o = mfma<DT_BF16>(w, pack8<DT_BF16>(big), o);
   }
+  const v8s ones = Odd<DT>::ones(seen);
 #pragma unroll 1
   for (int kind = 0; kind < 3; ++kind) {
     v16f n;
     n = 0.0f;
-    n = mfma<DT>(Odd<DT>::is(v, kind), seen, n);
+    n = mfma<DT>(Odd<DT>::is(v, kind), ones, n);
     const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __uint_as_float(kCanonicalNaN);
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] += n[i] > 0.0f ? add : 0.0f;

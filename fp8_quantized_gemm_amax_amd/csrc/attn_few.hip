@@ -183,6 +183,11 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
               s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
             }
         }
+        uint32_t seen = 0;      // ODD: the keys that this lane's row sees
+        if constexpr (ODD) {
+#pragma unroll
+          for (int i = 0; i < 16 * kSub; ++i) seen |= (s[i / 16][i % 16] == -INFINITY ? 0u : 1u) << i;
+        }
         float top = s[0][0];
 #pragma unroll
         for (int i = 1; i < 16 * kSub; ++i) top = fmaxf(top, s[i / 16][i % 16]);
@@ -219,7 +224,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
             for (int g = 0; g < 2; ++g) {
               const v4f x = *reinterpret_cast<const v4f*>(my_vs + 16 * w + 8 * g + 4 * half);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) z[4 * g + y] = ODD && z[4 * g + y] == 0.0f ? 0.0f : z[4 * g + y] * x[y];
+              for (int y = 0; y < 4; ++y) z[4 * g + y] = ODD && !(seen >> (8 * w + 4 * g + y) & 1) ? 0.0f : z[4 * g + y] * x[y];
             }
           }
           const v8s p = pack8<DT>(z);
@@ -247,7 +252,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
               const v4s z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(at + k1 * 128 + (chunk_of(chunk, k1) << 4)));
               v = __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7);
             }
-            if constexpr (ODD) o[i] = mfma_odd<DT, kSplit>(v, z, o[i]);
+            if constexpr (ODD) o[i] = mfma_odd<DT, kSplit>(v, z, seen >> (8 * w), o[i]);
             else o[i] = mfma<DT>(v, p, o[i]);
           }
         }

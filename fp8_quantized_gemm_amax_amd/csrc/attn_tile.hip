@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float z = x[4 * g + i] * y[i];
-            x[4 * g + i] = ODD && x[4 * g + i] == 0.0f ? 0.0f : z;
+            x[4 * g + i] = ODD && s[w / 2][8 * (w & 1) + 4 * g + i] == -INFINITY ? 0.0f : z;
           }
         }
       }
@@ -395,7 +395,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           for (int w = 0; w < 4; ++w) {
             float z[8];
             weigh(std::true_type{}, s, w, mb, vscale[0], z);
-            part[0] = mfma_odd<DT, kSplit>(read_v1(0, w, x), z, part[0]);
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) seen |= (s[w / 2][8 * (w & 1) + i] == -INFINITY ? 0u : 1u) << i;
+            part[0] = mfma_odd<DT, kSplit>(read_v1(0, w, x), z, seen, part[0]);
           }
         }
 #pragma unroll

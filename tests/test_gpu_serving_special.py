@@ -177,3 +177,118 @@ def test_value_scales_beyond_fp16(length, many, dim):
     out = paged(cache, q, [new])
     assert torch.equal(out[:-1], before[:-1])
     check_request(cache, q, out, dim)
+
+
+# ------------------------------------------------- keys and values that are not finite, paged caches
+
+BAD = {"nan": float("nan"), "inf": float("inf"), "-inf": float("-inf")}
+KINDS = [("bf16", False), ("bf16", True), ("f16", False), ("f16", True)]
+
+
+def run_bits(cache, q, new, window=0):
+    out, lse = paged(cache, q, [new], window=window, return_lse=True)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def same(a, b):
+    """The same bits, NaN among them."""
+    return torch.equal(a.contiguous().view(torch.int16 if a.element_size() == 2 else torch.int32),
+                       b.contiguous().view(torch.int16 if b.element_size() == 2 else torch.int32))
+
+
+def spoil(cache, name, token, head, channel, what):
+    """Puts a value that is not finite into one head's row of a token: in a 16-bit cache one channel; in an e4m3 one the
+    code of NaN in one channel ("code"), or the row's scale."""
+    page, at = int(cache.table[0, token // cache.page]), token % cache.page
+    if not cache.e4m3:
+        getattr(cache, name)[page, head, at, channel] = BAD[what]
+    elif what == "code":
+        getattr(cache, name)[page, head, at, channel] = 0xFF
+    else:
+        getattr(cache, name + "s")[page, head, at] = BAD[what]
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("length", [130, 3000])
+def test_values_that_are_not_finite(length, many, dim, dtype, e4m3):
+    """A late token's value: the rows before it and the other key head keep their bits, the rows that see it get the IEEE
+    result.  130 keys are walked whole, 3000 are cut into pieces that are joined."""
+    new = few_or_many(many)
+    q = normal((new, 8, dim), dtype, 22)
+    for what in ("nan", "inf", "-inf") if not e4m3 else ("nan", "inf", "code"):
+        cache = Cache([length], 2, dim, 16, dtype, e4m3, 21)
+        good, good_lse = run_bits(cache, q, new)
+        at = length - 3
+        spoil(cache, "v", at, 1, 7, what)
+        out, lse = run_bits(cache, q, new)
+        assert same(lse, good_lse), what
+        assert same(out[:-3], good[:-3]) and same(out[:, :4], good[:, :4]), what
+        hit = out[-3:, 4:]
+        if e4m3 and what != "code":
+            codes = cache.v[int(cache.table[0, at // 16]), 1, at % 16].cpu()
+            want = torch.from_numpy(decode_e4m3(codes.numpy())).float() * BAD[what]
+            assert torch.equal(hit.float().cpu().nan_to_num(7.0, 8.0, -8.0), want.nan_to_num(7.0, 8.0, -8.0).expand(hit.shape)), what
+        else:
+            want = torch.full_like(hit[..., 7].float(), BAD["nan" if what == "code" else what])
+            assert torch.equal(hit[..., 7].float().nan_to_num(7.0, 8.0, -8.0), want.nan_to_num(7.0, 8.0, -8.0)), what
+            rest = [c for c in range(dim) if c != 7]
+            assert same(hit[..., rest], good[-3:, 4:][..., rest]), what
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_before_the_window_nothing_matters(name, many, dim, dtype, e4m3):
+    """A key or value that no row's window reaches, in a tile of keys that some of their windows share."""
+    new, window, length = few_or_many(many), 40, 230
+    q = normal((new, 8, dim), dtype, 26)
+    for what in ("nan", "inf", "-inf") if not e4m3 else ("nan", "inf", "code"):
+        cache = Cache([length], 2, dim, 16, dtype, e4m3, 25)
+        good, good_lse = run_bits(cache, q, new, window)
+        spoil(cache, name, length - new - window, 1, 7, what)
+        out, lse = run_bits(cache, q, new, window)
+        assert same(out, good) and same(lse, good_lse), what
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_a_value_that_is_not_finite_under_a_small_weight(bad, many, dtype, e4m3):
+    """A weight of e^-25 is 0 in fp16 and not in float32: the rows that see the value are not finite."""
+    new, dim = few_or_many(many), 64
+    q = normal((new, 8, dim), dtype, 28, 0.1) + torch.ones(dim, dtype=torch.bfloat16 if dtype == "bf16" else torch.float16, device=DEV)
+    cache = Cache([150], 2, dim, 16, dtype, e4m3, 27)
+    page = int(cache.table[0, 0])
+    if e4m3:
+        cache.k[page, :, 7], cache.ks[page, :, 7] = 0xB8, 25.0 / math.sqrt(dim)     # 0xB8: -1
+    else:
+        cache.k[page, :, 7] = -25.0 / math.sqrt(dim)
+    good, _ = run_bits(cache, q, new)
+    assert good.isfinite().all()
+    spoil(cache, "v", 7, 0, 5, "code" if e4m3 and bad == "nan" else bad)
+    out, _ = run_bits(cache, q, new)
+    assert same(out[:, 4:], good[:, 4:])
+    if bad == "nan":
+        assert out[:, :4, 5].isnan().all()
+    elif e4m3:
+        assert not out[:, :4].isfinite().any()
+    else:
+        assert (out[:, :4, 5] == math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_prompt_value_that_is_not_finite_under_a_small_weight(dtype):
+    n, dim = 100, 128
+    x = normal((n, 6, dim), dtype, 30, 0.1)
+    q, k, v = x[:, :4] + 1, x[:, 4:5].clone(), x[:, 5:6].clone()
+    k[7] = -25.0 / math.sqrt(dim)
+    good = fp8.fp8_attn_prompt(q, k, v, cu_of([n]))
+    v[7, 0, 5] = math.inf
+    out = fp8.fp8_attn_prompt(q, k, v, cu_of([n]))
+    assert (out[7:, :, 5] == math.inf).all() and same(out[:7], good[:7])
+    rest = [c for c in range(dim) if c != 5]
+    assert same(out[..., rest], good[..., rest])
