@@ -221,9 +221,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 #pragma unroll
       for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
       top = max_halves(top) * c;
-      if (__any(top > m + kSlack)) {
-        const float m1 = fmaxf(m, top);
-        const float keep = m == m1 ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+      const bool above = top > m + kSlack;
+      if (__any(above)) {      // each row by its own scores: another row's change nothing in it
+        const float m1 = above ? top : m;
+        const float keep = above ? __builtin_amdgcn_exp2f(m - m1) : 1.0f;
         m = m1;
         l *= keep;
 #pragma unroll

@@ -241,6 +241,43 @@ def test_values_that_are_not_finite(length, many, dim, dtype, e4m3):
 @pytest.mark.parametrize("dtype,e4m3", KINDS)
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("length", [130, 3000])
+def test_keys_that_are_not_finite(length, many, dim, dtype, e4m3):
+    """A late token's key: a score of NaN or +inf gives NaN, one of -inf no weight; rows that do not see it keep their bits."""
+    new = few_or_many(many)
+    q = normal((new, 8, dim), dtype, 24)
+    for what in ("nan", "inf", "-inf") if not e4m3 else ("nan", "inf", "code"):
+        cache = Cache([length], 2, dim, 16, dtype, e4m3, 23)
+        good, good_lse = run_bits(cache, q, new)
+        at = length - 3
+        spoil(cache, "k", at, 1, 7, what)
+        out, lse = run_bits(cache, q, new)
+        assert same(out[:-3], good[:-3]) and same(out[:, :4], good[:, :4]), what
+        assert same(lse[:-3], good_lse[:-3]) and same(lse[:, :4], good_lse[:, :4]), what
+        reread(cache) if e4m3 else cache.values.update(k=f64_of(cache.k))
+        page = int(cache.table[0, at // 16])
+        with np.errstate(invalid="ignore"):
+            score = np.einsum("thd,d->th", f64_of(q[-3:, 4:]), cache.values["k"][page, 1, at % 16])
+        if e4m3 and what == "inf":      # (sum of the codes' products) * inf; the float64 products would mix signs
+            codes = decode_e4m3(cache.k[page, 1, at % 16].cpu().numpy()).astype(np.float64)
+            score = np.einsum("thd,d->th", f64_of(q[-3:, 4:]), codes) * math.inf
+        none = torch.from_numpy(score == -math.inf).to(DEV)
+        assert out[-3:, 4:][~none].isnan().all() and lse[-3:, 4:][~none].isnan().all(), what
+        kk, vv = cache.request("k", 0).copy(), cache.request("v", 0)
+        kk[at, 1] = 0
+        for t in range(3):          # without the key, which has no weight: a request one key shorter
+            if none[t].any():
+                n = length - 2 + t
+                keep = [j for j in range(n) if j != at]
+                ref = attention_ref(f64_of(q[new - 3 + t:new - 2 + t]), kk[keep], vv[keep], len(keep) - 1, 1 / math.sqrt(dim), 0)
+                pick = np.flatnonzero(np.r_[np.zeros(4, bool), none[t].cpu().numpy()])
+                ref = tuple(x[:, pick] for x in ref)
+                check_rows(out[new - 3 + t:new - 2 + t][:, pick], lse[new - 3 + t:new - 2 + t][:, pick], ref, dtype, n, dim, float(np.abs(vv).max()), what)
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("name", ["k", "v"])
 def test_before_the_window_nothing_matters(name, many, dim, dtype, e4m3):
     """A key or value that no row's window reaches, in a tile of keys that some of their windows share."""
