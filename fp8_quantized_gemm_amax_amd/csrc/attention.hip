@@ -105,6 +105,18 @@ void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnA
   else attn::launch_attn_tile(dt, head_dim, e4m3, a, s);
 }
 
+int64_t attn_prompt_groups(int64_t tokens, int64_t batch, int64_t hq, int64_t hk) {
+  return attn::tile_groups(tokens, batch, hq / hk, hk, false);
+}
+
+int64_t attn_paged_groups(bool e4m3, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int64_t capacity, int64_t max_new) {
+  using namespace attn;
+  const int64_t group = hq / hk;
+  const bool split = may_split(tokens, group, batch, hk, capacity);
+  return few_rows(e4m3, max_new, group, tokens, batch) ? few_groups(tokens, batch, group, hk, capacity, split)
+                                                       : tile_groups(tokens, batch, group, hk, split);
+}
+
 int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
                              int64_t max_new) {
   using namespace attn;

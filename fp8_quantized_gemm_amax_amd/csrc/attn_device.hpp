@@ -673,7 +673,15 @@ __device__ __forceinline__ v16f mfma_odd(const v8s& v, const float (&z)[8], uint
   return o;
 }
 
-// Host side: the paged kernels for many rows and for few.
+// Host side: workgroups of a launch for many rows and for few, and the launches.
+inline int64_t tile_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, bool split) {
+  return (tile_bound(tokens, group, batch, 128) + (split ? extra_units(hk) : 0)) * hk;
+}
+inline int64_t few_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, int64_t capacity, bool split) {
+  const int64_t tiles = tile_bound(tokens, group, batch, 32) * hk, pieces = tiles * ((capacity + kMinKeys - 1) / kMinKeys);
+  if (!split) return tiles;
+  return pieces < kFewGroups ? pieces : kFewGroups;   // no more than the pieces have work
+}
 void launch_attn_tile(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
 void launch_attn_few(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
 void launch_attn_join(int dt, int head_dim, const AttnArgs& a, hipStream_t s);   // after launch_attn_tile's

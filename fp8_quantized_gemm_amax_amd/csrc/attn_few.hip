@@ -15,7 +15,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
 #include <type_traits>
 
 #include "attn_device.hpp"
@@ -390,11 +389,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
 
 template <int DT, int D, int SRC>
 void launch(const AttnArgs& a, hipStream_t s) {
-  const int64_t tiles = tile_bound(a.tokens, a.group, a.batch, kRows);
   const int64_t capacity = static_cast<int64_t>(a.width) << a.page_shift;
   const bool split = may_split(a.tokens, a.group, a.batch, a.hk, capacity);
-  const int64_t pieces = tiles * a.hk * ((capacity + kMinKeys - 1) / kMinKeys);   // no more than these have work
-  attn_few_kernel<DT, D, SRC><<<static_cast<unsigned>(split ? std::min<int64_t>(kFewGroups, pieces) : tiles * a.hk), 256, 0, s>>>(a, split);
+  const int64_t groups = few_groups(a.tokens, a.batch, a.group, a.hk, capacity, split);
+  attn_few_kernel<DT, D, SRC><<<static_cast<unsigned>(groups), 256, 0, s>>>(a, split);
 }
 
 template <int SRC>

@@ -461,10 +461,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 
 template <int DT, int D, int SRC>
 void launch(const AttnArgs& a, hipStream_t s) {
-  const int64_t tiles = tile_bound(a.tokens, a.group, a.batch, kRows);
   const bool split = SRC != SRC_PACKED && may_split(a.tokens, a.group, a.batch, a.hk, static_cast<int64_t>(a.width) << a.page_shift);
-  const int64_t units = (tiles + (split ? extra_units(a.hk) : 0)) * a.hk;
-  attn_tile_kernel<DT, D, SRC><<<static_cast<unsigned>(units), 64 * kWaves, 0, s>>>(a, split);
+  const int64_t groups = tile_groups(a.tokens, a.batch, a.group, a.hk, split);
+  attn_tile_kernel<DT, D, SRC><<<static_cast<unsigned>(groups), 64 * kWaves, 0, s>>>(a, split);
   if (split) launch_attn_join(DT, D, a, s);
 }
 

@@ -169,8 +169,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
 
 template <int DT, int D>
 void append(bool e4m3, const AppendArgs& a, hipStream_t s) {
-  constexpr int kRows = kAppendThreads / (D / 8);
-  const int grid = (a.tokens * a.heads + kRows - 1) / kRows;
+  const unsigned grid = static_cast<unsigned>(kv_append_groups(a.tokens, a.heads, D));
   if (e4m3) kv_append_kernel<DT, D, true><<<grid, kAppendThreads, 0, s>>>(a);
   else kv_append_kernel<DT, D, false><<<grid, kAppendThreads, 0, s>>>(a);
 }
@@ -180,6 +179,11 @@ void append(bool e4m3, const AppendArgs& a, hipStream_t s) {
 void launch_paged_plan(const PlanArgs& a, hipStream_t s) {
   const int groups = max(1, min((a.tokens + kPlanThreads - 1) / kPlanThreads, 1024));
   paged_plan_kernel<<<groups, kPlanThreads, static_cast<size_t>(a.batch) * 8, s>>>(a);
+}
+
+int64_t kv_append_groups(int64_t tokens, int64_t heads, int head_dim) {
+  const int rows = kAppendThreads / (head_dim / 8);
+  return (tokens * heads + rows - 1) / rows;
 }
 
 void launch_kv_append(int dt, int head_dim, bool e4m3, const AppendArgs& a, hipStream_t s) {

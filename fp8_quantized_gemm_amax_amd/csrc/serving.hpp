@@ -36,6 +36,7 @@ struct AppendArgs {
   void *kc, *vc;
   float *ks, *vs;
 };
+int64_t kv_append_groups(int64_t tokens, int64_t heads, int head_dim);   // workgroups of the launch
 void launch_kv_append(int dt, int head_dim, bool e4m3, const AppendArgs& a, hipStream_t s);
 
 // Attention over packed prompts (table == nullptr: k and v strided tensors of the same tokens)
@@ -55,6 +56,8 @@ struct AttnArgs {
 };
 void launch_attn_prompt(int dt, int head_dim, const AttnArgs& a, hipStream_t s);
 void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnArgs& a, hipStream_t s);
+int64_t attn_prompt_groups(int64_t tokens, int64_t batch, int64_t hq, int64_t hk);   // workgroups of the launch
+int64_t attn_paged_groups(bool e4m3, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int64_t capacity, int64_t max_new);
 int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
                              int64_t max_new);
 

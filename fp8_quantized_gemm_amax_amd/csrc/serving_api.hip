@@ -13,6 +13,7 @@ namespace {
 constexpr int64_t kMaxInt = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
 constexpr int64_t kMaxKeys = int64_t{1} << 30;     // of a request: key numbers and their sums stay below 2^31
+constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;   // workgroups of 256 threads: a launch holds 2^32 - 1
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool valid_dt(fp8_dtype_t dt) { return dt == FP8_BF16 || dt == FP8_F16; }
@@ -93,6 +94,7 @@ fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t
   if (st == FP8_OK) st = check_strides(tokens, kv_heads, v_token_stride, v_head_stride);
   if (st != FP8_OK) return st;
   if (tokens == 0) return FP8_OK;
+  if (fp8amax::kv_append_groups(tokens, kv_heads, head_dim) > kMaxGroups) return FP8_ERR_TOO_LARGE;
   const bool e4m3 = format == FP8_KV_E4M3;
   if (!k || !v || !slots || !k_cache || !v_cache || (e4m3 && (!k_scales || !v_scales))) return FP8_ERR_NULL_POINTER;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8) ||
@@ -123,6 +125,7 @@ fp8_status_t fp8_attn_prompt(const void* q, const void* k, const void* v, fp8_dt
   if (tokens > 1 && (k_token_stride < head_dim || v_token_stride < head_dim)) return FP8_ERR_BAD_SHAPE;
   if (k_token_stride > (int64_t{1} << 20) || v_token_stride > (int64_t{1} << 20)) return FP8_ERR_TOO_LARGE;
   if (tokens == 0 || batch == 0) return FP8_OK;
+  if (fp8amax::attn_prompt_groups(tokens, batch, q_heads, kv_heads) > kMaxGroups) return FP8_ERR_TOO_LARGE;
   if (!q || !k || !v || !cu_tokens || !out) return FP8_ERR_NULL_POINTER;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_tokens, 4) ||
       !aligned(lse, 4))
@@ -163,6 +166,8 @@ fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const
   if ((st = check_strides(tokens, q_heads, q_token_stride, q_head_stride)) != FP8_OK) return st;
   if (tokens == 0 || batch == 0) return FP8_OK;
   const bool e4m3 = format == FP8_KV_E4M3;
+  if (fp8amax::attn_paged_groups(e4m3, tokens, batch, q_heads, kv_heads, width * page_size, max_new) > kMaxGroups)
+    return FP8_ERR_TOO_LARGE;
   const int64_t need = fp8amax::attn_paged_workspace(tokens, batch, q_heads, kv_heads, head_dim, width * page_size, max_new);
   if (workspace_bytes < need) return FP8_ERR_BAD_SHAPE;
   if (!q || !cu_tokens || !k_cache || !v_cache || !block_table || !seq_lens || !out || (need > 0 && !workspace) ||

@@ -31,6 +31,10 @@
  * and head strides are given in elements, non-negative multiples of 8 (so that a fused
  * projection's output is read in place).  Data pointers need 16-byte, int32 and float32
  * pointers 4-byte, int64 pointers 8-byte alignment.
+ *
+ * Sizes.  FP8_ERR_TOO_LARGE, before any HIP call, where tokens * heads passes 2^30 or the work would
+ * need 2^24 workgroups or more (a launch holds less than 2^32 threads): a workgroup appends 16 rows
+ * of 128 channels or 32 of 64, and attends for 128 rows or 32 of one request and key head.
  */
 #ifndef FP8AMAX_SERVING_H
 #define FP8AMAX_SERVING_H

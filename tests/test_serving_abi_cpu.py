@@ -200,3 +200,27 @@ def test_enumerations_take_any_integer():
     assert call("fp8_kv_append", APPEND, dt=2 ** 31 - 1) == DTYPE
     assert call("fp8_attn_paged", PAGED, fmt=-1) == DTYPE
     assert ctypes.sizeof(ctypes.c_int) == 4
+
+
+@pytest.mark.parametrize("name,base,most,change", [
+    ("fp8_kv_append", APPEND, "tokens", dict(heads=1, dim=128)),                # 16 rows a workgroup
+    ("fp8_kv_append", APPEND, "tokens", dict(heads=1, dim=64, kts=64, vts=64)),     # 32
+    ("fp8_attn_prompt", PROMPT, "batch", dict(hq=1, hk=1)),                     # one a request, and one for 128 rows
+    ("fp8_attn_paged", PAGED, "batch", dict(hq=1, hk=1)),
+    ("fp8_attn_paged", PAGED, "batch", dict(hq=1, hk=1, width=1)),
+])
+def test_more_work_than_a_launch_holds_is_too_large(name, base, most, change):
+    """2^24 workgroups of 256 threads are one thread more than a launch takes; one fewer passes on to the null pointer."""
+    each = {128: 16, 64: 32}[change["dim"]] if name == "fp8_kv_append" else 1
+    first = {k: None for k in ("k" if name == "fp8_kv_append" else "q",)}
+    limit = (2 ** 24 - 1) * each
+    assert call(name, base, **change, **first, **{most: limit}) == NULLP
+    assert call(name, base, **change, **first, **{most: limit + 1}) == LARGE
+    assert call(name, base, **change, **first, **{most: 2 ** 29}) == LARGE
+
+
+def test_more_work_than_a_launch_holds_by_rows():
+    """Paged attention for few rows needs a workgroup for 32, for many one for 128."""
+    big = dict(q=None, hq=1, hk=1, tokens=2 ** 29 + 2 ** 20, width=1, max_new=1)
+    assert call("fp8_attn_paged", PAGED, **big, batch=2 ** 23 + 2 ** 15) == LARGE     # 64 rows a request at most: for few
+    assert call("fp8_attn_paged", PAGED, **big, batch=2 ** 12) == NULLP                # for many
