@@ -22,6 +22,11 @@ bool valid_dim(int32_t d) { return d == 64 || d == 128; }
 bool valid_page(int32_t p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 int shift_of(int32_t p) { return __builtin_ctz(static_cast<unsigned>(p)); }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && (x < y ? y - x < static_cast<uint64_t>(a_bytes) : x - y < static_cast<uint64_t>(b_bytes));
+}
+
 fp8_status_t finish_launch() { return hipGetLastError() == hipSuccess ? FP8_OK : FP8_ERR_LAUNCH; }
 
 // Token and head strides of a [tokens, heads, dim] tensor: the kernels read 16 bytes at a time.
@@ -68,7 +73,17 @@ fp8_status_t fp8_paged_plan(const int32_t* cached, const int32_t* added, int64_t
       !aligned(taken_in, 4) || !aligned(cu_tokens, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) ||
       !aligned(slots, 8) || !aligned(taken_out, 4) || !aligned(missing, 4))
     return FP8_ERR_MISALIGNED;
-  if (taken_in == taken_out) return FP8_ERR_BAD_SHAPE;
+  // What one workgroup writes others still read: outputs, the table among them, stand apart.
+  struct Range {
+    const void* p;
+    int64_t bytes;
+  };
+  const Range ranges[] = {{block_table, batch * width * 4}, {cu_tokens, batch * 4 + 4}, {seq_lens, batch * 4}, {positions, tokens * 4},
+                          {slots, tokens * 8}, {taken_out, 4}, {missing, 4},   // outputs; then inputs
+                          {cached, batch * 4}, {added, batch * 4}, {free_pages, n_free * 4}, {taken_in, 4}};
+  for (int i = 0; i < 7; ++i)
+    for (int j = i + 1; j < 11; ++j)
+      if (overlap(ranges[i].p, ranges[i].bytes, ranges[j].p, ranges[j].bytes)) return FP8_ERR_BAD_SHAPE;
   fp8amax::PlanArgs a{};
   a.cached = cached; a.added = added; a.batch = static_cast<int>(batch); a.page_shift = shift_of(page_size);
   a.table = block_table; a.width = static_cast<int>(width);

@@ -32,6 +32,8 @@
  * projection's output is read in place).  Data pointers need 16-byte, int32 and float32
  * pointers 4-byte, int64 pointers 8-byte alignment.
  *
+ * What a call writes shares no memory with what it reads.
+ *
  * Sizes.  FP8_ERR_TOO_LARGE, before any HIP call, where tokens * heads passes 2^30 or the work would
  * need 2^24 workgroups or more (a launch holds less than 2^32 threads): a workgroup appends 16 rows
  * of 128 channels or 32 of 64, and attends for 128 rows or 32 of one request and key head.
@@ -56,7 +58,7 @@ typedef enum FP8_ENUM_BASE { FP8_KV_SAME = 0, FP8_KV_E4M3 = 1 } fp8_kv_format_t;
  *                 and the entries ceil(cached / page_size) .. ceil((cached + added) / page_size)
  *                 get pages from the free list, in the order of the requests; others stay.
  *   free_pages  : int32 [n_free]; taken_in int32 [1]: how many of them are in use already.
- *   taken_out   : int32 [1], taken_in plus the pages given out (may not be taken_in itself).
+ *   taken_out   : int32 [1], taken_in plus the pages given out.
  *   missing     : int32 [1], pages that were needed and not given: the free list was used up
  *                 (their entries become -1) or the table has no entry for them.
  *   cu_tokens   : int32 [batch + 1], the prefix sums of `added`.
@@ -64,6 +66,8 @@ typedef enum FP8_ENUM_BASE { FP8_KV_SAME = 0, FP8_KV_E4M3 = 1 } fp8_kv_format_t;
  *   positions   : int32 [tokens], each new token's position in its request, -1 past the last.
  *   slots       : int64 [tokens], each new token's slot; -1 past the last token and for tokens
  *                 without a page.
+ * The outputs, block_table among them, share no memory with an input or with each other (refused as
+ * FP8_ERR_BAD_SHAPE): lengths are not advanced in place, nor is taken_in.
  * tokens is the size of positions and slots; new tokens past it are counted in cu_tokens only.
  * batch <= 16384; batch == 0 fills positions and slots with -1.  Requires width >= 1.
  */

@@ -224,3 +224,21 @@ def test_more_work_than_a_launch_holds_by_rows():
     big = dict(q=None, hq=1, hk=1, tokens=2 ** 29 + 2 ** 20, width=1, max_new=1)
     assert call("fp8_attn_paged", PAGED, **big, batch=2 ** 23 + 2 ** 15) == LARGE     # 64 rows a request at most: for few
     assert call("fp8_attn_paged", PAGED, **big, batch=2 ** 12) == NULLP                # for many
+
+
+# The plan's buffers apart from each other, 4 KiB each; taken_in and what follows are never dereferenced here.
+APART = dict(PLAN, **{n: A + 4096 * i for i, n in enumerate(("cached", "added", "table", "free", "taken", "cu", "lens", "positions",
+                                                             "slots", "taken_out", "missing"))})
+
+
+@pytest.mark.parametrize("out", ["table", "cu", "lens", "positions", "slots", "taken_out", "missing"])
+@pytest.mark.parametrize("other", ["cached", "added", "free", "taken", "table", "cu", "lens", "positions", "slots", "taken_out", "missing"])
+def test_plan_refuses_outputs_that_share_memory(out, other):
+    """Lengths advanced in place (seq_lens is cached) would be read by other workgroups after they are written."""
+    if out == other:
+        return
+    assert call("fp8_paged_plan", APART, **{out: APART[other]}) == SHAPE
+    size = dict(cached=16, added=16, table=128, free=20, taken=4, cu=20, lens=16, positions=40, slots=80, taken_out=4, missing=4)[other]
+    last = APART[other] + size - 4              # the other's last entry
+    if out != "slots" or last % 8 == 0:
+        assert call("fp8_paged_plan", APART, **{out: last}) == SHAPE
