@@ -14,11 +14,20 @@ namespace {
 // Whether a batch goes to the kernel for few rows: where its requests have at most 32 rows a key head on
 // average (64 over an e4m3 cache, which the kernel for many rows has to widen on the way), and none, as
 // far as max_new says, has more than 512, since that one's keys are read once for every 32 rows.
-// Kernel for many rows against the one for few, in us, 24 to 32 requests over up to 4000 keys, 128
-// channels, by average rows a request:
-//   16 bits  19 rows 48.7 : 44.6    31 rows 49.3 : 51.0    39 rows (500 keys) 17.6 : 27.7    73 rows 157 : 280
-//   e4m3     15 rows 52.2 : 32.0    32 rows 54.3 : 37.5    56 rows 68.3 : 43.4    61 rows 59.8 : 50.7
-//            73 rows 195 : 184      80 rows 65.4 : 66.3
+// Kernel for many rows against the one for few, us on one card, 128 channels, requests of equal rows over
+// half to all of so many keys:
+//   16 bits, rows      4            16           32           40
+//     24 x 500   17.1 : 13.0  17.4 : 13.3  17.8 : 13.7  17.9 : 27.9
+//      8 x 2000  22.3 : 21.3  21.3 : 23.5  21.1 : 28.9  21.7 : 36.0
+//     64 x 4000   155 : 152    153 : 164    154 : 172    156 : 300
+//     1 x 100000   97 :  79     96 : 110     92 : 123     95 : 146
+//   e4m3, rows         4            32           64           80
+//     24 x 500   22.3 : 12.6  23.1 : 13.5  23.6 : 17.7  23.9 : 31.3
+//      8 x 2000  27.0 : 16.0  26.8 : 22.8  28.1 : 30.0  30.4 : 31.5
+//     64 x 4000   157 :  87    159 : 102    162 : 175    163 : 233
+//     1 x 100000  108 :  50    103 :  90    105 :  97    113 : 113
+// No number of rows suits every length: at the limits the kernel for few is up to 23% faster over short
+// caches and up to 37% slower over long ones in 16 bits (above 12 rows), 25% faster to 8% slower over e4m3.
 bool few_rows(bool e4m3, int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
   return std::min(max_new, tokens) * group <= 512 && tokens * group <= (e4m3 ? 64 : 32) * batch;
 }

@@ -173,9 +173,12 @@ __device__ __forceinline__ v4i key_rows(const AttnArgs& a, const Rows& r, const 
 // of a tile of rows are cut into pieces that different workgroups take, each leaving its maximum,
 // sum and output, which the last of them joins.  The requests' lengths are on the device, so the
 // cut is made there: every workgroup sums the batch's work (three integers a request).
-constexpr int kMaxSplitBatch = 1024;   // above, there is enough to do without cuts
+// The most requests whose sums the workgroups hold in LDS.  Above, nothing is cut, which costs nothing
+// where requests are alike (1100 e4m3 requests of up to 300 keys: 184 us with a limit of 1024 or 2048)
+// and much where one is long (131072 keys among them: 1368 us and 256).
+constexpr int kMaxSplitBatch = 1024;
 constexpr int kMaxSplitHeads = 1024;
-constexpr int kMinKeys = 256;          // no piece below (one request of 701 keys, 32 heads: 128, 256, 512 keys 11.2, 11.3, 17.3 us)
+constexpr int kMinKeys = 256;          // no piece below (one request of 701 keys, 32 heads: 128, 256, 512 keys 11.2, 11.5, 17.5 us)
 constexpr int kMaxSlots = 4096;        // partial results of a launch
 
 struct Unit {
@@ -329,7 +332,7 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int i, const Request&
 // request, the last first, so that the tiles that see the most keys start first whatever request
 // they are of (hardware starts workgroups in order).  Up to kSlots workgroups are all on the card at
 // once, two to a CU: there the second of a CU is the lightest left, not the next.  12 prompts of up to
-// 2048 tokens: 68.4 us so, 73.2 in the order of the requests.
+// 2048 tokens: 59 us so, 64 in the order of the requests.
 constexpr int kSlots = 512;
 template <int SIZE>
 __device__ __forceinline__ bool find_ranked(const AttnArgs& a, Unit& u) {
@@ -404,11 +407,12 @@ __device__ __forceinline__ int64_t partial_at(int row, int quad) {
 //   max(kMinTileKeys, work / kUnits)
 // keys, numbered request by request, the tiles that see the most first.  A full batch of equal
 // lengths stays uncut.  A second launch joins the partial results: 128 rows of them are too much for
-// one workgroup at the end of the first (measured: 2 tiles a head over 100000 keys 406 us that way).
+// one workgroup at the end of the first (2 tiles a head over 100000 keys took 2.3 times as long that way).
 // One unit a CU rather than the two that fit, since a partial result of 128 rows is 64 KB to write and
-// to read: 512 and 256 units take 569 and 535 us for 4 x 1024 tokens over up to 16000 keys, 111 and 101
-// for 16 over 100000, 54 and 50 for 16 x 64 over up to 4096; 192 take 528, 111 and 53.  Pieces of at
-// least 512 keys: 24 mixed requests of up to 2000 keys, e4m3, 31 us; with 256 35, with 1024 38.
+// to read: with 512, 256 and 192 units 3442 tokens over up to 16000 keys take 489, 455 and 456 us, 16
+// over 100000 110, 99 and 109, 16 x 64 over up to 4096 53, 48 and 51.  Pieces of at least 512 keys: 24
+// mixed requests of up to 2000 keys take 26.7 us (e4m3) and 21.1 (16 bits); with 256 27.0 and 21.1, with
+// 1024 33.1 and 25.2.
 constexpr int kUnits = 256;
 constexpr int kMinTileKeys = 512;
 // Units per key head are at most the tiles and this many more, and partial results at most twice it.
@@ -475,8 +479,8 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, int block, int* lds
 
 // The cut for few rows, where the keys are read once and every step costs the same: the batch's
 // steps in one line, an equal stretch for each of kFewGroups workgroups (two to a CU: with 256, 512
-// and 1024 the 64-request e4m3 batch takes 91.5, 75.6 and 83.7 us, 4 requests of up to 131072 keys 174,
-// 182 and 192).
+// and 1024 the 64-request e4m3 batch takes 88.9, 73.9 and 81.7 us, 4 requests of up to 131072 keys 171,
+// 179 and 189).
 constexpr int kFewGroups = 512;
 static_assert(2 * kFewGroups <= kMaxSlots, "partial results of the cut for few rows");
 

@@ -8,10 +8,10 @@
 // multiplied, V while the next scores are: 16 KB a wave, two workgroups a CU, so 128 KB of reads in
 // flight a CU.
 // Long caches are bound by HBM: 4 requests of up to 131072 keys, 8 heads of 128 in bf16, 977 MB,
-// take 181 us (5.4 TB/s; a copy of 2 GiB reaches 4.8, reads and writes together); 64 e4m3 requests of
-// up to 8192 keys, 322 MB, 74 us (4.4 TB/s).  Short ones are bound by a chain of dependent reads of 1
+// take 180 us (5.4 TB/s; a plain read of 1 GiB reaches 7.0, a copy 4.9 with its writes); 64 e4m3
+// requests of up to 8192 keys, 322 MB, 74 us (4.4 TB/s).  Short ones are bound by a chain of dependent reads of 1
 // to 2 us each (lengths, table, K and V, partial results): one request of 701 keys, 32 heads of 128,
-// 11.5 MB, takes 11.5 us.
+// 11.5 MB, takes 11.7 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,8 +25,8 @@ namespace {
 
 constexpr int kRows = 32;
 // Up to this many keys a tile is not worth cutting: the join costs what walking over them does.  64
-// requests of up to 300 keys, e4m3: cut 17.8 us, whole 13.6; of up to 500, 16 bits: 18.9 and 15.4; one
-// request of 500: 10.9 and 11.4.  At 768: 16 e4m3 requests of up to 700 keys, cut 11.9, whole 14.5.
+// requests of up to 300 keys, e4m3: cut 17.6 us, whole 13.1; of up to 500, 16 bits: 18.5 and 15.2; one
+// request of 500: 10.8 and 11.1.  At 768: 16 e4m3 requests of up to 700 keys, cut 11.6, whole 14.5.
 constexpr int kWholeKeys = 512;
 
 // One dword from `p` into LDS at to + lane where `on` holds for the lane, 0 where it does not.

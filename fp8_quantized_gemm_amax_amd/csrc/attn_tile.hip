@@ -5,14 +5,15 @@
 // for its product with V, and O / l once to the output's type.
 // Per tile and wave, 128 channels: 32 MFMAs of 32 cycles each and 187 vector instructions, 32 of them
 // exponentials of 8 cycles, so the matrix and the vector unit are both in demand; tile i's weights are
-// formed while tile i + 1's keys and the weights that are ready are multiplied (2.14 -> 2.08 ms at
-// 16384 tokens).  64 KB of LDS a workgroup, so two share a CU and one's barriers hide behind the
+// formed while tile i + 1's keys and the weights that are ready are multiplied (3% of 16384 tokens'
+// time).  64 KB of LDS a workgroup, so two share a CU and one's barriers hide behind the
 // other's work; one workgroup a CU with tiles further ahead, or with two teams of four waves that
 // take turns, was slower.
-// Measured, 32 heads on 8 of 128 channels, bf16: 16384 tokens 1.96 ms, 1123 TFLOP/s, where a library
-// product of 8192^3 reaches 1185 on the same card: power bounds both, with inputs of zeros they run
-// at 1415 and 1767.  12 packed prompts of up to 2048 tokens 57 us, bound by the steps of the
-// longest (32 tiles, 1.1 us each).  4 x 1024 tokens over up to 16000 cached keys 443 us (1060 TFLOP/s).
+// Measured on one card, 32 heads on 8 of 128 channels, bf16: 16384 tokens 2.02 ms, 1090 TFLOP/s, where a
+// library product of 8192^3 reaches 1240: power bounds both, with inputs of zeros they run at 1528 and
+// 1768.  12 packed prompts of up to 2048 tokens 58 us: 41 steps of 64 keys a CU at 0.95 us where two
+// workgroups share it are 39 us, the rest is that the longest tiles, 32 steps, share to their end.  3442
+// new tokens of four requests over up to 16000 cached keys 455 us (1032 TFLOP/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,8 +29,8 @@ constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
 // The running maximum follows a larger score only past this much (in powers of two): weights are then
 // at most 2^8 rather than 1, which float32 sums and 16-bit weights hold as well, and most tiles leave
-// o as it is.  Without slack (0) 16384 tokens take 2165 us instead of 2080, 4 x 1024 over up to 16000
-// keys 616 instead of 569.
+// o as it is.  Without slack (0) 16384 tokens take 2058 us instead of 1988, 3442 over up to 16000 keys
+// 472 instead of 455 (one card).
 constexpr float kSlack = 8.0f;
 
 // The workgroup's unit: cut from the batch's work (find_unit) or a whole tile of rows.

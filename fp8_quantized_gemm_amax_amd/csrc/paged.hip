@@ -52,8 +52,8 @@ __device__ __forceinline__ int pages_for(int64_t len, int shift, int width) {
 // share of the tokens and of the new table entries, each found by a search in the sums.  A token
 // on a new page takes the page from the free list itself rather than from the table, which other
 // workgroups are writing.  Bound by the launch and its chain of reads (lengths, then a page number):
-// 64 requests and 64 tokens 5.8 us, 1024 requests and 34000 tokens (0.36 MB) 6.6 us; with 256 requests a
-// scan, one scan after the other, 7.5.
+// 64 requests and 64 tokens 5.7 us, 1024 requests and 34000 tokens (0.36 MB) 6.6 us; with 256 requests a
+// scan, one scan after the other, it took 14% longer.
 __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
   extern __shared__ int sums[];
   int* const cu = sums;                 // inclusive sums of the new tokens, at most 2^31 - 1
@@ -138,9 +138,9 @@ constexpr int kAppendThreads = 256;
 // One group of D / 8 lanes per token and head: 16 bytes a lane of the key and of the value, the rows'
 // largest magnitudes by DPP within the group, then the codes (8 bytes a lane) and the scales, or
 // the 16 bytes as they are.  Bound by memory: 16384 tokens of 8 heads of 128 to e4m3, 102 MB, take
-// 23.4 us (4.4 TB/s; a 2 GiB copy runs at 4.8).  Key and value of a row in one thread, so that two
-// loads are under way: with one tensor a workgroup it took 30.3; with two and four rows a
-// thread 25.3 and 29.6.
+// 23.4 us (4.4 TB/s; a 2 GiB copy runs at 4.9).  Key and value of a row in one thread, so that two
+// loads are under way: with one tensor a workgroup it took 23% longer; with two and four rows a
+// thread 2% and 20%.
 template <int DT, int D, bool E4M3>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8;
