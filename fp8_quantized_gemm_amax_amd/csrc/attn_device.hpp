@@ -72,19 +72,19 @@ __device__ __forceinline__ v8s pack8(const float (&x)[8]) {
   return __builtin_bit_cast(v8s, v4u{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
 }
 
-// Eight e4m3 codes as 16-bit values (exact: both types hold every code).
+// Eight e4m3 codes as 16-bit values (exact: both types hold every code), times a power of two.
 template <int DT>
-__device__ __forceinline__ v4u codes8(uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ v4u codes8(uint32_t lo, uint32_t hi, float power = 1.0f) {
   if constexpr (DT == DT_BF16)
-    return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
+    return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, true)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, true))};
   else
-    return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true))};
+    return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, power, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, power, true)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, true))};
 }
 
 // fp16 queries over an e4m3 cache.  A weight times its value's scale can lie far outside fp16's range,
@@ -100,13 +100,6 @@ struct SplitScale {
 __device__ __forceinline__ SplitScale split_scale(float scale) {
   const uint32_t e = min(max((__float_as_uint(scale) >> 23) & 0xff, 127u - 14), 127u + 7);
   return {__uint_as_float(e << 23), scale * __uint_as_float((254 - e) << 23)};
-}
-// Eight e4m3 codes times a power of two as fp16 values.
-__device__ __forceinline__ v4u codes8_times(uint32_t lo, uint32_t hi, float power) {
-  return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, power, false)),
-             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, power, true)),
-             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, false)),
-             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, true))};
 }
 
 // {a of lane l % 32, b of lane l % 32} in the low and high half, and the same of lanes 32-63.

@@ -143,16 +143,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
         scale = y.rest;
         power = __shfl(y.power, lane >> 2);
       }
-      auto widen = [&](uint32_t lo, uint32_t hi) -> v4u {
-        if constexpr (SPLIT) return codes8_times(lo, hi, power);
-        else return codes8<DT>(lo, hi);
-      };
 #pragma unroll
       for (int x = 0; x < kPlanes; ++x) {
         const int c = (lane & 3) * (D / 32) + 2 * x;       // first of the two chunks of eight channels
         char* to = lds + buffer * kTile + (c >> 3) * kPlane + key * 128;
-        *reinterpret_cast<v4u*>(to + (((c & 7) ^ gemm::swz(key & 15)) << 4)) = widen(from.c[x][0], from.c[x][1]);
-        *reinterpret_cast<v4u*>(to + (((c & 7) + 1) ^ gemm::swz(key & 15)) * 16) = widen(from.c[x][2], from.c[x][3]);
+        *reinterpret_cast<v4u*>(to + (((c & 7) ^ gemm::swz(key & 15)) << 4)) = codes8<DT>(from.c[x][0], from.c[x][1], power);
+        *reinterpret_cast<v4u*>(to + (((c & 7) + 1) ^ gemm::swz(key & 15)) * 16) = codes8<DT>(from.c[x][2], from.c[x][3], power);
       }
       if (lane < 16) to_scale[16 * wave + lane] = scale;
     };

@@ -179,6 +179,24 @@ def test_value_scales_beyond_fp16(length, many, dim):
     check_request(cache, q, out, dim)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [1, 70])
+def test_every_code_at_every_power_of_two(group, dtype):
+    """Requests of one key and queries of zeros, so that its weight is exactly 1: the output is the value, code times scale,
+    rounded once, for every finite code and the scales 2^-24 .. 2^7.  70 rows a request go to the kernel for many rows."""
+    n, dim, page = 32, 128, 16
+    codes = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F] + [0, 0x80], dtype=torch.uint8, device=DEV).view(2, dim)
+    cache = Cache([1] * n, 2, dim, page, dtype, True, 19)
+    for r in range(n):
+        at = int(cache.table[r, 0])
+        cache.v[at, :, 0], cache.vs[at, :, 0] = codes, 2.0 ** (r - 24)
+    q = normal((n, 2 * group, dim), dtype, 20, 0.0)
+    out = fp8.fp8_attn_paged(q, cache.k, cache.v, cache.dev_table, cache.dev_lens, cu_of([1] * n), cache.ks, cache.vs, max_new=1)
+    exact = decode_e4m3(codes.cpu().numpy()).astype(np.float64)[None] * 2.0 ** (np.arange(n)[:, None, None] - 24)
+    want = torch.from_numpy(exact).to(q.dtype).repeat_interleave(group, dim=1).to(DEV)
+    assert torch.equal(out, want)
+
+
 # ------------------------------------------------- keys and values that are not finite, paged caches
 
 BAD = {"nan": float("nan"), "inf": float("inf"), "-inf": float("-inf")}
