@@ -13,7 +13,7 @@ from .binding import (Fp8Error, fp8_amax, fp8_quantize_per_tensor, fp8_quantize_
                       fp8_gemm_grouped_blockwise, fp8_gemm_grouped_blockwise_ue8m0,
                       fp8_debug_byte_mix, fp8_debug_gemm_plan, fp8_gemv_dynamic, lib, LIB_PATH)
 from .serving import (PagedPlan, fp8_attn_paged, fp8_attn_paged_workspace, fp8_attn_prompt, fp8_kv_append,
-                      fp8_paged_plan, paged_plan_buffers)
+                      fp8_paged_plan, fp8_rope_append, paged_plan_buffers, rope_table)
 
 __all__ = ["Fp8Error", "fp8_amax", "fp8_quantize_per_tensor", "fp8_quantize_per_token_group",
            "fp8_gemm_scaled_tensorwise", "fp8_gemm_scaled_blockwise", "fp8_debug_cast_f32",
@@ -23,4 +23,4 @@ __all__ = ["Fp8Error", "fp8_amax", "fp8_quantize_per_tensor", "fp8_quantize_per_
            "fp8_gemm_grouped_blockwise", "fp8_gemm_grouped_blockwise_ue8m0",
            "fp8_debug_byte_mix", "fp8_debug_gemm_plan", "fp8_gemv_dynamic", "lib", "LIB_PATH",
            "PagedPlan", "fp8_attn_paged", "fp8_attn_paged_workspace", "fp8_attn_prompt",
-           "fp8_kv_append", "fp8_paged_plan", "paged_plan_buffers"]
+           "fp8_kv_append", "fp8_paged_plan", "fp8_rope_append", "paged_plan_buffers", "rope_table"]

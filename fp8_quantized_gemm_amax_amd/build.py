@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8amax.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemv.hip", "serving_api.hip", "paged.hip", "attention.hip",
-           "attn_tile.hip", "attn_few.hip"]
+           "attn_tile.hip", "attn_few.hip", "attn_mx4.hip"]
 OBJ_DIR = os.path.join(PKG, "_build")
 # the Python binding of the serving operators: host code against torch's headers
 BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")

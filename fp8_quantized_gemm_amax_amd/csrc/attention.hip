@@ -28,8 +28,8 @@ namespace {
 //     1 x 100000  108 :  50    103 :  90    105 :  97    113 : 113
 // No number of rows suits every length: at the limits the kernel for few is up to 23% faster over short
 // caches and up to 37% slower over long ones in 16 bits (above 12 rows), 25% faster to 8% slower over e4m3.
-bool few_rows(bool e4m3, int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
-  return std::min(max_new, tokens) * group <= 512 && tokens * group <= (e4m3 ? 64 : 32) * batch;
+bool few_rows(int format, int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
+  return std::min(max_new, tokens) * group <= 512 && tokens * group <= (format == FP8_KV_SAME ? 32 : 64) * batch;
 }
 
 // Joins the partial results of the launch for many rows, of 128 rows each: a thread takes one row and
@@ -109,21 +109,22 @@ void launch_attn_join(int dt, int head_dim, const AttnArgs& a, hipStream_t s) {
 
 }  // namespace attn
 
-void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnArgs& a, hipStream_t s) {
-  if (attn::few_rows(e4m3, max_new, a.group, a.tokens, a.batch)) attn::launch_attn_few(dt, head_dim, e4m3, a, s);
-  else attn::launch_attn_tile(dt, head_dim, e4m3, a, s);
+void launch_attn_paged(int dt, int head_dim, int format, int max_new, const AttnArgs& a, hipStream_t s) {
+  if (!attn::few_rows(format, max_new, a.group, a.tokens, a.batch)) attn::launch_attn_tile(dt, head_dim, format, a, s);
+  else if (format == FP8_KV_MXFP4) attn::launch_attn_mx4_few(dt, head_dim, a, s);
+  else attn::launch_attn_few(dt, head_dim, format == FP8_KV_E4M3, a, s);
 }
 
 int64_t attn_prompt_groups(int64_t tokens, int64_t batch, int64_t hq, int64_t hk) {
   return attn::tile_groups(tokens, batch, hq / hk, hk, false);
 }
 
-int64_t attn_paged_groups(bool e4m3, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int64_t capacity, int64_t max_new) {
+int64_t attn_paged_groups(int format, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int64_t capacity, int64_t max_new) {
   using namespace attn;
   const int64_t group = hq / hk;
   const bool split = may_split(tokens, group, batch, hk, capacity);
-  return few_rows(e4m3, max_new, group, tokens, batch) ? few_groups(tokens, batch, group, hk, capacity, split)
-                                                       : tile_groups(tokens, batch, group, hk, split);
+  if (!few_rows(format, max_new, group, tokens, batch)) return tile_groups(tokens, batch, group, hk, split);
+  return few_groups(tokens, batch, group, hk, capacity, split, format == FP8_KV_MXFP4 ? mx4_rows(tokens, group, batch) : 32);
 }
 
 int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
@@ -133,9 +134,9 @@ int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t 
   auto bytes = [&](bool few) {
     return workspace_bytes(few ? 2 * kFewGroups : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
   };
-  // Enough for either format of the cache.
-  return std::max(bytes(few_rows(false, max_new, hq / hk, tokens, batch)),
-                  bytes(few_rows(true, max_new, hq / hk, tokens, batch)));
+  // Enough for every format of the cache.
+  return std::max(bytes(few_rows(FP8_KV_SAME, max_new, hq / hk, tokens, batch)),
+                  bytes(few_rows(FP8_KV_E4M3, max_new, hq / hk, tokens, batch)));
 }
 
 }  // namespace fp8amax

@@ -36,7 +36,7 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 // Where keys and values come from.
-enum Source { SRC_PACKED = 0, SRC_PAGED = 1, SRC_E4M3 = 2 };
+enum Source { SRC_PACKED = 0, SRC_PAGED = 1, SRC_E4M3 = 2, SRC_MXFP4 = 3 };
 
 constexpr int kKeys = 64;                  // keys in an LDS tile
 constexpr int kPlane = kKeys * 128;        // bytes of a plane: 64 channels of every key of the tile
@@ -86,6 +86,22 @@ __device__ __forceinline__ v4u codes8(uint32_t lo, uint32_t hi, float power = 1.
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, false)),
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, power, true))};
 }
+
+// Eight e2m1 codes, the first in the low bits, times the power of two of a scale byte (mx4_power).
+template <int DT>
+__device__ __forceinline__ v4u mx4_values8(uint32_t w, float power) {
+  if constexpr (DT == DT_BF16)
+    return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 0)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 1)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 2)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 3))};
+  else
+    return v4u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 0)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 1)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 2)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 3))};
+}
+__device__ __forceinline__ float mx4_power(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // fp16 queries over an e4m3 cache.  A weight times its value's scale can lie far outside fp16's range,
 // next to another key's above all, so the scale is split into 2^e and the rest: the power of two goes
@@ -517,9 +533,10 @@ struct Joined {
 //   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
 // A thread takes four channels of a row, and has eight pieces' reads in flight (they go to memory, at
 // more than a microsecond each); with few rows, several threads share a row's pieces.  `lds` is
-// kJoinBytes of LDS that nothing else uses any more.
+// kJoinBytes of LDS that nothing else uses any more.  A place for a partial result holds SIZE rows,
+// of which a tile has ROWS at most.
 constexpr int kJoinBytes = 16 + 256 * 8 * 4;
-template <int DT, int D, int SIZE>
+template <int DT, int D, int SIZE, int ROWS = SIZE>
 __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, char* lds) {
   constexpr int kPieces = 8;
   int* const flag = reinterpret_cast<int*>(lds);
@@ -536,7 +553,7 @@ __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, 
   }
   __syncthreads();
   if (!*flag) return;
-  const int rows = min(SIZE, r.rows - r.row0);
+  const int rows = min(ROWS, r.rows - r.row0);
   int bits = 0;                       // rows, rounded up to a power of two
   while ((1 << bits) < rows) ++bits;
   const int items = (D / 4) << bits;  // item n: row n % 2^bits, channels 4 (n >> bits) .. + 3
@@ -583,6 +600,80 @@ __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, 
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D + 4 * quad) =
         make_uint2(pack2<DT>(j.o[0] * inv, j.o[1] * inv), pack2<DT>(j.o[2] * inv, j.o[3] * inv));
     if (a.lse && quad == 0) a.lse[out_row] = none ? -INFINITY : (j.m + __builtin_amdgcn_logf(j.l)) * kLn2;
+  }
+}
+
+// Up to this many keys a tile is not worth cutting: the join costs what walking over them does.  64
+// requests of up to 300 keys, e4m3: cut 17.6 us, whole 13.1; of up to 500, 16 bits: 18.5 and 15.2; one
+// request of 500: 10.8 and 11.1.  At 768: 16 e4m3 requests of up to 700 keys, cut 11.6, whole 14.5.
+constexpr int kWholeKeys = 512;
+
+
+// Runs `run(unit)` for the calling workgroup's share of the batch: the batch's work as one line of
+// steps of STEP keys, head by head, request by request, in tiles of SIZE rows, cut into one equal
+// stretch for each workgroup: a stretch may end one tile, hold others whole and begin the next.
+// Where there are few steps and no tile has more than kWholeKeys, a tile is one step and stays whole.
+// Without cuts a workgroup takes a whole tile.  `ends`: kMaxSplitBatch + 4 integers of LDS.
+template <int SIZE, int STEP, typename Run>
+__device__ __forceinline__ void walk_few(const AttnArgs& a, bool split, int* ends, Run run) {
+  constexpr int kLeast = kMinKeys > STEP ? kMinKeys / STEP : 1;
+  const int lane = threadIdx.x & 63;
+  Sums<true> sums(a, ends);
+  int step_keys = STEP, least = kLeast;
+  auto make = [&] {
+    sums.make(a, [&](const Request& q) {
+      const Shape s = shape_of<SIZE>(a, q, step_keys);
+      return s.tiles * s.steps;
+    });
+  };
+  if (split) {
+    make();
+    auto longer = [&] {
+      const Shape s = shape_of<SIZE>(a, sums.lane_request, STEP);
+      return lane < a.batch && s.tiles > 0 && s.steps * STEP > kWholeKeys;
+    };
+    if (a.batch <= 64 && sums.total * a.hk <= 2 * static_cast<int>(gridDim.x) && !__any(longer())) {
+      step_keys = 1 << 30;
+      least = 1;
+      make();
+    }
+  }
+  const int total = split ? sums.total * a.hk : gridDim.x;
+  const int each = split ? max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), least) : 1;
+  const int to = min(total, static_cast<int>(blockIdx.x + 1) * each);
+  for (int from = static_cast<int>(blockIdx.x) * each; from < to;) {
+    Unit unit;
+    int n = 1;
+    if (split) {
+      unit.head = from / sums.total;
+      int end;
+      const int x = from - unit.head * sums.total;
+      const int i = sums.find(a.batch, x, end);
+      const Request q = sums.request(a, i);
+      const Shape s = shape_of<SIZE>(a, q, step_keys);
+      const int steps = s.steps, local = x - (end - s.tiles * steps), tile = local / steps, step = local - tile * steps;
+      n = min(to - from, steps - step);
+      unit.r = rows_of(a, i, q, tile, SIZE);
+      tile_keys(a, unit.r, SIZE, unit.j0, unit.j1);
+      unit.j0 = max(unit.j0, s.low + step * step_keys);
+      unit.j1 = min(unit.j1, s.low + (step + n) * step_keys);
+      // the tile's pieces: a workgroup has at most two partial results, of its first tile and its last
+      const int begin = from - step, first = begin / each, last = (begin + steps - 1) / each;
+      unit.piece = static_cast<int>(blockIdx.x) - first;
+      unit.count = last - first + 1;
+      unit.slot0 = 2 * first + (begin == first * each ? 0 : 1);
+      unit.slot1 = 2 * (first + 1);
+      unit.slot_step = 2;
+    } else {
+      unit.head = blockIdx.x % a.hk;
+      if (!find_rows(a, blockIdx.x / a.hk, SIZE, true, unit.r)) return;
+      tile_keys(a, unit.r, SIZE, unit.j0, unit.j1);
+      unit.piece = 0;
+      unit.count = 1;
+    }
+    run(unit);
+    from += n;
+    if (from < to) __syncthreads();   // before the next tile takes the LDS over
   }
 }
 
@@ -670,17 +761,42 @@ __device__ __forceinline__ v16f mfma_odd(const v8s& v, const float (&z)[8], uint
   return o;
 }
 
+// The same for a tile of 16 channels and 16 rows, 32 keys at a time (16x16x32).
+template <int DT>
+__device__ __forceinline__ v4f mfma16(const v8s& a, const v8s& b, const v4f& c) {
+  if constexpr (DT == DT_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+template <int DT>
+__device__ __forceinline__ v4f mfma16_odd(const v8s& v, const v8s& p, uint32_t seen, v4f o) {
+  o = mfma16<DT>(Odd<DT>::without(v), p, o);
+  const v8s ones = Odd<DT>::ones(seen);
+#pragma unroll 1
+  for (int kind = 0; kind < 3; ++kind) {
+    const v4f n = mfma16<DT>(Odd<DT>::is(v, kind), ones, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+    const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __uint_as_float(kCanonicalNaN);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] += n[i] > 0.0f ? add : 0.0f;
+  }
+  return o;
+}
+
 // Host side: workgroups of a launch for many rows and for few, and the launches.
 inline int64_t tile_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, bool split) {
   return (tile_bound(tokens, group, batch, 128) + (split ? extra_units(hk) : 0)) * hk;
 }
-inline int64_t few_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, int64_t capacity, bool split) {
-  const int64_t tiles = tile_bound(tokens, group, batch, 32) * hk, pieces = tiles * ((capacity + kMinKeys - 1) / kMinKeys);
+inline int64_t few_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, int64_t capacity, bool split, int size = 32) {
+  const int64_t tiles = tile_bound(tokens, group, batch, size) * hk, pieces = tiles * ((capacity + kMinKeys - 1) / kMinKeys);
   if (!split) return tiles;
   return pieces < kFewGroups ? pieces : kFewGroups;   // no more than the pieces have work
 }
-void launch_attn_tile(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
+// Over an mxfp4 cache the kernel for few rows takes 16 or 32 at a time.
+inline int mx4_rows(int64_t tokens, int64_t group, int64_t batch) { return tokens * group <= 16 * batch ? 16 : 32; }
+void launch_attn_tile(int dt, int head_dim, int format, const AttnArgs& a, hipStream_t s);
 void launch_attn_few(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
+void launch_attn_mx4_few(int dt, int head_dim, const AttnArgs& a, hipStream_t s);
 void launch_attn_join(int dt, int head_dim, const AttnArgs& a, hipStream_t s);   // after launch_attn_tile's
 
 }  // namespace attn

@@ -53,7 +53,7 @@ __device__ __forceinline__ bool unit_of(const AttnArgs& a, bool split, char* lds
 template <int DT, int D, int SRC>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, bool split) {
   constexpr int kPlanes = D / 64, kTile = kPlanes * kPlane, kSteps = D / 16;
-  constexpr bool kPaged = SRC != SRC_PACKED, kCodes = SRC == SRC_E4M3, kSplit = splits_scale(DT, kCodes);
+  constexpr bool kPaged = SRC != SRC_PACKED, kCodes = SRC == SRC_E4M3, kMx4 = SRC == SRC_MXFP4, kSplit = splits_scale(DT, kCodes);
   __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];   // K, K, V, V
   __shared__ __attribute__((aligned(16))) float kscale[kCodes ? 4 : 1][kKeys], vscale[kCodes ? 2 : 1][kKeys];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -82,10 +82,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const v8s*>(qp + 16 * s + 8 * half);
 
     // A tile into LDS: this wave brings keys 16 wave .. 16 wave + 15, 16-bit ones by DMA, codes
-    // through registers, where they are converted (exactly) once for all four waves.
+    // through registers, where they are converted once for all four waves (e4m3 exactly, without the
+    // scale; e2m1 with it, to the 16-bit numbers that the format's definition has).
     const uint32_t base = lds_addr(lds);
     uint32_t koff[2], voff[2];
-    if constexpr (!kCodes) {
+    if constexpr (!kCodes && !kMx4) {
       const uint32_t kb = kPaged ? D * 2 : static_cast<uint32_t>(a.kts * 2), vb = kPaged ? D * 2 : static_cast<uint32_t>(a.vts * 2);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -120,15 +121,27 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
         for (int x = 0; x < kPlanes; ++x)
           dma16(rs, base + buffer * kTile + x * kPlane + (2 * wave + g) * 1024, off[g] + x * 128);
     };
-    // codes in flight: a lane's D / 4 bytes of one key and one scale
+    // codes in flight: a lane's D / 4 channels of one key and one scale
     struct Codes {
-      v4i c[kPlanes];
+      v4i c[kMx4 ? 1 : kPlanes];
       float s;
     };
-    auto fetch = [&](const void* p, const float* sp, const Place& at, Codes& to) {
+    auto fetch = [&](const void* p, const void* sp, const Place& at, Codes& to) {
       auto buffer = [&](const void* q, int each) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(q)) + at.row * each, 0, at.n * each, kRsrcWord3);
       };
+      if constexpr (kMx4) {      // 32 channels are a scale's block
+        const auto rc = buffer(p, D / 2);
+        if constexpr (D == 128) {
+          to.c[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, lane * 16, 0, 0);
+        } else {
+          const auto x = __builtin_amdgcn_raw_buffer_load_b64(rc, lane * 8, 0, 0);
+          to.c[0][0] = x[0];
+          to.c[0][1] = x[1];
+        }
+        to.s = mx4_power(__builtin_amdgcn_raw_buffer_load_b8(buffer(sp, D / 32), D == 128 ? lane : lane >> 1, 0, 0));
+        return;
+      }
       const auto rc = buffer(p, D);
 #pragma unroll
       for (int x = 0; x < kPlanes; ++x) to.c[x] = __builtin_amdgcn_raw_buffer_load_b128(rc, lane * (D / 4) + 16 * x, 0, 0);
@@ -137,6 +150,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     auto put = [&](auto value, const Codes& from, int buffer, float* to_scale) {
       constexpr bool SPLIT = kSplit && decltype(value)::value;   // a value's power of two goes to its codes
       const int key = 16 * wave + (lane >> 2);
+      if constexpr (kMx4) {
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          const int c = (lane & 3) * (D / 32) + x;         // chunk of eight channels
+          *reinterpret_cast<v4u*>(lds + buffer * kTile + (c >> 3) * kPlane + key * 128 + (((c & 7) ^ gemm::swz(key & 15)) << 4)) =
+              mx4_values8<DT>(from.c[0][x], from.s);
+        }
+        return;
+      }
       float power = 1.0f, scale = from.s;
       if constexpr (SPLIT) {
         const SplitScale y = split_scale(scale);
@@ -263,7 +285,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       const Place at0 = place(j0, page_of(j0));
       Place at1 = place(j0 + kKeys, page_of(j0 + kKeys));   // of the tile whose V comes next
       int page = page_of(j0 + 2 * kKeys);                   // of the tile whose K comes next
-      if constexpr (kCodes) {
+      if constexpr (kCodes || kMx4) {
         Codes first;
         fetch(a.k, a.ks, at0, first);
         fetch(a.k, a.ks, at1, ck);
@@ -294,9 +316,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       auto step = [&](auto parity, v16f (&s)[2], v16f (&next)[2]) {
         constexpr int B = decltype(parity)::value;      // tile i's buffer
         wait_lds_reads();
-        if constexpr (!kCodes) wait_vmcnt<0>();
+        if constexpr (!kCodes && !kMx4) wait_vmcnt<0>();
         stage_barrier();
-        if constexpr (kCodes) {
+        if constexpr (kCodes || kMx4) {
           put(std::false_type{}, ck, B, kscale[kCodes ? (tile + 2) & 3 : 0]);
           put(std::true_type{}, cv, 2 + (B ^ 1), vscale[kCodes ? B ^ 1 : 0]);
           const Place at = place(t + 3 * kKeys, page);
@@ -365,7 +387,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           const Place at = place(t, page_of(t));
           wait_lds_reads();
           stage_barrier();
-          if constexpr (kCodes) {
+          if constexpr (kCodes || kMx4) {
             Codes codes;
             fetch(a.k, a.ks, at, codes);
             put(std::false_type{}, codes, 0, kscale[0]);
@@ -472,8 +494,10 @@ void launch_typed(int dt, int head_dim, const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-void launch_attn_tile(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s) {
-  e4m3 ? launch_typed<SRC_E4M3>(dt, head_dim, a, s) : launch_typed<SRC_PAGED>(dt, head_dim, a, s);
+void launch_attn_tile(int dt, int head_dim, int format, const AttnArgs& a, hipStream_t s) {
+  if (format == FP8_KV_E4M3) launch_typed<SRC_E4M3>(dt, head_dim, a, s);
+  else if (format == FP8_KV_MXFP4) launch_typed<SRC_MXFP4>(dt, head_dim, a, s);
+  else launch_typed<SRC_PAGED>(dt, head_dim, a, s);
 }
 
 }  // namespace attn

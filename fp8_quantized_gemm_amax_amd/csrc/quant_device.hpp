@@ -97,4 +97,67 @@ struct GroupScale {
   }
 };
 
+// Eight float32 values -> eight e4m3 codes.  The fast quotient wants a scale of at least 2^-60 here:
+// a float32 value has 24 bits, and the remainder of its quotient must not reach the subnormal numbers.
+__device__ __forceinline__ bool fast_scale_f32(float s) { return s >= 0x1p-60f && s <= 3.40282347e38f; }
+__device__ __forceinline__ uint2 enc8_f32(const float (&x)[8], float s, float r, bool fast) {
+  if (fast)
+    return make_uint2(cvt4(quot_fast(x[0], s, r), quot_fast(x[1], s, r), quot_fast(x[2], s, r), quot_fast(x[3], s, r)),
+                      cvt4(quot_fast(x[4], s, r), quot_fast(x[5], s, r), quot_fast(x[6], s, r), quot_fast(x[7], s, r)));
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = e4m3_encode(x[i] / s);
+  return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+}
+
+// ------------------------------------------------------------------------------------
+// e2m1 codes with a power-of-two scale for 32 values (OCP MX, FP4).  A magnitude key is the bits of
+// |x| as float32; NaN sorts above infinity, which sorts above the rest.
+
+// The scale byte s of a block whose largest key is `key`: 2^(s - 127) the smallest power of two from
+// 2^-127 not below amax / 6; 127 for a block of zeros, 255 for one with a value that is not finite.
+// Integer work on amax = (1 + f) 2^E: 6 = 1.5 * 2^2, so E - 2 where 1 + f <= 1.5 and E - 1 above.
+__device__ __forceinline__ uint32_t mx4_scale(uint32_t key) {
+  if (key >= 0x7f800000u) return 255u;
+  if (key == 0u) return 127u;
+  return static_cast<uint32_t>(max(static_cast<int>(key >> 23) - 2 + ((key & 0x7fffffu) > 0x400000u ? 1 : 0), 0));
+}
+
+// The largest code's value: 6, or 3 where 4 times the scale is past the 16-bit type's range (2^14 with
+// fp16, 2^126 with bf16), which rounding would reach from 3.5.
+template <int DT>
+__device__ __forceinline__ float mx4_limit(uint32_t s) {
+  return s >= (DT == DT_BF16 ? 127u + 126 : 127u + 14) ? 3.0f : 6.0f;
+}
+
+// Eight float32 values -> eight codes in one dword, the first in the low bits: round to nearest even
+// on the grid 0, 0.5, 1, 1.5, 2, 3, 4, 6.  The product with the power of two is exact, or so small
+// that the code is 0.
+template <int DT>
+__device__ __forceinline__ uint32_t enc8_mx4(const float (&x)[8], uint32_t s) {
+  if (s == 255u) return 0u;
+  const float r = __uint_as_float((254u - s) << 23), top = mx4_limit<DT>(s);
+  uint32_t w = 0;
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(x[i] * r, -top, top);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[0], y[1], 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[4], y[5], 1.0f, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[6], y[7], 1.0f, 3);
+}
+
+// Eight 16-bit inputs as float32.
+template <int DT>
+__device__ __forceinline__ void widen8(const U4& v, float (&x)[8]) {
+  x[0] = lo16<DT>(v.x); x[1] = hi16<DT>(v.x); x[2] = lo16<DT>(v.y); x[3] = hi16<DT>(v.y);
+  x[4] = lo16<DT>(v.z); x[5] = hi16<DT>(v.z); x[6] = lo16<DT>(v.w); x[7] = hi16<DT>(v.w);
+}
+
+// Max over each aligned group of four lanes.
+__device__ __forceinline__ uint32_t max4(uint32_t v) {
+  v = max(v, dpp_u32<0xB1>(v));    // quad_perm [1,0,3,2]
+  return max(v, dpp_u32<0x4E>(v));   // quad_perm [2,3,0,1]
+}
+
 }  // namespace fp8amax

@@ -34,16 +34,30 @@ struct AppendArgs {
   int64_t n_slots;
   int page_shift;
   void *kc, *vc;
-  float *ks, *vs;
+  void *ks, *vs;                // float32 (e4m3) or e8m0 bytes (mxfp4)
 };
 int64_t kv_append_groups(int64_t tokens, int64_t heads, int head_dim);   // workgroups of the launch
-void launch_kv_append(int dt, int head_dim, bool e4m3, const AppendArgs& a, hipStream_t s);
+void launch_kv_append(int dt, int head_dim, int format, const AppendArgs& a, hipStream_t s);
+
+// The rotation of queries and keys, and the append of keys and values.
+struct RopeArgs {
+  AppendArgs kv;
+  const void* q;
+  void* q_out;
+  int64_t qts, qhs;
+  int q_heads;
+  const int* positions;
+  const float* cos_sin;
+  int n_positions, rotary;
+};
+int64_t rope_append_groups(int64_t tokens, int64_t q_heads, int64_t kv_heads, int head_dim);
+void launch_rope_append(int dt, int head_dim, int format, bool interleaved, const RopeArgs& a, hipStream_t s);
 
 // Attention over packed prompts (table == nullptr: k and v strided tensors of the same tokens)
 // or over a paged cache.
 struct AttnArgs {
   const void *q, *k, *v;
-  const float *ks, *vs;         // e4m3 caches only
+  const void *ks, *vs;          // float32 (e4m3 caches), e8m0 bytes (mxfp4)
   const int *cu, *table, *lens; // table, lens: paged only
   void* out;
   float* lse;                   // may be null
@@ -55,9 +69,9 @@ struct AttnArgs {
   float scale;
 };
 void launch_attn_prompt(int dt, int head_dim, const AttnArgs& a, hipStream_t s);
-void launch_attn_paged(int dt, int head_dim, bool e4m3, int max_new, const AttnArgs& a, hipStream_t s);
+void launch_attn_paged(int dt, int head_dim, int format, int max_new, const AttnArgs& a, hipStream_t s);
 int64_t attn_prompt_groups(int64_t tokens, int64_t batch, int64_t hq, int64_t hk);   // workgroups of the launch
-int64_t attn_paged_groups(bool e4m3, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int64_t capacity, int64_t max_new);
+int64_t attn_paged_groups(int format, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int64_t capacity, int64_t max_new);
 int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
                              int64_t max_new);
 

@@ -17,7 +17,7 @@ constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;   // workgroups of 256 th
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool valid_dt(fp8_dtype_t dt) { return dt == FP8_BF16 || dt == FP8_F16; }
-bool valid_format(fp8_kv_format_t f) { return f == FP8_KV_SAME || f == FP8_KV_E4M3; }
+bool valid_format(fp8_kv_format_t f) { return f == FP8_KV_SAME || f == FP8_KV_E4M3 || f == FP8_KV_MXFP4; }
 bool valid_dim(int32_t d) { return d == 64 || d == 128; }
 bool valid_page(int32_t p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 int shift_of(int32_t p) { return __builtin_ctz(static_cast<unsigned>(p)); }
@@ -49,6 +49,32 @@ fp8_status_t check_heads(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, 
   if (!std::isfinite(scale) || scale <= 0.0f || window < 0) return FP8_ERR_BAD_SHAPE;
   if (tokens > kMaxInt || batch > kMaxInt || hq > 65535) return FP8_ERR_TOO_LARGE;
   if (tokens * hq > kMaxInt / 2 || batch * hq > kMaxInt / 2) return FP8_ERR_TOO_LARGE;   // rows and tiles are indexed with int
+  return FP8_OK;
+}
+
+// The arguments of an append (FP8_OK: `a` is filled, or there are no tokens).
+fp8_status_t check_append(const void* k, const void* v, fp8_dtype_t dt, int64_t tokens, int64_t kv_heads, int32_t head_dim,
+                          int64_t kts, int64_t khs, int64_t vts, int64_t vhs, const int64_t* slots, int64_t pages,
+                          int32_t page_size, fp8_kv_format_t format, void* k_cache, void* v_cache, void* k_scales,
+                          void* v_scales, fp8amax::AppendArgs& a) {
+  if (tokens < 0 || kv_heads < 1 || !valid_dim(head_dim)) return FP8_ERR_BAD_SHAPE;
+  if (tokens > kMaxInt || kv_heads > 65535 || tokens * kv_heads > kMaxInt / 2) return FP8_ERR_TOO_LARGE;
+  if (!valid_dt(dt) || !valid_format(format)) return FP8_ERR_BAD_DTYPE;
+  fp8_status_t st = check_cache(pages, kv_heads, head_dim, page_size);
+  if (st == FP8_OK) st = check_strides(tokens, kv_heads, kts, khs);
+  if (st == FP8_OK) st = check_strides(tokens, kv_heads, vts, vhs);
+  if (st != FP8_OK) return st;
+  if (tokens == 0) return FP8_OK;
+  if (fp8amax::kv_append_groups(tokens, kv_heads, head_dim) > kMaxGroups) return FP8_ERR_TOO_LARGE;
+  const bool scaled = format != FP8_KV_SAME;
+  if (!k || !v || !slots || !k_cache || !v_cache || (scaled && (!k_scales || !v_scales))) return FP8_ERR_NULL_POINTER;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8) ||
+      (scaled && (!aligned(k_scales, 4) || !aligned(v_scales, 4))))
+    return FP8_ERR_MISALIGNED;
+  a.k = k; a.v = v; a.kts = kts; a.khs = khs; a.vts = vts; a.vhs = vhs;
+  a.tokens = static_cast<int>(tokens); a.heads = static_cast<int>(kv_heads);
+  a.slots = slots; a.n_slots = pages * page_size; a.page_shift = shift_of(page_size);
+  a.kc = k_cache; a.vc = v_cache; a.ks = k_scales; a.vs = v_scales;
   return FP8_OK;
 }
 
@@ -99,29 +125,43 @@ fp8_status_t fp8_paged_plan(const int32_t* cached, const int32_t* added, int64_t
 fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t tokens, int64_t kv_heads,
                            int32_t head_dim, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
                            int64_t v_head_stride, const int64_t* slots, int64_t pages, int32_t page_size,
-                           fp8_kv_format_t format, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                           fp8_kv_format_t format, void* k_cache, void* v_cache, void* k_scales, void* v_scales,
                            void* stream) {
-  if (tokens < 0 || kv_heads < 1 || !valid_dim(head_dim)) return FP8_ERR_BAD_SHAPE;
-  if (tokens > kMaxInt || kv_heads > 65535 || tokens * kv_heads > kMaxInt / 2) return FP8_ERR_TOO_LARGE;
-  if (!valid_dt(dt) || !valid_format(format)) return FP8_ERR_BAD_DTYPE;
-  fp8_status_t st = check_cache(pages, kv_heads, head_dim, page_size);
-  if (st == FP8_OK) st = check_strides(tokens, kv_heads, k_token_stride, k_head_stride);
-  if (st == FP8_OK) st = check_strides(tokens, kv_heads, v_token_stride, v_head_stride);
-  if (st != FP8_OK) return st;
-  if (tokens == 0) return FP8_OK;
-  if (fp8amax::kv_append_groups(tokens, kv_heads, head_dim) > kMaxGroups) return FP8_ERR_TOO_LARGE;
-  const bool e4m3 = format == FP8_KV_E4M3;
-  if (!k || !v || !slots || !k_cache || !v_cache || (e4m3 && (!k_scales || !v_scales))) return FP8_ERR_NULL_POINTER;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8) ||
-      (e4m3 && (!aligned(k_scales, 4) || !aligned(v_scales, 4))))
-    return FP8_ERR_MISALIGNED;
   fp8amax::AppendArgs a{};
-  a.k = k; a.v = v; a.kts = k_token_stride; a.khs = k_head_stride; a.vts = v_token_stride; a.vhs = v_head_stride;
-  a.tokens = static_cast<int>(tokens); a.heads = static_cast<int>(kv_heads);
-  a.slots = slots; a.n_slots = pages * page_size; a.page_shift = shift_of(page_size);
-  a.kc = k_cache; a.vc = v_cache; a.ks = k_scales; a.vs = v_scales;
+  const fp8_status_t st = check_append(k, v, dt, tokens, kv_heads, head_dim, k_token_stride, k_head_stride, v_token_stride,
+                                       v_head_stride, slots, pages, page_size, format, k_cache, v_cache, k_scales, v_scales, a);
+  if (st != FP8_OK || tokens == 0) return st;
   (void)hipGetLastError();
-  fp8amax::launch_kv_append(static_cast<int>(dt), head_dim, e4m3, a, static_cast<hipStream_t>(stream));
+  fp8amax::launch_kv_append(static_cast<int>(dt), head_dim, format, a, static_cast<hipStream_t>(stream));
+  return finish_launch();
+}
+
+fp8_status_t fp8_rope_append(const void* q, const void* k, const void* v, fp8_dtype_t dt, int64_t tokens,
+                             int64_t q_heads, int64_t kv_heads, int32_t head_dim, int64_t q_token_stride,
+                             int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, const int32_t* positions,
+                             const float* cos_sin, int64_t n_positions, int32_t rotary_dim, int32_t interleaved,
+                             const int64_t* slots, int64_t pages, int32_t page_size, fp8_kv_format_t format,
+                             void* k_cache, void* v_cache, void* k_scales, void* v_scales, void* q_out,
+                             void* stream) {
+  if (q_heads < 0 || n_positions < 0 || !valid_dim(head_dim) || rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0)
+    return FP8_ERR_BAD_SHAPE;
+  if (n_positions > kMaxInt || q_heads > 65535) return FP8_ERR_TOO_LARGE;
+  fp8amax::RopeArgs a{};
+  fp8_status_t st = check_append(k, v, dt, tokens, kv_heads, head_dim, k_token_stride, k_head_stride, v_token_stride,
+                                 v_head_stride, slots, pages, page_size, format, k_cache, v_cache, k_scales, v_scales, a.kv);
+  if (st != FP8_OK) return st;
+  if (q_heads > 0 && (st = check_strides(tokens, q_heads, q_token_stride, q_head_stride)) != FP8_OK) return st;
+  if (tokens * q_heads > kMaxInt / 2) return FP8_ERR_TOO_LARGE;
+  if (tokens == 0) return FP8_OK;
+  if (fp8amax::rope_append_groups(tokens, q_heads, kv_heads, head_dim) > kMaxGroups) return FP8_ERR_TOO_LARGE;
+  if (!positions || (n_positions > 0 && !cos_sin) || (q_heads > 0 && (!q || !q_out))) return FP8_ERR_NULL_POINTER;
+  if (!aligned(positions, 4) || !aligned(cos_sin, 16) || (q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))))
+    return FP8_ERR_MISALIGNED;
+  a.q = q; a.q_out = q_out; a.qts = q_token_stride; a.qhs = q_head_stride; a.q_heads = static_cast<int>(q_heads);
+  a.positions = positions; a.cos_sin = cos_sin; a.n_positions = static_cast<int>(n_positions); a.rotary = rotary_dim;
+  (void)hipGetLastError();
+  fp8amax::launch_rope_append(static_cast<int>(dt), head_dim, format, interleaved != 0, a, static_cast<hipStream_t>(stream));
   return finish_launch();
 }
 
@@ -168,7 +208,7 @@ int64_t fp8_attn_paged_workspace(int64_t tokens, int64_t batch, int64_t q_heads,
 fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const int32_t* cu_tokens, int64_t batch,
                             int64_t q_heads, int64_t kv_heads, int32_t head_dim, int64_t q_token_stride,
                             int64_t q_head_stride, fp8_kv_format_t format, const void* k_cache, const void* v_cache,
-                            const float* k_scales, const float* v_scales, int64_t pages, int32_t page_size,
+                            const void* k_scales, const void* v_scales, int64_t pages, int32_t page_size,
                             const int32_t* block_table, int64_t width, const int32_t* seq_lens, float softmax_scale,
                             int64_t window, int64_t max_new, void* out, float* lse, void* workspace,
                             int64_t workspace_bytes, void* stream) {
@@ -180,17 +220,17 @@ fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const
   if (width > kMaxKeys / page_size || (batch > 0 && width > kMaxElems / batch)) return FP8_ERR_TOO_LARGE;
   if ((st = check_strides(tokens, q_heads, q_token_stride, q_head_stride)) != FP8_OK) return st;
   if (tokens == 0 || batch == 0) return FP8_OK;
-  const bool e4m3 = format == FP8_KV_E4M3;
-  if (fp8amax::attn_paged_groups(e4m3, tokens, batch, q_heads, kv_heads, width * page_size, max_new) > kMaxGroups)
+  const bool scaled = format != FP8_KV_SAME;
+  if (fp8amax::attn_paged_groups(format, tokens, batch, q_heads, kv_heads, width * page_size, max_new) > kMaxGroups)
     return FP8_ERR_TOO_LARGE;
   const int64_t need = fp8amax::attn_paged_workspace(tokens, batch, q_heads, kv_heads, head_dim, width * page_size, max_new);
   if (workspace_bytes < need) return FP8_ERR_BAD_SHAPE;
   if (!q || !cu_tokens || !k_cache || !v_cache || !block_table || !seq_lens || !out || (need > 0 && !workspace) ||
-      (e4m3 && (!k_scales || !v_scales)))
+      (scaled && (!k_scales || !v_scales)))
     return FP8_ERR_NULL_POINTER;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(workspace, 16) || !aligned(cu_tokens, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
-      !aligned(lse, 4) || (e4m3 && (!aligned(k_scales, 4) || !aligned(v_scales, 4))))
+      !aligned(lse, 4) || (scaled && (!aligned(k_scales, 4) || !aligned(v_scales, 4))))
     return FP8_ERR_MISALIGNED;
   fp8amax::AttnArgs a{};
   a.q = q; a.k = k_cache; a.v = v_cache; a.ks = k_scales; a.vs = v_scales;
@@ -202,7 +242,7 @@ fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const
   a.pages = static_cast<int>(pages); a.page_shift = shift_of(page_size); a.width = static_cast<int>(width);
   a.window = window_of(window); a.scale = softmax_scale;
   (void)hipGetLastError();
-  fp8amax::launch_attn_paged(static_cast<int>(dt), head_dim, e4m3, static_cast<int>(max_new > tokens ? tokens : max_new), a,
+  fp8amax::launch_attn_paged(static_cast<int>(dt), head_dim, format, static_cast<int>(max_new > tokens ? tokens : max_new), a,
                              static_cast<hipStream_t>(stream));
   return finish_launch();
 }

@@ -21,6 +21,7 @@ namespace {
 
 decltype(&fp8_paged_plan) plan_fn;
 decltype(&fp8_kv_append) append_fn;
+decltype(&fp8_rope_append) rope_fn;
 decltype(&fp8_attn_prompt) prompt_fn;
 decltype(&fp8_attn_paged) paged_fn;
 decltype(&fp8_attn_paged_workspace) workspace_fn;
@@ -104,24 +105,39 @@ at::Tensor output(PyObject* given, const at::Tensor& q, std::initializer_list<co
   return out;
 }
 
+// Four-bit codes come with scales of one byte for 32 channels: a last index more than e4m3's.
+bool is_byte_scale(at::ScalarType t) { return t == at::kByte || t == at::kFloat8_e8m0fnu; }
+
 struct Cache {
   at::Tensor k, v, ks, vs;
   fp8_kv_format_t format;
+  int64_t dim;      // channels
 };
 Cache cache_of(PyObject* k, PyObject* v, PyObject* ks, PyObject* vs, at::ScalarType type) {
-  Cache c{tensor(k, "k_cache"), tensor(v, "v_cache"), {}, {}, FP8_KV_SAME};
+  Cache c{tensor(k, "k_cache"), tensor(v, "v_cache"), {}, {}, FP8_KV_SAME, 0};
   TORCH_CHECK_VALUE(c.k.dim() == 4, "k_cache must be [pages, kv_heads, page_size, head_dim], got ", shape_of(c.k));
   const auto kind = c.k.scalar_type();
   dense(c.k, "k_cache", kind, c.k.sizes());
   dense(c.v, "v_cache", kind, c.k.sizes());
+  c.dim = c.k.size(3);
   TORCH_CHECK_VALUE((ks == Py_None) == (vs == Py_None), "k_scales and v_scales go together");
   if (ks == Py_None) {
     TORCH_CHECK_TYPE(kind == type, "a cache without scales must be ", type, ", got ", kind);
     return c;
   }
-  TORCH_CHECK_TYPE(kind == at::kByte || kind == at::kFloat8_e4m3fn, "a cache with scales must be uint8 or float8_e4m3fn, got ", kind);
   c.ks = tensor(ks, "k_scales");
   c.vs = tensor(vs, "v_scales");
+  const auto scale = c.ks.scalar_type();
+  if (is_byte_scale(scale)) {
+    TORCH_CHECK_TYPE(kind == at::kByte || kind == at::kFloat4_e2m1fn_x2, "a cache with scales of a byte must be uint8 or float4_e2m1fn_x2, got ", kind);
+    c.dim = 2 * c.k.size(3);
+    const int64_t shape[4] = {c.k.size(0), c.k.size(1), c.k.size(2), c.dim / 32};
+    dense(c.ks, "k_scales", scale, shape);
+    dense(c.vs, "v_scales", scale, shape);
+    c.format = FP8_KV_MXFP4;
+    return c;
+  }
+  TORCH_CHECK_TYPE(kind == at::kByte || kind == at::kFloat8_e4m3fn, "a cache with scales must be uint8 or float8_e4m3fn, got ", kind);
   dense(c.ks, "k_scales", at::kFloat, c.k.sizes().slice(0, 3));
   dense(c.vs, "v_scales", at::kFloat, c.k.sizes().slice(0, 3));
   c.format = FP8_KV_E4M3;
@@ -129,9 +145,10 @@ Cache cache_of(PyObject* k, PyObject* v, PyObject* ks, PyObject* vs, at::ScalarT
 }
 void on_cache(const at::Tensor& like, const Cache& c) {
   on(like, {{&c.k, "k_cache"}, {&c.v, "v_cache"}});
-  if (c.format == FP8_KV_E4M3) on(like, {{&c.ks, "k_scales"}, {&c.vs, "v_scales"}});
+  if (c.format != FP8_KV_SAME) on(like, {{&c.ks, "k_scales"}, {&c.vs, "v_scales"}});
 }
 
+void* raw(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 template <typename T>
 T* ptr(const at::Tensor& t) { return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr; }
 
@@ -229,7 +246,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   TORCH_CHECK_VALUE(v0.scalar_type() == k0.scalar_type() && v0.sizes() == k0.sizes(), "v must be like k, got ", v0.scalar_type(), " ", shape_of(v0), " and ",
                     k0.scalar_type(), " ", shape_of(k0));
   const Cache c = cache_of(a[3], a[4], a[5], a[6], k0.scalar_type());
-  const int64_t heads = c.k.size(1), dim = c.k.size(3), page = c.k.size(2);
+  const int64_t heads = c.k.size(1), dim = c.dim, page = c.k.size(2);
   const at::Tensor k = rows(k0, "k", dim), v = rows(v0, "v", dim);
   TORCH_CHECK_VALUE(k.size(1) == heads, "k has ", k.size(1), " heads, the cache ", heads);
   const at::Tensor slots = vec(tensor(a[2], "slots"), "slots", at::kLong, k.size(0));
@@ -239,8 +256,67 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   on_cache(k, c);
   const c10::DeviceGuard guard(k.device());   // the launch goes to the tensors' GPU
   return status(append_fn(k.data_ptr(), v.data_ptr(), dt, k.size(0), heads, static_cast<int32_t>(dim), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                          ptr<int64_t>(slots), c.k.size(0), static_cast<int32_t>(page), c.format, c.k.data_ptr(), c.v.data_ptr(), ptr<float>(c.ks),
-                          ptr<float>(c.vs), stream_of(a[7])));
+                          ptr<int64_t>(slots), c.k.size(0), static_cast<int32_t>(page), c.format, c.k.data_ptr(), c.v.data_ptr(), raw(c.ks),
+                          raw(c.vs), stream_of(a[7])));
+  END_HANDLE_TH_ERRORS
+}
+
+// q (or None), k, v, positions, cos_sin, slots, k_cache, v_cache, k_scales, v_scales, interleaved, out, stream
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  ARGS(13);
+  const at::Tensor& k0 = tensor(a[1], "k");
+  const at::Tensor& v0 = tensor(a[2], "v");
+  const fp8_dtype_t dt = dtype_of(k0, "k");
+  TORCH_CHECK_VALUE(v0.scalar_type() == k0.scalar_type() && v0.sizes() == k0.sizes(), "v must be like k, got ", v0.scalar_type(), " ", shape_of(v0), " and ",
+                    k0.scalar_type(), " ", shape_of(k0));
+  const Cache c = cache_of(a[6], a[7], a[8], a[9], k0.scalar_type());
+  const int64_t heads = c.k.size(1), dim = c.dim, page = c.k.size(2);
+  const at::Tensor k = rows(k0, "k", dim), v = rows(v0, "v", dim);
+  TORCH_CHECK_VALUE(k.size(1) == heads, "k has ", k.size(1), " heads, the cache ", heads);
+  const int64_t tokens = k.size(0);
+  const bool with_q = a[0] != Py_None;
+  TORCH_CHECK_VALUE(with_q || a[11] == Py_None, "out goes with q");
+  at::Tensor q;
+  if (with_q) {
+    const at::Tensor& q0 = tensor(a[0], "q");
+    TORCH_CHECK_TYPE(q0.scalar_type() == k0.scalar_type(), "q must be of k's type, got ", q0.scalar_type(), " and ", k0.scalar_type());
+    q = rows(q0, "q", dim);
+    TORCH_CHECK_VALUE(q.size(0) == tokens, "q has ", q.size(0), " tokens, k ", tokens);
+  }
+  const at::Tensor positions = vec(tensor(a[3], "positions"), "positions", at::kInt, tokens);
+  const at::Tensor& table = tensor(a[4], "cos_sin");
+  TORCH_CHECK_VALUE(table.dim() == 2, "cos_sin must be [positions, rotary_dim], got ", shape_of(table));
+  dense(table, "cos_sin", at::kFloat, table.sizes());
+  const int64_t rotary = table.size(1);
+  TORCH_CHECK_VALUE(rotary >= 16 && rotary <= dim && rotary % 16 == 0, "rotary_dim must be a multiple of 16, 16 .. ", dim, ", got ", rotary);
+  const at::Tensor slots = vec(tensor(a[5], "slots"), "slots", at::kLong, tokens);
+  for (const at::Tensor* t : {&c.k, &c.v, &c.ks, &c.vs})
+    for (const at::Tensor* in : std::initializer_list<const at::Tensor*>{&q, &k, &v, &positions, &table, &slots})
+      TORCH_CHECK_VALUE(!t->defined() || !in->defined() || !overlaps(*t, *in), "a cache overlaps an input");
+  if (a[11] == Py_None) {
+    on(k, {{&v, "v"}, {&positions, "positions"}, {&table, "cos_sin"}, {&slots, "slots"}});
+    on_cache(k, c);
+    if (with_q) on(k, {{&q, "q"}});
+  }
+  const at::Tensor out = with_q ? output(a[11], q, {&q, &k, &v, &positions, &table, &slots, &c.k, &c.v, &c.ks, &c.vs}) : at::Tensor();
+  if (a[11] != Py_None) {
+    on(k, {{&v, "v"}, {&positions, "positions"}, {&table, "cos_sin"}, {&slots, "slots"}, {&q, "q"}, {&out, "out"}});
+    on_cache(k, c);
+  }
+  const c10::DeviceGuard guard(k.device());   // the launch goes to the tensors' GPU
+  const fp8_status_t code = rope_fn(
+      raw(q), k.data_ptr(), v.data_ptr(), dt, tokens, with_q ? q.size(1) : 0, heads, static_cast<int32_t>(dim), with_q ? q.stride(0) : 0,
+      with_q ? q.stride(1) : 0, k.stride(0), k.stride(1), v.stride(0), v.stride(1), ptr<int32_t>(positions), ptr<float>(table), table.size(0),
+      static_cast<int32_t>(rotary), PyObject_IsTrue(a[10]) == 1, ptr<int64_t>(slots), c.k.size(0), static_cast<int32_t>(page), c.format,
+      c.k.data_ptr(), c.v.data_ptr(), raw(c.ks), raw(c.vs), raw(out), stream_of(a[12]));
+  if (code != FP8_OK) return status(code);
+  if (!with_q) Py_RETURN_NONE;
+  if (a[11] != Py_None) {
+    Py_INCREF(a[11]);
+    return a[11];
+  }
+  return wrap(out);
   END_HANDLE_TH_ERRORS
 }
 
@@ -308,7 +384,7 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const at::Tensor& q0 = tensor(a[0], "q");
   const fp8_dtype_t dt = dtype_of(q0, "q");
   const Cache c = cache_of(a[1], a[2], a[6], a[7], q0.scalar_type());
-  const int64_t pages = c.k.size(0), hk = c.k.size(1), page = c.k.size(2), dim = c.k.size(3);
+  const int64_t pages = c.k.size(0), hk = c.k.size(1), page = c.k.size(2), dim = c.dim;
   const at::Tensor q = rows(q0, "q", dim);
   const int64_t tokens = q.size(0), hq = q.size(1);
   const at::Tensor lens = vec(tensor(a[4], "seq_lens"), "seq_lens", at::kInt, -1);
@@ -339,28 +415,29 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   }
   const c10::DeviceGuard guard(q.device());   // the launch goes to the tensors' GPU
   const fp8_status_t code = paged_fn(q.data_ptr(), dt, tokens, ptr<int32_t>(cu), batch, hq, hk, static_cast<int32_t>(dim), q.stride(0), q.stride(1), c.format,
-                                     c.k.data_ptr(), c.v.data_ptr(), ptr<float>(c.ks), ptr<float>(c.vs), pages, static_cast<int32_t>(page),
+                                     c.k.data_ptr(), c.v.data_ptr(), raw(c.ks), raw(c.vs), pages, static_cast<int32_t>(page),
                                      ptr<int32_t>(tab), width, ptr<int32_t>(lens), s.scale, s.window, most, out.data_ptr(), ptr<float>(lse), ws.data_ptr(),
                                      ws.size(0), stream);
   return code == FP8_OK ? result(out, lse, a[11]) : status(code);
   END_HANDLE_TH_ERRORS
 }
 
-// The addresses of fp8_paged_plan, fp8_kv_append, fp8_attn_prompt, fp8_attn_paged, fp8_attn_paged_workspace.
+// The addresses of fp8_paged_plan, fp8_kv_append, fp8_rope_append, fp8_attn_prompt, fp8_attn_paged, fp8_attn_paged_workspace.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
-  ARGS(5);
+  ARGS(6);
   plan_fn = reinterpret_cast<decltype(plan_fn)>(PyLong_AsVoidPtr(a[0]));
   append_fn = reinterpret_cast<decltype(append_fn)>(PyLong_AsVoidPtr(a[1]));
-  prompt_fn = reinterpret_cast<decltype(prompt_fn)>(PyLong_AsVoidPtr(a[2]));
-  paged_fn = reinterpret_cast<decltype(paged_fn)>(PyLong_AsVoidPtr(a[3]));
-  workspace_fn = reinterpret_cast<decltype(workspace_fn)>(PyLong_AsVoidPtr(a[4]));
+  rope_fn = reinterpret_cast<decltype(rope_fn)>(PyLong_AsVoidPtr(a[2]));
+  prompt_fn = reinterpret_cast<decltype(prompt_fn)>(PyLong_AsVoidPtr(a[3]));
+  paged_fn = reinterpret_cast<decltype(paged_fn)>(PyLong_AsVoidPtr(a[4]));
+  workspace_fn = reinterpret_cast<decltype(workspace_fn)>(PyLong_AsVoidPtr(a[5]));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(paged_plan), METHOD(kv_append), METHOD(attn_prompt), METHOD(attn_paged), METHOD(bind), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(paged_plan), METHOD(kv_append), METHOD(rope_append), METHOD(attn_prompt), METHOD(attn_paged), METHOD(bind), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

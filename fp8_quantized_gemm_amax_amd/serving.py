@@ -18,7 +18,7 @@ import torch
 from . import binding
 from .binding import Fp8Error
 
-FP8_KV_SAME, FP8_KV_E4M3 = 0, 1
+FP8_KV_SAME, FP8_KV_E4M3, FP8_KV_MXFP4 = 0, 1, 4
 COUNTER_BYTES = 16384          # FP8_ATTN_COUNTER_BYTES
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serving.so")
 
@@ -30,6 +30,8 @@ _SIGNATURES = {
     "fp8_paged_plan": ([_P, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "fp8_kv_append": ([_P, _P, ctypes.c_int, _I64, _I64, _I32, _I64, _I64, _I64, _I64, _P, _I64, _I32, ctypes.c_int,
                        _P, _P, _P, _P, _P], ctypes.c_int),
+    "fp8_rope_append": ([_P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I32, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64,
+                         _I32, _I32, _P, _I64, _I32, ctypes.c_int, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "fp8_attn_prompt": ([_P, _P, _P, ctypes.c_int, _I64, _P, _I64, _I64, _I64, _I32, _I64, _I64, _I64, _I64, _I64,
                          _I64, _F32, _I64, _P, _P, _P], ctypes.c_int),
     "fp8_attn_paged": ([_P, ctypes.c_int, _I64, _P, _I64, _I64, _I64, _I32, _I64, _I64, ctypes.c_int, _P, _P, _P, _P,
@@ -118,12 +120,43 @@ def fp8_paged_plan(cached, added, block_table, free_pages, taken, tokens, page_s
 
 def fp8_kv_append(k, v, slots, k_cache, v_cache, k_scales=None, v_scales=None):
     """New keys and values [tokens, kv_heads, head_dim] into their slots (int64 [tokens], -1:
-    skipped) of the caches [pages, kv_heads, page_size, head_dim], in place: of k's type, or
-    e4m3 codes with float32 scales [pages, kv_heads, page_size]."""
+    skipped) of the caches [pages, kv_heads, page_size, head_dim], in place: of k's type;
+    e4m3 codes with float32 scales [pages, kv_heads, page_size]; or 4 bits, e2m1 codes uint8 (or
+    float4_e2m1fn_x2) [.., head_dim / 2], two a byte, with scale bytes uint8 (or float8_e8m0fnu)
+    [pages, kv_heads, page_size, head_dim / 32]."""
     code = (_ext or _load()).kv_append(k, v, slots, k_cache, v_cache, k_scales, v_scales, _stream(k))
     if code:
         _refuse("fp8_kv_append", code)
     return k_cache, v_cache
+
+
+def rope_table(positions, rotary_dim, base=10000.0, device="cuda"):
+    """cos_sin for fp8_rope_append: float32 [positions, rotary_dim], row p the cosines and then the
+    sines of p * base ** (-2 i / rotary_dim).  The angles are formed in float64: a far position's
+    angle has no correct digit after the point in float32.  Tables of other angles (scaled or
+    stretched ones) have the same layout."""
+    if rotary_dim < 2 or rotary_dim % 2 or positions < 0:
+        raise ValueError(f"rotary_dim must be even and positive and positions not negative, got {rotary_dim} and {positions}")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * float(base) ** (-2.0 * i / rotary_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def fp8_rope_append(q, k, v, positions, cos_sin, slots, k_cache, v_cache, k_scales=None, v_scales=None,
+                    interleaved=False, out=None):
+    """fp8_kv_append with the position rotation on the way: q [tokens, q_heads, head_dim] (or None) and
+    k rotated by their tokens' positions (int32 [tokens], as fp8_paged_plan gives them; -1: the token
+    is skipped), k and v into their slots, in one launch.
+
+    cos_sin float32 [n, rotary_dim], row p the cosines and the sines of position p (rope_table);
+    channels i and i + rotary_dim / 2 turn together, with interleaved 2 i and 2 i + 1, those from
+    rotary_dim on stay.  Returns the rotated queries (None without q), dense, in `out` if given;
+    a skipped token's row of them is not written."""
+    r = (_ext or _load()).rope_append(q, k, v, positions, cos_sin, slots, k_cache, v_cache, k_scales, v_scales,
+                                      interleaved, out, _stream(k))
+    if r.__class__ is int:
+        _refuse("fp8_rope_append", r)
+    return r
 
 
 def fp8_attn_prompt(q, k, v, cu_tokens, softmax_scale=None, window=0, out=None, return_lse=False):

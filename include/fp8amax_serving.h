@@ -1,18 +1,27 @@
 /*
  * fp8amax_serving.h - C ABI of what a serving step runs between the FP8 projections: the
- * bookkeeping of a paged key/value cache, the write of new keys and values into it, and
- * causal attention over whole prompts or over the cache, for MI355X (gfx950).  Same library,
+ * bookkeeping of a paged key/value cache, the rotation of queries and keys by their positions,
+ * the write of new keys and values into the cache, and causal attention over whole prompts or
+ * over the cache, for MI355X (gfx950).  Same library,
  * status codes and conventions as fp8amax.h: device pointers owned by the caller, nothing
  * allocated and no state kept, arguments validated on the host before any HIP call, all work
  * enqueued on `stream`, no synchronisation, capturable in a HIP graph.
  *
  * The cache.  K and V each hold `pages` pages of `page_size` tokens,
  *   cache[page][kv_head][token in page][head_dim],
- * in one of two formats:
+ * in one of three formats:
  *   FP8_KV_SAME: the 16-bit type of the new keys and values;
  *   FP8_KV_E4M3: uint8 e4m3fn codes and one float32 scale per token and head,
  *     scales[page][kv_head][token in page]; value = code * scale, with scale and codes by the
- *     rules of fp8amax.h over the head_dim values (scale = amax / 448, 1 for an all-zero row).
+ *     rules of fp8amax.h over the head_dim values (scale = amax / 448, 1 for an all-zero row);
+ *   FP8_KV_MXFP4: e2m1 codes, two a byte (an even channel in the low half), in rows of head_dim / 2
+ *     bytes, and one scale byte s for a token, head and 32 channels, scales[page][kv_head][token in
+ *     page][head_dim / 32]; value = {0, 0.5, 1, 1.5, 2, 3, 4, 6}[code & 7] * 2^(s - 127), negative with
+ *     bit 3 of the code, and NaN with s = 255.  As written: 2^(s - 127) is the smallest power of two
+ *     (from 2^-127) not below a block's amax / 6, 1 (s = 127) for an all-zero block, and each code the
+ *     one nearest to x / 2^(s - 127), ties to the even code; where 4 times the scale is past dt's
+ *     range (a block's amax from 3 / 4 of 2^16 in fp16, of 2^128 in bf16) no larger than 3.  A block that
+ *     holds a value that is not finite has s = 255 and codes 0.
  * A token's slot is page * page_size + (token in page).  Request r's tokens p, p + 1, .. lie in
  * the pages block_table[r][p / page_size] (row-major [batch, width]); entries that name no
  * page of the cache are allowed: what they hold reads as zero and is never written.
@@ -29,14 +38,14 @@
  *
  * Strides.  q, k and v are [tokens, heads, head_dim] with the last index contiguous; the token
  * and head strides are given in elements, non-negative multiples of 8 (so that a fused
- * projection's output is read in place).  Data pointers need 16-byte, int32 and float32
- * pointers 4-byte, int64 pointers 8-byte alignment.
+ * projection's output is read in place).  Data pointers need 16-byte, int32, float32
+ * and scale pointers 4-byte, int64 pointers 8-byte alignment.
  *
  * What a call writes shares no memory with what it reads.
  *
  * Sizes.  FP8_ERR_TOO_LARGE, before any HIP call, where tokens * heads passes 2^30 or the work would
  * need 2^24 workgroups or more (a launch holds less than 2^32 threads): a workgroup appends 16 rows
- * of 128 channels or 32 of 64, and attends for 128 rows or 32 of one request and key head.
+ * of 128 channels or 32 of 64 (with rotation at least as many), and attends for 128 rows or 32 of one request and key head.
  */
 #ifndef FP8AMAX_SERVING_H
 #define FP8AMAX_SERVING_H
@@ -47,7 +56,7 @@
 extern "C" {
 #endif
 
-typedef enum FP8_ENUM_BASE { FP8_KV_SAME = 0, FP8_KV_E4M3 = 1 } fp8_kv_format_t;
+typedef enum FP8_ENUM_BASE { FP8_KV_SAME = 0, FP8_KV_E4M3 = 1, FP8_KV_MXFP4 = 4 } fp8_kv_format_t;
 
 /*
  * fp8_paged_plan - block tables, slots and positions of one step, in one launch, from the
@@ -77,18 +86,47 @@ fp8_status_t fp8_paged_plan(const int32_t* cached, const int32_t* added, int64_t
                             int32_t* positions, int64_t* slots, int32_t* taken_out, int32_t* missing, void* stream);
 
 /*
- * fp8_kv_append - new keys and values into the pages of their slots, as they are or quantized
- * with one scale per token and head, in one launch.
+ * fp8_kv_append - new keys and values into the pages of their slots, as they are or quantized,
+ * in one launch.
  *   k, v    : [tokens, kv_heads, head_dim] of dt, strided.
  *   slots   : int64 [tokens]; a slot outside [0, pages * page_size) is skipped (-1: padding).
  *             Two tokens with one slot leave either's values.
- *   k_cache, v_cache : as above; k_scales, v_scales : float32, FP8_KV_E4M3 only (else NULL).
+ *   k_cache, v_cache : as above; k_scales, v_scales : float32 (FP8_KV_E4M3) or bytes (FP8_KV_MXFP4),
+ *   NULL for FP8_KV_SAME.
  */
 fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t tokens, int64_t kv_heads,
                            int32_t head_dim, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
                            int64_t v_head_stride, const int64_t* slots, int64_t pages, int32_t page_size,
-                           fp8_kv_format_t format, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                           fp8_kv_format_t format, void* k_cache, void* v_cache, void* k_scales, void* v_scales,
                            void* stream);
+
+/*
+ * fp8_rope_append - fp8_kv_append with the position rotation on the way: the queries and keys of a
+ * step rotated by their positions, the queries into q_out, the keys with their values into the
+ * pages of their slots, in one launch.  With R = rotary_dim and row p of the table,
+ *   cos_sin[p] = cos_0 .. cos_(R/2 - 1), sin_0 .. sin_(R/2 - 1),
+ * a token at position p gets, for i < R / 2,
+ *   x'_a = x_a cos_i - x_b sin_i,   x'_b = x_b cos_i + x_a sin_i,
+ *   (a, b) = (i, i + R / 2), or (2 i, 2 i + 1) with interleaved != 0;
+ * channels from R on stay.  Products and sums are float32 (each rounded once); q_out and a cache of
+ * FP8_KV_SAME get the result rounded once to dt, the other formats quantize the float32 result.
+ *   q       : [tokens, q_heads, head_dim] of dt, strided; q_heads may be 0 (q and q_out unused) and
+ *             need not be a multiple of kv_heads.
+ *   q_out   : [tokens, q_heads, head_dim] of dt, dense.
+ *   positions : int32 [tokens]; a token whose position is outside [0, n_positions) is skipped: neither
+ *             q_out nor the cache is written.  One with a position but without a slot (as in
+ *             fp8_kv_append) gets its queries.
+ *   cos_sin : float32 [n_positions, R], 16-byte aligned; R a multiple of 16, 16 .. head_dim.
+ * Other arguments as fp8_kv_append.
+ */
+fp8_status_t fp8_rope_append(const void* q, const void* k, const void* v, fp8_dtype_t dt, int64_t tokens,
+                             int64_t q_heads, int64_t kv_heads, int32_t head_dim, int64_t q_token_stride,
+                             int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, const int32_t* positions,
+                             const float* cos_sin, int64_t n_positions, int32_t rotary_dim, int32_t interleaved,
+                             const int64_t* slots, int64_t pages, int32_t page_size, fp8_kv_format_t format,
+                             void* k_cache, void* v_cache, void* k_scales, void* v_scales, void* q_out,
+                             void* stream);
 
 /*
  * fp8_attn_prompt - causal attention over whole prompts.  For query i of a request, over the
@@ -103,6 +141,9 @@ fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t
  * rounded to dt for the product with v, and the result once to dt.  Over a cache in FP8_KV_E4M3 a
  * key's scale multiplies its score in float32, and a value's scale its weight before that rounding;
  * with fp16 the scale's power of two, from 2^-14 to 2^7, multiplies the codes instead, exactly.
+ * Over FP8_KV_MXFP4 keys and values enter as numbers of dt: exactly with bf16, and with fp16 for
+ * scales from 2^-23 to 2^13 (below, rounded to its subnormal numbers; values past its range are
+ * infinite).
  */
 fp8_status_t fp8_attn_prompt(const void* q, const void* k, const void* v, fp8_dtype_t dt, int64_t tokens,
                              const int32_t* cu_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads,
@@ -133,7 +174,7 @@ int64_t fp8_attn_paged_workspace(int64_t tokens, int64_t batch, int64_t q_heads,
 fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const int32_t* cu_tokens, int64_t batch,
                             int64_t q_heads, int64_t kv_heads, int32_t head_dim, int64_t q_token_stride,
                             int64_t q_head_stride, fp8_kv_format_t format, const void* k_cache, const void* v_cache,
-                            const float* k_scales, const float* v_scales, int64_t pages, int32_t page_size,
+                            const void* k_scales, const void* v_scales, int64_t pages, int32_t page_size,
                             const int32_t* block_table, int64_t width, const int32_t* seq_lens, float softmax_scale,
                             int64_t window, int64_t max_new, void* out, float* lse, void* workspace,
                             int64_t workspace_bytes, void* stream);
