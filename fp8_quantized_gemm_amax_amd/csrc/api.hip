@@ -2,6 +2,7 @@
 // launches on the caller's stream.  Validation makes no HIP call, so every error path can
 // be exercised on a machine without a GPU.
 #include "fp8amax.h"
+#include "fp8amax_int8.h"
 
 #include <hip/hip_runtime.h>
 
@@ -12,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;   // kernels index rows/cols with int
 constexpr int64_t kMaxElems = int64_t{1} << 40;
+constexpr int64_t kMaxInt8K = 131071;                  // 128 * 128 K < 2^31: the sums are exact
 constexpr int64_t kMaxExperts = int64_t{1} << 16;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -146,6 +148,26 @@ fp8_status_t fp8_gemm_scaled_rowwise(const uint8_t* qa, const float* sa, const u
                                      const float* sb, int64_t M, int64_t N, int64_t K, void* c,
                                      fp8_dtype_t out_dt, void* stream) {
   return gemm_common(fp8amax::SM_ROW, qa, sa, qb, sb, M, N, K, c, out_dt, stream);
+}
+
+fp8_status_t int8_quantize_rowwise(const void* x, fp8_dtype_t dt, int64_t rows, int64_t cols, int8_t* q,
+                                   float* scales, void* stream) {
+  fp8_status_t st = check_2d(rows, cols);
+  if (st != FP8_OK) return st;
+  if (!valid_dt(dt)) return FP8_ERR_BAD_DTYPE;
+  if (rows == 0) return FP8_OK;
+  if (!scales || (cols > 0 && (!x || !q))) return FP8_ERR_NULL_POINTER;
+  if ((x && !aligned16(x)) || (q && !aligned16(q)) || !aligned4(scales)) return FP8_ERR_MISALIGNED;
+  (void)hipGetLastError();
+  fp8amax::launch_rows_int8(static_cast<int>(dt), x, rows, cols, q, scales, static_cast<hipStream_t>(stream));
+  return finish_launch();
+}
+
+fp8_status_t int8_gemm_scaled_rowwise(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M,
+                                      int64_t N, int64_t K, void* c, fp8_dtype_t out_dt, void* stream) {
+  if (K > kMaxInt8K) return FP8_ERR_TOO_LARGE;
+  return gemm_common(fp8amax::SM_INT8, reinterpret_cast<const uint8_t*>(qa), sa, reinterpret_cast<const uint8_t*>(qb), sb, M, N,
+                     K, c, out_dt, stream);
 }
 
 fp8_status_t fp8_gemm_grouped_blockwise(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb,

@@ -32,7 +32,7 @@ constexpr int kStreamOnce = 2;
 // past the ends read the last entry (their outputs are not stored).
 template <int SM, int MI, int NJ>
 struct FragFactors {
-  static constexpr bool kRow = SM == SM_ROW;
+  static constexpr bool kRow = row_scaled(SM);
   float a[kRow ? MI : 1];
   float b[kRow ? NJ : 1][4];
   __device__ __forceinline__ void load(const float* sa, const float* sb, int m0, int n0, int M, int N) {
@@ -217,6 +217,46 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
          (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
 }
+
+// The same for 32-bit integers.
+__device__ __forceinline__ int wave_sum(int v) {
+  v += static_cast<int>(dpp_u32<0xB1>(static_cast<uint32_t>(v)));
+  v += static_cast<int>(dpp_u32<0x4E>(static_cast<uint32_t>(v)));
+  v += static_cast<int>(dpp_u32<0x141>(static_cast<uint32_t>(v)));
+  v += static_cast<int>(dpp_u32<0x140>(static_cast<uint32_t>(v)));
+  return (__builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16)) +
+         (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
+}
+
+// Accumulators of the matrix products and what a 128-byte slab adds to them: float32 sums of e4m3
+// products, or 32-bit integer sums of int8 products, in two halves of 64 (16 bytes a lane each; both
+// operands in the same order, so the order does not matter); and a sum times its scales.
+template <int SM>
+struct Product {
+  typedef float Acc __attribute__((ext_vector_type(4)));
+  typedef int Slab __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ float scaled(float acc, float factor) { return acc * factor; }
+  static __device__ __forceinline__ Acc add(const Slab& a, const Slab& b, const Acc& c) {
+    // cbsz = blgp = 0: both operands e4m3; E8M0 scale 127 = 2^0 on both.
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+  }
+};
+template <>
+struct Product<SM_INT8> {
+  typedef int Acc __attribute__((ext_vector_type(4)));
+  typedef int Slab __attribute__((ext_vector_type(8)));
+  // The product as a float32 number of its own, with either output type: fused with the rounding to
+  // fp16 it would be rounded once less than with bf16.
+  static __device__ __forceinline__ float scaled(int acc, float factor) {
+    float p = static_cast<float>(acc) * factor;
+    asm("" : "+v"(p));
+    return p;
+  }
+  static __device__ __forceinline__ Acc add(const Slab& a, const Slab& b, const Acc& c) {
+    const Acc d = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_shufflevector(a, a, 0, 1, 2, 3), __builtin_shufflevector(b, b, 0, 1, 2, 3), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_shufflevector(a, a, 4, 5, 6, 7), __builtin_shufflevector(b, b, 4, 5, 6, 7), d, 0, 0, 0);
+  }
+};
 
 // Max over the whole wave (64 lanes); every lane gets the result.
 __device__ __forceinline__ uint32_t max64(uint32_t v) {

@@ -8,12 +8,14 @@
 //   blockwise: each 128-wide K slab g has its own sa[m, g] * sb[n / 128, g] ("FP8 chi
 //     tiết", opening bullets), applied in registers to that slab's float32 partial sum;
 //   rowwise: scale = sa[m] * sb[n], one scale per token and per output channel (the
-//     Transformer Engine page §5, per-channel scaling), applied once like tensorwise.
+//     Transformer Engine page §5, per-channel scaling), applied once like tensorwise;
+//   int8: the same over 8-bit integers, whose products are summed exactly in 32 bits (K up to
+//     131071: 128 * 128 K stays below 2^31) and rounded to float32 once, in the epilogue.
 //
 // Kernels (CDNA4).  Every kernel walks K in 128-byte slabs and multiplies with
 // v_mfma_scale_f32_16x16x128_f8f6f4 (unit E8M0 scales, i.e. a plain FP8 product, or the
 // UE8M0 block scales themselves); one instruction covers exactly one slab, so the float32
-// blockwise epilogue is one FMA per accumulator per slab.
+// blockwise epilogue is one FMA per accumulator per slab; int8 takes two v_mfma_i32_16x16x64_i8.
 //   gemm_dma_kernel: the tiled product for 129+ tokens.  A and B slabs move global -> LDS
 //     by LDS DMA into an NS-stage ring, eight (or four) waves multiply fragments read from
 //     LDS.  256x256 tiles when there is at least one per CU, launched as whole rounds plus
@@ -159,11 +161,12 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(
     }
   };
 
-  v4f acc[TM][TN];
+  using Acc = typename Product<SM>::Acc;
+  Acc acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < TN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
   float scl[TM], scl_next[TM];
   int ea[TM], ea_next[TM], eb = 127, eb_next = 127;
@@ -197,7 +200,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], scl[i], acc[i][j][r]);
         } else {
-          acc[i][j] = mfma_fp8(bf, af[i], acc[i][j]);
+          acc[i][j] = Product<SM>::add(bf, af[i], acc[i][j]);
         }
       }
     }
@@ -227,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(
       uint32_t h[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        h[r] = f32_to_out_bits<OUT>(acc[i][j][r] * ff(alpha, i, j, r));
+        h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[i][j][r], ff(alpha, i, j, r)));
       if (vec_store && n + 3 < N) {
         *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       } else {
@@ -430,11 +433,12 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
   uint32_t sbw = 0;
   if constexpr (BLOCKWISE) sbw = load_window(0);
 
-  v4f acc[TM][TN];
+  using Acc = typename Product<SM>::Acc;
+  Acc acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < TN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
   if constexpr (BLOCKWISE) wait_vmcnt<0>();
 
   auto compute = [&](int s, int st) {
@@ -473,7 +477,7 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], scl[i], acc[i][j][r]);
         } else {
-          acc[i][j] = mfma_fp8(bf, af[i], acc[i][j]);
+          acc[i][j] = Product<SM>::add(bf, af[i], acc[i][j]);
         }
       }
     }
@@ -530,7 +534,7 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
       uint32_t h[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        h[r] = f32_to_out_bits<OUT>(acc[i][j][r] * ff(alpha, i, j, r));
+        h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[i][j][r], ff(alpha, i, j, r)));
       if (vec_store && n + 3 < N) {
         *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       } else {
@@ -707,11 +711,12 @@ __device__ __forceinline__ void skinny_body(
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  v4f acc[NB][MB];
+  using Acc = typename Product<SM>::Acc;
+  Acc acc[NB][MB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
 #pragma unroll
-    for (int b = 0; b < MB; ++b) acc[j][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < MB; ++b) acc[j][b] = Acc{0, 0, 0, 0};
   auto consume = [&](int s, int u) {
     const int st = s % NS;
     const uint8_t* As = Abuf[st];
@@ -736,7 +741,7 @@ __device__ __forceinline__ void skinny_body(
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[j][b][r] = __builtin_fmaf(p[r], scl, acc[j][b][r]);
         } else {
-          acc[j][b] = mfma_fp8(wf[u][j], af, acc[j][b]);
+          acc[j][b] = Product<SM>::add(wf[u][j], af, acc[j][b]);
         }
       }
     }
@@ -785,7 +790,7 @@ __device__ __forceinline__ void skinny_body(
       const int n = n0 + 16 * j + 4 * kq;
       uint32_t h[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) h[r] = f32_to_out_bits<OUT>(acc[j][b][r] * ff(alpha, b, j, r));
+      for (int r = 0; r < 4; ++r) h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[j][b][r], ff(alpha, b, j, r)));
       if (vec_store && n + 3 < N) {
         *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       } else {
@@ -892,7 +897,7 @@ template <int SM>
 const void* scale_cols(const void* sb, int64_t n_off, int K) {
   if constexpr (SM == SM_BLOCK) return static_cast<const float*>(sb) + (n_off / kSlab) * (K / kSlab);
   else if constexpr (SM == SM_E8M0) return static_cast<const uint8_t*>(sb) + (n_off / kSlab) * e8m0_row_bytes(K / kSlab);
-  else if constexpr (SM == SM_ROW) return static_cast<const float*>(sb) + n_off;
+  else if constexpr (row_scaled(SM)) return static_cast<const float*>(sb) + n_off;
   else return sb;
 }
 
@@ -1011,6 +1016,7 @@ bool launch_grouped(int mode, int out_dt, const uint8_t* qa, const void* sa, con
 
 bool launch_gemm(int mode, int out_dt, const fp8_gemm_plan_t& p, const uint8_t* qa, const void* sa,
                  const uint8_t* qb, const void* sb, int M, int N, int K, void* c, hipStream_t s) {
+  if (mode == SM_INT8) return launch_gemm_m<SM_INT8>(p, out_dt, qa, sa, qb, sb, M, N, K, c, s);
   if (mode == SM_ROW) return launch_gemm_m<SM_ROW>(p, out_dt, qa, sa, qb, sb, M, N, K, c, s);
   if (mode == SM_E8M0) return launch_gemm_m<SM_E8M0>(p, out_dt, qa, sa, qb, sb, M, N, K, c, s);
   if (mode == SM_BLOCK) return launch_gemm_m<SM_BLOCK>(p, out_dt, qa, sa, qb, sb, M, N, K, c, s);

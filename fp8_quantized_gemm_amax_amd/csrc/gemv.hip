@@ -16,6 +16,8 @@
 // row block (W as the first operand, A padded to 16 rows as the second) gives lane l the
 // partial sums of C[m = l % 16][n = n0 + 16 j + 4 (l / 16) + r].  The waves' K shares are
 // summed in LDS and the epilogue scales and stores.
+#include <type_traits>
+
 #include "fp8_device.hpp"
 #include "gemm_plan.hpp"
 #include "launch.hpp"
@@ -74,7 +76,8 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
   constexpr bool E8M0 = SM == SM_E8M0;
   const float* __restrict__ sa = static_cast<const float*>(sa_);
   const float* __restrict__ sb = static_cast<const float*>(sb_);
-  __shared__ v4f red[WAVES > 1 ? (WAVES - 1) * NB * MB * 64 : 1];
+  using Acc = typename Product<SM>::Acc;
+  __shared__ Acc red[WAVES > 1 ? (WAVES - 1) * NB * MB * 64 : 1];
 
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -159,11 +162,11 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
     for (int j = 0; j < NB; ++j) { wf[u][j] = v8i{0, 0, 0, 0, 0, 0, 0, 0}; sbv[u][j] = 0.0f; }
     slab[u] = 0;
   }
-  v4f acc[NB][MB];
+  Acc acc[NB][MB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
 #pragma unroll
-    for (int b = 0; b < MB; ++b) acc[j][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < MB; ++b) acc[j][b] = Acc{0, 0, 0, 0};
   auto consume = [&](int u) {
 #pragma unroll
     for (int j = 0; j < NB; ++j)
@@ -178,7 +181,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[j][b][r] = __builtin_fmaf(p[r], scale, acc[j][b][r]);
         } else {
-          acc[j][b] = mfma_fp8(wf[u][j], af[u][b], acc[j][b]);
+          acc[j][b] = Product<SM>::add(wf[u][j], af[u][b], acc[j][b]);
         }
       }
   };
@@ -211,7 +214,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
-          const v4f o = red[(((q - 1) * NB + j) * MB + b) * 64 + lane];
+          const Acc o = red[(((q - 1) * NB + j) * MB + b) * 64 + lane];
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[j][b][r] += o[r];
         }
@@ -228,7 +231,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
       const int n = n0 + 16 * j + 4 * kq;
       uint32_t h[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) h[r] = f32_to_out_bits<OUT>(acc[j][b][r] * ff(alpha, b, j, r));
+      for (int r = 0; r < 4; ++r) h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[j][b][r], ff(alpha, b, j, r)));
       if ((N & 3) == 0 && n + 3 < N) {
         *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       } else {
@@ -245,7 +248,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
 // one row, so every load instruction streams 1 KB of contiguous HBM (the access pattern that
 // keeps HBM busiest) and no LDS is involved.  The 16 codes are widened exactly to f16
 // (every e4m3 value is an f16 normal) and multiplied with v_dot2c_f32_f16, which forms the
-// products exactly and accumulates in float32.  A lane's 16 K positions lie in one
+// products exactly and accumulates in float32 (int8: v_dot4_i32_i8, exact).  A lane's 16 K positions lie in one
 // 128-wide slab, so the blockwise scale sa[m, g] * sb[n / 128, g] is applied to each
 // lane's 16-term partial.  At the end the 64 lanes' partials of each (m, row) are summed
 // with DPP within rows of 16 lanes and readlane across them (wave_sum).  The float32 sum is
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(256) void gemv_valu_kernel(
   // rowwise: the factor of the output this lane stores (lane m * RPW + r writes C[m, row0 + r]),
   // fetched now so that the load overlaps the K loop
   float row_factor = 1.0f;
-  if constexpr (SM == SM_ROW)
+  if constexpr (row_scaled(SM))
     row_factor = sa[min(lane / RPW, M - 1)] * sb[row0 + min(lane % RPW, rows - 1)];
   const int KG = K / kSlab;                                   // blockwise: K % 128 == 0
   const int SR = E8M0 ? static_cast<int>(e8m0_row_bytes(KG)) : KG * 4;   // bytes per scale row
@@ -328,13 +331,23 @@ __global__ __launch_bounds__(256) void gemv_valu_kernel(
     sbv[u] = 0.0f;
     gsl[u] = 0;
   }
-  float acc[MT][RPW];
+  using Sum = std::conditional_t<SM == SM_INT8, int, float>;
+  Sum acc[MT][RPW];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int r = 0; r < RPW; ++r) acc[m][r] = 0.0f;
+    for (int r = 0; r < RPW; ++r) acc[m][r] = 0;
 
   auto consume = [&](int u) {
+    if constexpr (SM == SM_INT8) {       // sixteen products a lane, four an instruction
+#pragma unroll
+      for (int r = 0; r < RPW; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) acc[m][r] = __builtin_amdgcn_sdot4(wv[u][r][d], av[u][m][d], acc[m][r], false);
+      return;
+    }
     h2 ah[MT][8];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -393,7 +406,7 @@ __global__ __launch_bounds__(256) void gemv_valu_kernel(
   float alpha = 1.0f;
   if constexpr (SM == SM_TENSOR) alpha = sa[0] * sb[0];
   // lane m * RPW + r writes C[m, row0 + r]
-  float mine = 0.0f;
+  Sum mine = 0;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -402,7 +415,7 @@ __global__ __launch_bounds__(256) void gemv_valu_kernel(
   const int m = lane / RPW, r = lane % RPW;
   if (lane < MT * RPW && m < M && r < rows)
     c[static_cast<int64_t>(m) * N + row0 + r] =
-        static_cast<uint16_t>(f32_to_out_bits<OUT>(mine * (SM == SM_ROW ? row_factor : alpha)));
+        static_cast<uint16_t>(f32_to_out_bits<OUT>(Product<SM>::scaled(mine, row_scaled(SM) ? row_factor : alpha)));
 }
 
 // One token on the vector ALUs, persistent: a grid that fills the chip; wave gw takes rows
@@ -790,6 +803,7 @@ void launch_dynamic_m(int in_dt, int out_dt, const void* x, const uint8_t* qb, c
 
 bool launch_gemv(int mode, int out_dt, const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa,
                  const uint8_t* qb, const void* sb, int M, int N, int K, void* c, hipStream_t s) {
+  if (mode == SM_INT8) return launch_gemv_m<SM_INT8>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
   if (mode == SM_ROW) return launch_gemv_m<SM_ROW>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
   if (mode == SM_E8M0) return launch_gemv_m<SM_E8M0>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
   if (mode == SM_BLOCK) return launch_gemv_m<SM_BLOCK>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);

@@ -13,12 +13,16 @@ namespace fp8amax {
 //   SM_BLOCK:  float32 scales per 1x128 activation group and 128x128 weight block;
 //   SM_E8M0:   the same groups and blocks with UE8M0 scales, one e8m0fnu byte each,
 //              every scale row padded to whole 32-bit words (e8m0_row_bytes);
-//   SM_ROW:    one float32 scale per row of A (token) and per row of B (output channel).
-enum ScaleMode { SM_TENSOR = 0, SM_BLOCK = 1, SM_E8M0 = 2, SM_ROW = 3 };
+//   SM_ROW:    one float32 scale per row of A (token) and per row of B (output channel);
+//   SM_INT8:   the same scales over operands of 8-bit integers, summed in 32-bit integers.
+enum ScaleMode { SM_TENSOR = 0, SM_BLOCK = 1, SM_E8M0 = 2, SM_ROW = 3, SM_INT8 = 4 };
 
 // Modes whose scales change every 128-wide K slab, applied inside the K loop; the others
 // scale the finished float32 accumulator once in the epilogue.
 __host__ __device__ constexpr bool slab_scaled(int sm) { return sm == SM_BLOCK || sm == SM_E8M0; }
+
+// Modes with one scale per row of A and per row of B.
+__host__ __device__ constexpr bool row_scaled(int sm) { return sm == SM_ROW || sm == SM_INT8; }
 
 // Bytes per row of a UE8M0 scale tensor with `groups` scales: four per 32-bit word.
 __host__ __device__ constexpr int64_t e8m0_row_bytes(int64_t groups) { return (groups + 3) & ~int64_t{3}; }
@@ -36,6 +40,10 @@ void launch_groups_e8m0(int dt, const void* x, int64_t rows, int64_t cols, int32
 // One float32 scale per row: amax of the row / 448, the row cast with it.
 void launch_rows(int dt, const void* x, int64_t rows, int64_t cols, uint8_t* q, float* scales,
                  hipStream_t s);
+
+// The same in 8-bit integers: scale = amax / 127, the row's quotients rounded to nearest even.
+void launch_rows_int8(int dt, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scales,
+                      hipStream_t s);
 
 // Whole-tensor amax of n elements into the float *amax (0 for n == 0).
 void launch_tensor_amax(int dt, const void* x, int64_t n, float* amax, hipStream_t s);

@@ -163,8 +163,76 @@ __global__ __launch_bounds__(kThreads) void group_1x128_scalar_kernel(
 // the cast: WPR = 1 gives a row to one wave (VEC 16-byte pieces per lane, up to 4096
 // elements), WPR = 4 to the whole workgroup (up to 16384).  Each row is read through a
 // buffer resource of exactly its bytes, so pieces past its end load as zeros and every load
-// is issued without a branch.  cols % 8 == 0 (every row starts 16-byte aligned).
-template <int DT, int WPR, int VEC>
+// is issued without a branch.  cols % 8 == 0 (every row starts 16-byte aligned).  CODE: e4m3
+// codes, or 8-bit integers with scale = amax / 127.
+struct E4m3Code {
+  float s, r;
+  bool fast;
+  static __device__ __forceinline__ float scale(float amax) { return scale_from_amax(amax); }
+  __device__ __forceinline__ explicit E4m3Code(float scale) : s(scale), r(1.0f / scale), fast(fast_scale(scale)) {}
+  template <int DT>
+  __device__ __forceinline__ uint2 enc8(const U4& v) const { return fp8amax::enc8<DT>(v, s, r, fast); }
+  template <int DT>
+  __device__ __forceinline__ uint8_t enc1(uint32_t h) const { return fp8amax::enc1<DT>(h, s, r, fast); }
+};
+
+// The integer nearest to x / s, ties to even, exactly: y = x r is within 2^-15 of the quotient (|y| at
+// most 127, r the rounded reciprocal), so only where it lies that close to a half is the rounding of y in
+// doubt; there the sign of x - h s decides, h the half next to it, which one fused product and sum gives
+// exactly (h has 8 bits and s 24).  Scales below 2^-60, whose remainders could fall below float32's
+// numbers, are multiplied by 2^64 with their values first, exactly.  A value or scale that is not finite
+// gives 0 for NaN quotients (its row's scale then carries what is not finite).
+struct Int8Code {
+  float s, r, up;
+  static __device__ __forceinline__ float scale(float amax) {
+    if (amax != amax) return __uint_as_float(kCanonicalNaN);
+    return amax == 0.0f ? 1.0f : amax / 127.0f;
+  }
+  __device__ __forceinline__ explicit Int8Code(float scale) {
+    up = scale < 0x1p-60f ? 0x1p64f : 1.0f;
+    s = scale * up;
+    r = 1.0f / s;
+  }
+  static constexpr float kMagic = 12582912.0f;      // 1.5 * 2^23: a sum's low bits are the integer, rounded to even
+  static constexpr float kDoubt = 0.4999f;
+  __device__ __forceinline__ float settle(float x, float y) const {
+    const float k = (y + kMagic) - kMagic, d = y - k;
+    if (!(__builtin_fabsf(d) > kDoubt)) return k;
+    const float side = __builtin_copysignf(1.0f, d), t = __builtin_fmaf(-(k + 0.5f * side), s, x) * side;   // > 0: past the half
+    const bool odd = (static_cast<int>(k) & 1) != 0;
+    return t > 0.0f || (t == 0.0f && odd) ? k + side : k;
+  }
+  template <int DT>
+  __device__ __forceinline__ uint2 enc8(const U4& v) const {
+    float x[8], y[8];
+    widen8<DT>(v, x);
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] *= up;
+      y[i] = x[i] * r;
+      most = fmaxf(most, __builtin_fabsf(y[i] - ((y[i] + kMagic) - kMagic)));
+    }
+    if (most > kDoubt) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = settle(x[i], y[i]);
+    }
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(y[i] + kMagic);
+    auto pack = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400), __builtin_amdgcn_perm(b, a, 0x0c0c0400), 0x05040100);
+    };
+    return make_uint2(pack(b[0], b[1], b[2], b[3]), pack(b[4], b[5], b[6], b[7]));
+  }
+  template <int DT>
+  __device__ __forceinline__ uint8_t enc1(uint32_t h) const {
+    const float x = in_to_f32<DT>(h) * up;
+    return static_cast<uint8_t>(__float_as_uint(settle(x, x * r) + kMagic));
+  }
+};
+
+template <class CODE, int DT, int WPR, int VEC>
 __global__ __launch_bounds__(kThreads) void rows_vec_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                             int64_t cols, uint8_t* __restrict__ q,
                                                             float* __restrict__ scales) {
@@ -199,14 +267,13 @@ __global__ __launch_bounds__(kThreads) void rows_vec_kernel(const uint16_t* __re
       __syncthreads();                          // part is rewritten for the next row
     }
     if (live) {
-      const float scale = scale_from_amax(amax_from_key<DT>(m));
-      const bool fast = fast_scale(scale);
-      const float r = 1.0f / scale;
+      const float scale = CODE::scale(amax_from_key<DT>(m));
+      const CODE code(scale);
       uint8_t* qr = q + row * cols;
 #pragma unroll
       for (int u = 0; u < VEC; ++u) {
         const int64_t i = lt + u * T;
-        if (i < nv) *reinterpret_cast<uint2*>(qr + (i << 3)) = enc8<DT>(v[u], scale, r, fast);
+        if (i < nv) *reinterpret_cast<uint2*>(qr + (i << 3)) = code.template enc8<DT>(v[u]);
       }
       if (lt == 0) scales[row] = scale;
     }
@@ -216,7 +283,7 @@ __global__ __launch_bounds__(kThreads) void rows_vec_kernel(const uint16_t* __re
 // Rows longer than 16384 elements (VEC) or of any length (!VEC, rows not 16-byte aligned):
 // one workgroup per row, two passes - the amax, then the cast re-reading the row, which the
 // first pass has just brought into the caches.
-template <int DT, bool VEC>
+template <class CODE, int DT, bool VEC>
 __global__ __launch_bounds__(kThreads) void rows_two_pass_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                  int64_t cols, uint8_t* __restrict__ q,
                                                                  float* __restrict__ scales) {
@@ -240,13 +307,12 @@ __global__ __launch_bounds__(kThreads) void rows_two_pass_kernel(const uint16_t*
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) m = max(m, part[w]);
     __syncthreads();
-    const float scale = scale_from_amax(amax_from_key<DT>(m));
-    const bool fast = fast_scale(scale);
-    const float r = 1.0f / scale;
+    const float scale = CODE::scale(amax_from_key<DT>(m));
+    const CODE code(scale);
     uint8_t* qr = q + row * cols;
     for (int64_t v = t; v < nv; v += kThreads)
-      *reinterpret_cast<uint2*>(qr + (v << 3)) = enc8<DT>(load16(xr + (v << 3)), scale, r, fast);
-    for (int64_t j = (nv << 3) + t; j < cols; j += kThreads) qr[j] = enc1<DT>(xr[j], scale, r, fast);
+      *reinterpret_cast<uint2*>(qr + (v << 3)) = code.template enc8<DT>(load16(xr + (v << 3)));
+    for (int64_t j = (nv << 3) + t; j < cols; j += kThreads) qr[j] = code.template enc1<DT>(xr[j]);
     if (t == 0) scales[row] = scale;
   }
 }
@@ -856,12 +922,12 @@ void launch_tensor_amax_t(const void* x, int64_t n, float* amax, hipStream_t s) 
 
 namespace {
 
-template <int DT>
+template <class CODE, int DT>
 void launch_rows_t(const void* xv, int64_t rows, int64_t cols, uint8_t* q, float* scales, hipStream_t s) {
   const uint16_t* x = static_cast<const uint16_t*>(xv);
   constexpr int64_t kRowsCap = 256 * 64;       // workgroups; the kernels loop over further rows
   if (cols % 8 != 0 || cols == 0) {           // (empty rows: scale 1, x and q never touched)
-    rows_two_pass_kernel<DT, false><<<grid_for(rows, 1, kRowsCap), kThreads, 0, s>>>(x, rows, cols, q, scales);
+    rows_two_pass_kernel<CODE, DT, false><<<grid_for(rows, 1, kRowsCap), kThreads, 0, s>>>(x, rows, cols, q, scales);
     return;
   }
   const unsigned g_wave = grid_for(rows, kThreads / 64, kRowsCap);   // a row per wave
@@ -869,27 +935,33 @@ void launch_rows_t(const void* xv, int64_t rows, int64_t cols, uint8_t* q, float
   // few rows (decode tokens): a workgroup per row, so that each row has four times the loads
   // in flight and no CU holds several of them
   if (rows <= 256 && cols > 512 && cols <= 16384) {
-    if (cols <= 2048) rows_vec_kernel<DT, 4, 1><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
-    else if (cols <= 4096) rows_vec_kernel<DT, 4, 2><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
-    else if (cols <= 8192) rows_vec_kernel<DT, 4, 4><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
-    else rows_vec_kernel<DT, 4, 8><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
+    if (cols <= 2048) rows_vec_kernel<CODE, DT, 4, 1><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
+    else if (cols <= 4096) rows_vec_kernel<CODE, DT, 4, 2><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
+    else if (cols <= 8192) rows_vec_kernel<CODE, DT, 4, 4><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
+    else rows_vec_kernel<CODE, DT, 4, 8><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
     return;
   }
-  if (cols <= 512) rows_vec_kernel<DT, 1, 1><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
-  else if (cols <= 1024) rows_vec_kernel<DT, 1, 2><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
-  else if (cols <= 2048) rows_vec_kernel<DT, 1, 4><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
-  else if (cols <= 4096) rows_vec_kernel<DT, 1, 8><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
-  else if (cols <= 8192) rows_vec_kernel<DT, 4, 4><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
-  else if (cols <= 16384) rows_vec_kernel<DT, 4, 8><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
-  else rows_two_pass_kernel<DT, true><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
+  if (cols <= 512) rows_vec_kernel<CODE, DT, 1, 1><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
+  else if (cols <= 1024) rows_vec_kernel<CODE, DT, 1, 2><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
+  else if (cols <= 2048) rows_vec_kernel<CODE, DT, 1, 4><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
+  else if (cols <= 4096) rows_vec_kernel<CODE, DT, 1, 8><<<g_wave, kThreads, 0, s>>>(x, rows, cols, q, scales);
+  else if (cols <= 8192) rows_vec_kernel<CODE, DT, 4, 4><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
+  else if (cols <= 16384) rows_vec_kernel<CODE, DT, 4, 8><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
+  else rows_two_pass_kernel<CODE, DT, true><<<g_wg, kThreads, 0, s>>>(x, rows, cols, q, scales);
 }
 
 }  // namespace
 
 void launch_rows(int dt, const void* x, int64_t rows, int64_t cols, uint8_t* q, float* scales,
                  hipStream_t s) {
-  if (dt == DT_BF16) launch_rows_t<DT_BF16>(x, rows, cols, q, scales, s);
-  else launch_rows_t<DT_F16>(x, rows, cols, q, scales, s);
+  if (dt == DT_BF16) launch_rows_t<E4m3Code, DT_BF16>(x, rows, cols, q, scales, s);
+  else launch_rows_t<E4m3Code, DT_F16>(x, rows, cols, q, scales, s);
+}
+
+void launch_rows_int8(int dt, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scales, hipStream_t s) {
+  uint8_t* bytes = reinterpret_cast<uint8_t*>(q);
+  if (dt == DT_BF16) launch_rows_t<Int8Code, DT_BF16>(x, rows, cols, bytes, scales, s);
+  else launch_rows_t<Int8Code, DT_F16>(x, rows, cols, bytes, scales, s);
 }
 
 void launch_groups(int dt, const void* x, int64_t rows, int64_t cols, int32_t group_rows,
