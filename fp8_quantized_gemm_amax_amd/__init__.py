@@ -12,9 +12,9 @@ from .binding import (Fp8Error, fp8_amax, fp8_quantize_per_tensor, fp8_quantize_
                       DelayedScaling, fp8_quantize_rowwise, fp8_gemm_scaled_rowwise,
                       fp8_gemm_grouped_blockwise, fp8_gemm_grouped_blockwise_ue8m0,
                       fp8_debug_byte_mix, fp8_debug_gemm_plan, fp8_gemv_dynamic, lib, LIB_PATH)
-from .int8 import int8_gemm_scaled_rowwise, int8_quantize_rowwise
 from .serving import (PagedPlan, fp8_attn_paged, fp8_attn_paged_workspace, fp8_attn_prompt, fp8_kv_append,
                       fp8_paged_plan, fp8_rope_append, paged_plan_buffers, rope_table)
+from .int8 import int8_gemm_scaled_rowwise, int8_quantize_rowwise
 
 __all__ = ["Fp8Error", "fp8_amax", "fp8_quantize_per_tensor", "fp8_quantize_per_token_group",
            "fp8_gemm_scaled_tensorwise", "fp8_gemm_scaled_blockwise", "fp8_debug_cast_f32",

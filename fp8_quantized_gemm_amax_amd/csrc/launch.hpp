@@ -41,7 +41,7 @@ void launch_groups_e8m0(int dt, const void* x, int64_t rows, int64_t cols, int32
 void launch_rows(int dt, const void* x, int64_t rows, int64_t cols, uint8_t* q, float* scales,
                  hipStream_t s);
 
-// The same in 8-bit integers: scale = amax / 127, the row's quotients rounded to nearest even.
+// The same in 8-bit integers: scale = amax * (1 / 127), the row's quotients rounded to nearest even.
 void launch_rows_int8(int dt, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scales,
                       hipStream_t s);
 

@@ -164,7 +164,7 @@ __global__ __launch_bounds__(kThreads) void group_1x128_scalar_kernel(
 // elements), WPR = 4 to the whole workgroup (up to 16384).  Each row is read through a
 // buffer resource of exactly its bytes, so pieces past its end load as zeros and every load
 // is issued without a branch.  cols % 8 == 0 (every row starts 16-byte aligned).  CODE: e4m3
-// codes, or 8-bit integers with scale = amax / 127.
+// codes, or 8-bit integers with scale = amax times the rounded 1 / 127.
 struct E4m3Code {
   float s, r;
   bool fast;
@@ -186,7 +186,7 @@ struct Int8Code {
   float s, r, up;
   static __device__ __forceinline__ float scale(float amax) {
     if (amax != amax) return __uint_as_float(kCanonicalNaN);
-    return amax == 0.0f ? 1.0f : amax / 127.0f;
+    return amax == 0.0f ? 1.0f : amax * (1.0f / 127.0f);
   }
   __device__ __forceinline__ explicit Int8Code(float scale) {
     up = scale < 0x1p-60f ? 0x1p64f : 1.0f;

@@ -1,6 +1,7 @@
-// serving_binding.cpp - argument marshalling of the serving operators (serving.py): tensors checked
-// and unpacked, outputs allocated, the C ABI of include/fp8amax_serving.h called through the
-// addresses serving.py hands over.  The same in Python took 4 to 7 us of calls that take 8 to 11,
+// serving_binding.cpp - argument marshalling of the serving operators (serving.py) and of the 8-bit
+// integer product (int8.py): tensors checked and unpacked, outputs allocated, the C ABI of
+// include/fp8amax_serving.h and include/fp8amax_int8.h called through the addresses serving.py
+// hands over.  The same in Python took 4 to 7 us of calls that take 8 to 11,
 // where the kernels of a decode step run for 3 to 12.
 //
 // The functions return what the operator returns, or the status code (an int) of a refused call.
@@ -15,6 +16,7 @@
 #include <string>
 #include <utility>
 
+#include "fp8amax_int8.h"
 #include "fp8amax_serving.h"
 
 namespace {
@@ -25,6 +27,8 @@ decltype(&fp8_rope_append) rope_fn;
 decltype(&fp8_attn_prompt) prompt_fn;
 decltype(&fp8_attn_paged) paged_fn;
 decltype(&fp8_attn_paged_workspace) workspace_fn;
+decltype(&int8_quantize_rowwise) quantize8_fn;
+decltype(&int8_gemm_scaled_rowwise) gemm8_fn;
 
 std::string shape_of(const at::Tensor& t) {
   std::string s = "(";
@@ -422,22 +426,91 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
-// The addresses of fp8_paged_plan, fp8_kv_append, fp8_rope_append, fp8_attn_prompt, fp8_attn_paged, fp8_attn_paged_workspace.
+// A matrix as the kernels read it: dense, from a 16-byte boundary, copied if it is not.
+at::Tensor matrix(const at::Tensor& t, const char* what) {
+  TORCH_CHECK_VALUE(t.dim() == 2, what, " must be a 2-D tensor, got shape ", shape_of(t));
+  at::Tensor c = t.contiguous();
+  return reinterpret_cast<uintptr_t>(c.data_ptr()) & 15 ? c.clone() : c;
+}
+// An output: the caller's (checked later with the devices), or a new one.
+at::Tensor output_of(PyObject* given, const char* what, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
+  if (given == Py_None) return at::empty(shape, like.options().dtype(type));
+  const at::Tensor& out = tensor(given, what);
+  dense(out, what, type, shape);
+  return out;
+}
+PyObject* give(PyObject* given, const at::Tensor& t) { return given != Py_None ? (Py_INCREF(given), given) : wrap(t); }
+
+// x, q, scales, stream
+PyObject* quantize8(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  ARGS(4);
+  const at::Tensor& x0 = tensor(a[0], "x");
+  const fp8_dtype_t dt = dtype_of(x0, "x");
+  const at::Tensor x = matrix(x0, "x");
+  on(x, {});
+  const at::Tensor q = output_of(a[1], "q", x.sizes(), at::kChar, x), scales = output_of(a[2], "scales", {x.size(0)}, at::kFloat, x);
+  TORCH_CHECK_VALUE(!overlaps(q, x) && !overlaps(scales, x) && !overlaps(scales, q), "an output overlaps an input or the other output");
+  on(x, {{&q, "q"}, {&scales, "scales"}});
+  const c10::DeviceGuard guard(x.device());   // the launch goes to the tensors' GPU
+  const fp8_status_t code = quantize8_fn(x.data_ptr(), dt, x.size(0), x.size(1), ptr<int8_t>(q), ptr<float>(scales), stream_of(a[3]));
+  if (code != FP8_OK) return status(code);
+  PyObject* r = PyTuple_New(2);
+  if (r) {
+    PyTuple_SET_ITEM(r, 0, give(a[1], q));
+    PyTuple_SET_ITEM(r, 1, give(a[2], scales));
+  }
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// qa, sa, qb, sb, out_dtype is bfloat16, out, stream
+PyObject* gemm8(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  ARGS(7);
+  const at::Tensor &qa0 = tensor(a[0], "qa"), &qb0 = tensor(a[2], "qb");
+  TORCH_CHECK_TYPE(qa0.scalar_type() == at::kChar && qb0.scalar_type() == at::kChar, "operands must be int8, got ", qa0.scalar_type(), " and ", qb0.scalar_type());
+  const at::Tensor qa = matrix(qa0, "qa"), qb = matrix(qb0, "qb");
+  const int64_t m = qa.size(0), n = qb.size(0), k = qa.size(1);
+  TORCH_CHECK_VALUE(qb.size(1) == k, "K mismatch: qa has ", k, ", qb has ", qb.size(1));
+  const at::Tensor sa = vec(tensor(a[1], "sa"), "sa", at::kFloat, m), sb = vec(tensor(a[3], "sb"), "sb", at::kFloat, n);
+  on(qa, {{&sa, "sa"}, {&qb, "qb"}, {&sb, "sb"}});
+  at::Tensor out;
+  if (a[5] == Py_None) {
+    out = at::empty({m, n}, qa.options().dtype(PyObject_IsTrue(a[4]) == 1 ? at::kBFloat16 : at::kHalf));
+  } else {
+    out = tensor(a[5], "out");
+    dtype_of(out, "out");
+    dense(out, "out", out.scalar_type(), {m, n});
+    for (const at::Tensor* t : {&qa, &qb, &sa, &sb}) TORCH_CHECK_VALUE(!overlaps(out, *t), "out overlaps an input");
+    on(qa, {{&out, "out"}});
+  }
+  const c10::DeviceGuard guard(qa.device());   // the launch goes to the tensors' GPU
+  const fp8_status_t code = gemm8_fn(ptr<int8_t>(qa), ptr<float>(sa), ptr<int8_t>(qb), ptr<float>(sb), m, n, k, out.data_ptr(), dtype_of(out, "out"),
+                                     stream_of(a[6]));
+  return code == FP8_OK ? give(a[5], out) : status(code);
+  END_HANDLE_TH_ERRORS
+}
+
+// The addresses of fp8_paged_plan, fp8_kv_append, fp8_rope_append, fp8_attn_prompt, fp8_attn_paged, fp8_attn_paged_workspace,
+// int8_quantize_rowwise and int8_gemm_scaled_rowwise.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
-  ARGS(6);
+  ARGS(8);
   plan_fn = reinterpret_cast<decltype(plan_fn)>(PyLong_AsVoidPtr(a[0]));
   append_fn = reinterpret_cast<decltype(append_fn)>(PyLong_AsVoidPtr(a[1]));
   rope_fn = reinterpret_cast<decltype(rope_fn)>(PyLong_AsVoidPtr(a[2]));
   prompt_fn = reinterpret_cast<decltype(prompt_fn)>(PyLong_AsVoidPtr(a[3]));
   paged_fn = reinterpret_cast<decltype(paged_fn)>(PyLong_AsVoidPtr(a[4]));
   workspace_fn = reinterpret_cast<decltype(workspace_fn)>(PyLong_AsVoidPtr(a[5]));
+  quantize8_fn = reinterpret_cast<decltype(quantize8_fn)>(PyLong_AsVoidPtr(a[6]));
+  gemm8_fn = reinterpret_cast<decltype(gemm8_fn)>(PyLong_AsVoidPtr(a[7]));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(paged_plan), METHOD(kv_append), METHOD(rope_append), METHOD(attn_prompt), METHOD(attn_paged), METHOD(bind), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(paged_plan), METHOD(kv_append), METHOD(rope_append), METHOD(attn_prompt), METHOD(attn_paged), METHOD(quantize8), METHOD(gemm8), METHOD(bind), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -62,6 +62,7 @@ def _load():
     """The compiled marshalling, loaded once and given the library's addresses."""
     global _ext
     if _ext is None:
+        from . import int8                     # its marshalling is in the same extension
         fns = _lib()
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
@@ -69,7 +70,7 @@ def _load():
         loader = importlib.machinery.ExtensionFileLoader("_serving", BINDING_PATH)
         ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_serving", loader))
         loader.exec_module(ext)
-        ext.bind(*(ctypes.cast(fns[n], _P).value for n in _SIGNATURES))
+        ext.bind(*(ctypes.cast(f, _P).value for f in (*fns.values(), *int8._lib().values())))
         _ext = ext
     return _ext
 

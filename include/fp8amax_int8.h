@@ -17,7 +17,9 @@ extern "C" {
 
 /*
  * int8_quantize_rowwise - one float32 scale per row:
- *   scales[r] = amax(|x[r, :]|) / 127 (one float32 division; amax 0 -> 1.0, NaN -> NaN),
+ *   scales[r] = amax(|x[r, :]|) * (1 / 127) (the float32 product with the rounded 1 / 127, as
+ *               torch divides a GPU tensor by a number, so that its codes are these bit for
+ *               bit; amax 0 -> 1.0, NaN -> NaN),
  *   q[r, c]   = the integer nearest to x[r, c] / scales[r], ties to even: of the exact quotient,
  *               so within -127 .. 127.  Where the quotient is NaN (NaN, or infinity over an
  *               infinite scale) 0: the row's scale, which is then not finite, marks it.

@@ -30,7 +30,7 @@ def test_codes_are_the_nearest_integers():
         v = int8.input_to_f32(b, dtype)
         for r in range(40):
             scale = Fraction(float(s[r]))
-            assert abs(scale - Fraction(float(np.abs(v[r]).max())) / 127) <= scale * Fraction(1, 1 << 24)
+            assert abs(scale - Fraction(float(np.abs(v[r]).max())) / 127) <= scale * Fraction(1, 1 << 23)      # 1 / 127 and the product rounded
             assert [nearest(Fraction(float(y)) / scale) for y in v[r]] == q[r].tolist()
         assert np.abs(q.astype(int)).max() == 127
 
