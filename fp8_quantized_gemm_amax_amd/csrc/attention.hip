@@ -124,7 +124,7 @@ int64_t attn_paged_groups(int format, int64_t tokens, int64_t batch, int64_t hq,
   const int64_t group = hq / hk;
   const bool split = may_split(tokens, group, batch, hk, capacity);
   if (!few_rows(format, max_new, group, tokens, batch)) return tile_groups(tokens, batch, group, hk, split);
-  return few_groups(tokens, batch, group, hk, capacity, split, format == FP8_KV_MXFP4 ? mx4_rows(tokens, group, batch) : 32);
+  return format == FP8_KV_MXFP4 ? mx4_groups(tokens, batch, group, hk, capacity, split) : few_groups(tokens, batch, group, hk, capacity, split);
 }
 
 int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
@@ -132,7 +132,7 @@ int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t 
   using namespace attn;
   if (!may_split(tokens, hq / hk, batch, hk, capacity)) return 0;
   auto bytes = [&](bool few) {
-    return workspace_bytes(few ? 2 * kFewGroups : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
+    return workspace_bytes(few ? 2 * std::max<int64_t>(kFewGroups, hk) : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
   };
   // Enough for every format of the cache.
   return std::max(bytes(few_rows(FP8_KV_SAME, max_new, hq / hk, tokens, batch)),

@@ -244,15 +244,16 @@ __device__ __forceinline__ Shape shape_of(const AttnArgs& a, const Request& q, i
   return s;
 }
 
-// The inclusive sum of x over a wave.
+// The inclusive sum of x over a wave: within rows of 16 lanes, then across them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int shifted(int x) { return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false); }
 __device__ __forceinline__ int scan64(int x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
-  return x;
+  x += shifted<0x111, 0xf>(x);      // row_shr 1, 2, 4, 8
+  x += shifted<0x112, 0xf>(x);
+  x += shifted<0x114, 0xf>(x);
+  x += shifted<0x118, 0xf>(x);
+  x += shifted<0x142, 0xa>(x);      // row_bcast 15 into rows 1 and 3
+  return x + shifted<0x143, 0xc>(x);   // row_bcast 31 into rows 2 and 3
 }
 // The same over the workgroup's 256 threads; total gets the last one's.
 __device__ __forceinline__ int scan256(int x, int* part, int& total) {
@@ -603,80 +604,6 @@ __device__ __forceinline__ void join_partials(const AttnArgs& a, const Unit& u, 
   }
 }
 
-// Up to this many keys a tile is not worth cutting: the join costs what walking over them does.  64
-// requests of up to 300 keys, e4m3: cut 17.6 us, whole 13.1; of up to 500, 16 bits: 18.5 and 15.2; one
-// request of 500: 10.8 and 11.1.  At 768: 16 e4m3 requests of up to 700 keys, cut 11.6, whole 14.5.
-constexpr int kWholeKeys = 512;
-
-
-// Runs `run(unit)` for the calling workgroup's share of the batch: the batch's work as one line of
-// steps of STEP keys, head by head, request by request, in tiles of SIZE rows, cut into one equal
-// stretch for each workgroup: a stretch may end one tile, hold others whole and begin the next.
-// Where there are few steps and no tile has more than kWholeKeys, a tile is one step and stays whole.
-// Without cuts a workgroup takes a whole tile.  `ends`: kMaxSplitBatch + 4 integers of LDS.
-template <int SIZE, int STEP, typename Run>
-__device__ __forceinline__ void walk_few(const AttnArgs& a, bool split, int* ends, Run run) {
-  constexpr int kLeast = kMinKeys > STEP ? kMinKeys / STEP : 1;
-  const int lane = threadIdx.x & 63;
-  Sums<true> sums(a, ends);
-  int step_keys = STEP, least = kLeast;
-  auto make = [&] {
-    sums.make(a, [&](const Request& q) {
-      const Shape s = shape_of<SIZE>(a, q, step_keys);
-      return s.tiles * s.steps;
-    });
-  };
-  if (split) {
-    make();
-    auto longer = [&] {
-      const Shape s = shape_of<SIZE>(a, sums.lane_request, STEP);
-      return lane < a.batch && s.tiles > 0 && s.steps * STEP > kWholeKeys;
-    };
-    if (a.batch <= 64 && sums.total * a.hk <= 2 * static_cast<int>(gridDim.x) && !__any(longer())) {
-      step_keys = 1 << 30;
-      least = 1;
-      make();
-    }
-  }
-  const int total = split ? sums.total * a.hk : gridDim.x;
-  const int each = split ? max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), least) : 1;
-  const int to = min(total, static_cast<int>(blockIdx.x + 1) * each);
-  for (int from = static_cast<int>(blockIdx.x) * each; from < to;) {
-    Unit unit;
-    int n = 1;
-    if (split) {
-      unit.head = from / sums.total;
-      int end;
-      const int x = from - unit.head * sums.total;
-      const int i = sums.find(a.batch, x, end);
-      const Request q = sums.request(a, i);
-      const Shape s = shape_of<SIZE>(a, q, step_keys);
-      const int steps = s.steps, local = x - (end - s.tiles * steps), tile = local / steps, step = local - tile * steps;
-      n = min(to - from, steps - step);
-      unit.r = rows_of(a, i, q, tile, SIZE);
-      tile_keys(a, unit.r, SIZE, unit.j0, unit.j1);
-      unit.j0 = max(unit.j0, s.low + step * step_keys);
-      unit.j1 = min(unit.j1, s.low + (step + n) * step_keys);
-      // the tile's pieces: a workgroup has at most two partial results, of its first tile and its last
-      const int begin = from - step, first = begin / each, last = (begin + steps - 1) / each;
-      unit.piece = static_cast<int>(blockIdx.x) - first;
-      unit.count = last - first + 1;
-      unit.slot0 = 2 * first + (begin == first * each ? 0 : 1);
-      unit.slot1 = 2 * (first + 1);
-      unit.slot_step = 2;
-    } else {
-      unit.head = blockIdx.x % a.hk;
-      if (!find_rows(a, blockIdx.x / a.hk, SIZE, true, unit.r)) return;
-      tile_keys(a, unit.r, SIZE, unit.j0, unit.j1);
-      unit.piece = 0;
-      unit.count = 1;
-    }
-    run(unit);
-    from += n;
-    if (from < to) __syncthreads();   // before the next tile takes the LDS over
-  }
-}
-
 // ------------------------------------------------------------------------------------------
 // Values that are not finite.  The product with v multiplies a masked key's value by a weight of
 // zero, which is right unless that value is infinite or NaN.  A workgroup with a result that is not
@@ -787,13 +714,22 @@ __device__ __forceinline__ v4f mfma16_odd(const v8s& v, const v8s& p, uint32_t s
 inline int64_t tile_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, bool split) {
   return (tile_bound(tokens, group, batch, 128) + (split ? extra_units(hk) : 0)) * hk;
 }
-inline int64_t few_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, int64_t capacity, bool split, int size = 32) {
-  const int64_t tiles = tile_bound(tokens, group, batch, size) * hk, pieces = tiles * ((capacity + kMinKeys - 1) / kMinKeys);
+inline int64_t few_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, int64_t capacity, bool split) {
+  const int64_t tiles = tile_bound(tokens, group, batch, 32) * hk, pieces = tiles * ((capacity + kMinKeys - 1) / kMinKeys);
   if (!split) return tiles;
   return pieces < kFewGroups ? pieces : kFewGroups;   // no more than the pieces have work
 }
-// Over an mxfp4 cache the kernel for few rows takes 16 or 32 at a time.
-inline int mx4_rows(int64_t tokens, int64_t group, int64_t batch) { return tokens * group <= 16 * batch ? 16 : 32; }
+// Over an mxfp4 cache: tiles of kMx4Rows rows; when cut, a key head's workgroups and all of them.
+constexpr int kMx4Rows = 16;
+inline int64_t mx4_head_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, int64_t capacity) {
+  const int64_t pieces = tile_bound(tokens, group, batch, kMx4Rows) * ((capacity + kMinKeys - 1) / kMinKeys);
+  const int64_t most = hk < kFewGroups ? kFewGroups / hk : 1;
+  return pieces < most ? pieces : most;
+}
+inline int64_t mx4_groups(int64_t tokens, int64_t batch, int64_t group, int64_t hk, int64_t capacity, bool split) {
+  return (split ? mx4_head_groups(tokens, batch, group, hk, capacity) : tile_bound(tokens, group, batch, kMx4Rows)) * hk;
+}
+static_assert(2 * kFewGroups <= kMaxSlots && 2 * kMaxSplitHeads <= kMaxSlots, "partial results of the cut for few rows");
 void launch_attn_tile(int dt, int head_dim, int format, const AttnArgs& a, hipStream_t s);
 void launch_attn_few(int dt, int head_dim, bool e4m3, const AttnArgs& a, hipStream_t s);
 void launch_attn_mx4_few(int dt, int head_dim, const AttnArgs& a, hipStream_t s);
