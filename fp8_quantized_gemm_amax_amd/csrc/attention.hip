@@ -12,8 +12,9 @@ namespace attn {
 namespace {
 
 // Whether a batch goes to the kernel for few rows: where its requests have at most 32 rows a key head on
-// average (64 over an e4m3 cache, which the kernel for many rows has to widen on the way), and none, as
-// far as max_new says, has more than 512, since that one's keys are read once for every 32 rows.
+// average (64 over an e4m3 cache and 48 over an mxfp4 one, which the kernel for many rows has to widen on
+// the way), and none, as far as max_new says, has more than 512, since that one's keys are read once for
+// every 32 rows (16 over mxfp4).
 // Kernel for many rows against the one for few, us on one card, 128 channels, requests of equal rows over
 // half to all of so many keys:
 //   16 bits, rows      4            16           32           40
@@ -26,10 +27,16 @@ namespace {
 //      8 x 2000  27.0 : 16.0  26.8 : 22.8  28.1 : 30.0  30.4 : 31.5
 //     64 x 4000   157 :  87    159 : 102    162 : 175    163 : 233
 //     1 x 100000  108 :  50    103 :  90    105 :  97    113 : 113
+//   mxfp4, rows        4            32           48           64           80
+//     24 x 500   19.1 : 10.7  19.2 : 12.1  19.6 : 21.4  19.7 : 22.4  20.2 : 21.7
+//      8 x 2000  23.7 : 13.3  22.5 : 18.0  23.9 : 23.7  24.0 : 22.1  27.4 : 28.3
+//     64 x 4000   141 :  52    146 :  93    146 : 135    151 : 172    151 : 212
+//     1 x 100000   93 :  33     87 :  56     89 :  66     89 :  80     98 :  91
 // No number of rows suits every length: at the limits the kernel for few is up to 23% faster over short
-// caches and up to 37% slower over long ones in 16 bits (above 12 rows), 25% faster to 8% slower over e4m3.
+// caches and up to 37% slower over long ones in 16 bits (above 12 rows), 25% faster to 8% slower over e4m3,
+// 25% faster to 9% slower over mxfp4.
 bool few_rows(int format, int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
-  return std::min(max_new, tokens) * group <= 512 && tokens * group <= (format == FP8_KV_SAME ? 32 : 64) * batch;
+  return std::min(max_new, tokens) * group <= 512 && tokens * group <= (format == FP8_KV_SAME ? 32 : format == FP8_KV_E4M3 ? 64 : 48) * batch;
 }
 
 // Joins the partial results of the launch for many rows, of 128 rows each: a thread takes one row and
@@ -135,8 +142,9 @@ int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t 
     return workspace_bytes(few ? 2 * std::max<int64_t>(kFewGroups, hk) : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
   };
   // Enough for every format of the cache.
-  return std::max(bytes(few_rows(FP8_KV_SAME, max_new, hq / hk, tokens, batch)),
-                  bytes(few_rows(FP8_KV_E4M3, max_new, hq / hk, tokens, batch)));
+  int64_t most = 0;
+  for (int format : {FP8_KV_SAME, FP8_KV_E4M3, FP8_KV_MXFP4}) most = std::max(most, bytes(few_rows(format, max_new, hq / hk, tokens, batch)));
+  return most;
 }
 
 }  // namespace fp8amax

@@ -14,6 +14,10 @@
 // 1768.  12 packed prompts of up to 2048 tokens 58 us: 41 steps of 64 keys a CU at 0.95 us where two
 // workgroups share it are 39 us, the rest is that the longest tiles, 32 steps, share to their end.  3442
 // new tokens of four requests over up to 16000 cached keys 455 us (1032 TFLOP/s).
+// Over an mxfp4 cache a tile's codes are converted on their way into LDS, 32 conversions and 8 LDS writes a
+// wave, which the next products' start waits for: 3037 new tokens of four requests over up to 16000 keys 325 us
+// (915 TFLOP/s) where a cache of 16-bit numbers takes 298 to 307.  With those spread between the products,
+// from a second set of registers or the first, the registers spill: 361 to 569 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -60,7 +64,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
   Unit unit;
   if (!unit_of<kRows, kPaged>(a, split, lds, unit)) return;
   const Rows& r = unit.r;
-  const int h = unit.head, j0 = unit.j0, j1 = unit.j1;
+  // Scalars to the compiler, so that places and descriptors are scalar work (with the scheduling below: 339 us
+  // to 325 at 128 channels, 261 to 254 at 64); the other kernels keep their code.
+  auto uniform = [&](int x) { return kMx4 ? __builtin_amdgcn_readfirstlane(x) : x; };
+  const int h = uniform(unit.head), j0 = uniform(unit.j0), j1 = uniform(unit.j1), len = uniform(r.len), request = uniform(r.request);
 
   const float c = a.scale * kLog2e;
   v16f o[D / 32];
@@ -98,7 +105,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
     auto page_of = [&](int t) -> int {
       if constexpr (!kPaged) return 0;
       const int at = t + 16 * wave;
-      return at < r.len ? scalar_int(a.table + static_cast<int64_t>(r.request) * a.width + (at >> a.page_shift)) : -1;
+      return at < len ? scalar_int(a.table + static_cast<int64_t>(request) * a.width + (at >> a.page_shift)) : -1;
     };
     // Where the wave's 16 keys of the tile at key t lie: their first row, and how many there are.
     struct Place {
@@ -106,7 +113,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
       int n;
     };
     auto place = [&](int t, int page) -> Place {
-      const int at = t + 16 * wave, have = min(max(r.len - at, 0), 16);
+      page = uniform(page);
+      const int at = t + 16 * wave, have = min(max(len - at, 0), 16);
       if constexpr (!kPaged) return {r.begin + at, have};
       const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
       return {((static_cast<int64_t>(there ? page : 0) * a.hk + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1)), there ? have : 0};
@@ -357,7 +365,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           for (int n = 0; n < kSteps / 2 + (w > 0 ? D / 32 : 0); ++n) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // MFMA
             __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);    // LDS reads
-            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    // VALU
+            __builtin_amdgcn_sched_group_barrier(0x002, kMx4 ? 6 : 4, 0);    // VALU (mxfp4, 4, 5, 6, 8: 276, 256, 254, 259 us at 64 channels)
             __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);    // exponentials
           }
         }
