@@ -14,11 +14,11 @@
 // while this one is multiplied.
 // Bound by the reads of the cache, 144 bytes a key and head of 128 channels, once their number is large.
 // Measured on one card, 32 heads on 8 of 128 channels, bf16, one new token a request: 128 requests of up to
-// 8192 keys 95 us (431 MB, 4.5 TB/s), four of up to 131072 53 us (232 MB, 4.4 TB/s); the walks inside read
+// 8192 keys 92 us (431 MB, 4.7 TB/s), four of up to 131072 53 us (232 MB, 4.4 TB/s); the walks inside read
 // at 6.8 TB/s, and around them a call has 12 us that do not depend on the keys: the launch, the cut (one
 // microsecond), the first reads' latency, the join of the waves (two) and of the pieces (two to five).  One
 // request of 701 keys 8.4 us.  Of other arrangements, one wider (32 rows for a tile of 64 keys) spilled and
-// took 153 us where two passes over 16 rows take 71; a second tile on its way, three waves a SIMD, eight
+// took 153 us where two passes over 16 rows take 65; a second tile on its way, three waves a SIMD, eight
 // waves a workgroup and 768 to 2048 workgroups were all slower than this with two workgroups a CU.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -39,6 +39,15 @@ static_assert(kStep == kMinKeys, "pieces of the cut");
 // whole 8.7, 10.2 and 12.0 us, cut 9.0, 9.2 and 9.4; 16 requests over 8: whole 9.1, 10.8 and 15.3, cut
 // 11.8, 12.9 and 13.0.
 constexpr int kWholeKeys = 512;
+// What a tile costs a workgroup besides its keys (finding it, its queries, the first codes' latency, the
+// join and the result: 3.7 us, measured inside 64 requests' step), in steps; counted where a workgroup has
+// kManySteps of them or more.  With it and without, 32 heads: 64 ragged requests of up to 8192 keys 49.4
+// and 52.8 us, 128 of them 92.2 and 95.6, 32 of up to 2048 with a key head a head 34.5 and 40.4, 64 of up
+// to 4096 over 4 heads of 64 channels 16.8 and 20.2.  From two steps on rather than three, 64 of up to 3000
+// over 4 heads of 128: 18.6, not 21.7, 16 of 2000 keys each, two whole steps a workgroup: 16.9, not 15.1.
+template <int D>
+constexpr int kTileCost = D == 64 ? 2 : 1;
+constexpr int kManySteps = 2;
 #define FP8_GLOBAL __attribute__((address_space(1)))
 
 // x / d by d's reciprocal, x and d not negative: the quotient is off by one or two where it is below 2^22.
@@ -415,11 +424,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_mx4_few_kernel(AttnArgs a
   }
   // The work of a key head (blockIdx.y) as one line of steps, request by request, in tiles of kRows rows,
   // cut into stretches that differ by a step at most, one for each of the head's workgroups: a stretch may
-  // end one tile, hold others whole and begin the next.  Where there are few steps and no tile has more
-  // than kWholeKeys, a tile is one step and stays whole.  Every workgroup makes the cut for itself; a
+  // end one tile, hold others whole and begin the next.  Where there are many steps, a tile begins with
+  // `cost` steps without keys, so that a workgroup with more tiles has fewer keys.  Where there are few steps
+  // and no tile has more than kWholeKeys, a tile is one step and stays whole.  Every workgroup makes the cut for itself; a
   // division costs as much as a tenth of a tile, so there are few, by reciprocals.
   Sums<true> sums(a, ends);
   bool cut_tiles = true;
+  int cost = 0;
   auto shape = [&](const Request& q) {
     Shape s;
     s.tiles = static_cast<int>((static_cast<int64_t>(q.tokens) * a.group + kRows - 1) / kRows);
@@ -429,10 +440,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_mx4_few_kernel(AttnArgs a
   };
   auto work = [&](const Request& q) {
     const Shape s = shape(q);
-    return s.tiles * s.steps;
+    return s.tiles * (s.steps + cost);
   };
   sums.make(a, work);
   const int groups = gridDim.x;
+  if (sums.total / kManySteps >= groups) {
+    cost = kTileCost<D>;
+    sums.make(a, work);
+  }
   if (a.batch <= 64 && sums.total <= 2 * groups) {
     const Shape s = shape(sums.lane_request);
     if (!__any(lane < a.batch && s.tiles > 0 && s.steps * kStep > kWholeKeys)) {
@@ -458,9 +473,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_mx4_few_kernel(AttnArgs a
     const int i = sums.find(a.batch, from, end);
     const Request q = sums.request(a, i);
     const Shape s = shape(q);
-    const int local = from - (end - s.tiles * s.steps);
-    const int tile = uniform(quotient(local, s.steps, 1.0f / static_cast<float>(s.steps))), step = local - tile * s.steps;
-    const int n = min(to - from, s.steps - step);
+    const int all = s.steps + cost, local = from - (end - s.tiles * all);
+    const int tile = uniform(quotient(local, all, 1.0f / static_cast<float>(all))), at = local - tile * all;
+    const int n = min(to - from, all - at);      // of them `cost` without keys in front
+    const int start = from - at, stop = start + all;
+    from += n;
+    if (at + n <= cost) continue;                // (then the stretch ends here)
+    const int step = max(at - cost, 0), steps = at + n - cost - step;
     unit.r = rows_of(a, i, q, tile, kRows);
     const int last = uniform(token_of(min(unit.r.row0 + kRows, unit.r.rows) - 1));
     const int low = a.window > 0 ? max(0, unit.r.pos0 + uniform(token_of(unit.r.row0)) - a.window + 1) : 0;
@@ -468,19 +487,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_mx4_few_kernel(AttnArgs a
     unit.j0 = min(low, unit.j1) & ~(kKeys - 1);
     if (cut_tiles) {
       unit.j0 = max(unit.j0, s.low + step * kStep);
-      unit.j1 = min(unit.j1, s.low + (step + n) * kStep);
+      unit.j1 = min(unit.j1, s.low + (step + steps) * kStep);
     }
     // the tile's pieces: a workgroup has at most two partial results, of its first tile and its last
-    const int start = from - step, stop = start + s.steps;
-    const int first = start >= begin ? b : owner(start), final = stop <= cut(b + 1) ? b : owner(stop - 1);
+    const int first = start + cost >= begin ? b : owner(start + cost), final = stop <= cut(b + 1) ? b : owner(stop - 1);
     const int slots = 2 * static_cast<int>(blockIdx.y) * groups;
     unit.piece = b - first;
     unit.count = final - first + 1;
-    unit.slot0 = slots + 2 * first + (start == cut(first) ? 0 : 1);
+    unit.slot0 = slots + 2 * first + (start <= cut(first) ? 0 : 1);
     unit.slot1 = slots + 2 * (first + 1);
     unit.slot_step = 2;
     run(unit);
-    from += n;
     if (from < to) __syncthreads();   // before the next tile takes the LDS over
   }
 }

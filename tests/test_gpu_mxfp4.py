@@ -90,8 +90,8 @@ def test_single_tokens(page, dim, dtype):
 @pytest.mark.parametrize("page", [16, 32, 128])
 def test_chunks(page, dim, dtype):
     run4([1, 40, 64, 129, 200, 333], [1, 40, 2, 100, 33, 70], 4, 2, dim, page, dtype)      # many rows
-    run4([9, 40, 64, 129, 200, 333], [9, 10, 2, 7, 13, 8], 8, 2, dim, page, dtype)         # few: 32 at a time
-    run4([9, 40, 64, 129, 200, 333], [3, 2, 2, 7, 1, 8], 4, 2, dim, page, dtype)           # few: 16 at a time
+    run4([9, 40, 64, 129, 200, 333], [9, 10, 2, 7, 13, 8], 8, 2, dim, page, dtype)         # few, two tokens' rows and more a tile
+    run4([9, 40, 64, 129, 200, 333], [3, 2, 2, 7, 1, 8], 4, 2, dim, page, dtype)           # few
 
 
 @pytest.mark.parametrize("hq,hk", [(1, 1), (5, 1), (8, 1), (16, 2), (32, 32), (40, 1), (64, 1), (12, 4)])
@@ -114,6 +114,16 @@ def test_long(dtype):
     run4([5000], [2], 2, 2, 64, 16, dtype)
     run4([9000, 3, 2500], [5, 3, 6], 8, 2, 128, 64, dtype)
     run4([4000], [150], 4, 1, 128, 16, dtype)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("requests,kv_heads,window", [(24, 64, 0), (90, 32, 0), (90, 16, 500), (3, 256, 0)])
+def test_many_steps(requests, kv_heads, window, dim, dtype):
+    """Several pieces of 256 keys a workgroup, cut wherever they end: few workgroups a key head."""
+    rng = np.random.default_rng(requests)
+    lens = [int(x) for x in rng.choice([1, 5, 255, 256, 257, 511, 700, 1300, 2100], requests)]
+    lens[-1] = 1800
+    run4(lens, [0 if r % 11 == 3 else 1 for r in range(requests)], kv_heads, kv_heads, dim, 16, dtype, window=window)
 
 
 @TYPES
