@@ -10,7 +10,10 @@
 //   rowwise: scale = sa[m] * sb[n], one scale per token and per output channel (the
 //     Transformer Engine page §5, per-channel scaling), applied once like tensorwise;
 //   int8: the same over 8-bit integers, whose products are summed exactly in 32 bits (K up to
-//     131071: 128 * 128 K stays below 2^31) and rounded to float32 once, in the epilogue.
+//     131071: 128 * 128 K stays below 2^31) and rounded to float32 once, in the epilogue.  At the
+//     matrix unit's rate for e4m3, and within 5% of that mode's times: 4096x14336x4096 207 us (2.33
+//     POP/s; e4m3 198), 8192^3 405 us (2.72; 384), where operands of zeros take 174 and 331: power
+//     bounds it.
 //
 // Kernels (CDNA4).  Every kernel walks K in 128-byte slabs and multiplies with
 // v_mfma_scale_f32_16x16x128_f8f6f4 (unit E8M0 scales, i.e. a plain FP8 product, or the

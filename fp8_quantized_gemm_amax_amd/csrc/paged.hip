@@ -140,7 +140,9 @@ constexpr int kAppendThreads = 256;
 // the 16 bytes as they are.  Bound by memory: 16384 tokens of 8 heads of 128 to e4m3, 102 MB, take
 // 23.4 us (4.4 TB/s; a 2 GiB copy runs at 4.9).  Key and value of a row in one thread, so that two
 // loads are under way: with one tensor a workgroup it took 23% longer; with two and four rows a
-// thread 2% and 20%.
+// thread 2% and 20%.  To mxfp4 a lane's eight channels are a quarter of a block, whose largest magnitude
+// four lanes find by DPP, and 4 bytes of codes: the same call 20.7 us (85 MB, 4.1 TB/s), 64 tokens 2.6 us
+// in a graph, where e4m3 takes 2.8 and a launch by itself 2.
 template <int DT, int D, int FORMAT>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8;
@@ -283,9 +285,17 @@ __device__ __forceinline__ void store_row(void* cache, void* scales, int64_t row
   }
 }
 
-// Rotation and append.  A group of D / 16 lanes takes a unit of a token: kHeads query heads, or the
-// keys and values of kHeads / 2 key heads, so that kHeads rows' loads are in flight a lane and the
-// table's row is read once for them.
+// Rotation and append: of a token at position p, channels a and b of a pair and the pair's angle become
+//   a' = a cos - b sin, b' = b cos + a sin   (float32, from the table's row p),
+// queries are rounded to their type and keys, with the values as they are, to the cache's format: the
+// rotated keys never lie in memory in between, where a call for each of the three would read and write
+// them once more.
+// A group of D / 16 lanes takes a unit of a token: kRopeHeads query heads, or the keys and values of half
+// as many key heads, whose loads are all in flight while the table's row, that comes after the position,
+// is on its way.  Bound by memory: 16384 tokens of 32 heads over 8 of 128 channels into an e4m3 cache, 373
+// MB, 69 us (5.4 TB/s; a copy of 1 GiB runs at 5.2), into mxfp4 71 us, 64 channels 45 us; and by the chain
+// of reads where there are few: 64 tokens 3.1 us in a graph.  With four heads a unit and with eight, both
+// sizes were slower: 73.8 and 81.2 us, 5.0 and 8.3 us (fewer workgroups, longer each).
 constexpr int kRopeHeads = 2;
 template <int DT, int D, int FORMAT, bool PAIRS>
 __global__ __launch_bounds__(kAppendThreads) void rope_append_kernel(RopeArgs a) {

