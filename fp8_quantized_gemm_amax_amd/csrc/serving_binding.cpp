@@ -295,6 +295,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const int64_t rotary = table.size(1);
   TORCH_CHECK_VALUE(rotary >= 16 && rotary <= dim && rotary % 16 == 0, "rotary_dim must be a multiple of 16, 16 .. ", dim, ", got ", rotary);
   const at::Tensor slots = vec(tensor(a[5], "slots"), "slots", at::kLong, tokens);
+  const int interleaved = PyObject_IsTrue(a[10]);
+  if (interleaved < 0) return nullptr;
   for (const at::Tensor* t : {&c.k, &c.v, &c.ks, &c.vs})
     for (const at::Tensor* in : std::initializer_list<const at::Tensor*>{&q, &k, &v, &positions, &table, &slots})
       TORCH_CHECK_VALUE(!t->defined() || !in->defined() || !overlaps(*t, *in), "a cache overlaps an input");
@@ -312,7 +314,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const fp8_status_t code = rope_fn(
       raw(q), k.data_ptr(), v.data_ptr(), dt, tokens, with_q ? q.size(1) : 0, heads, static_cast<int32_t>(dim), with_q ? q.stride(0) : 0,
       with_q ? q.stride(1) : 0, k.stride(0), k.stride(1), v.stride(0), v.stride(1), ptr<int32_t>(positions), ptr<float>(table), table.size(0),
-      static_cast<int32_t>(rotary), PyObject_IsTrue(a[10]) == 1, ptr<int64_t>(slots), c.k.size(0), static_cast<int32_t>(page), c.format,
+      static_cast<int32_t>(rotary), interleaved, ptr<int64_t>(slots), c.k.size(0), static_cast<int32_t>(page), c.format,
       c.k.data_ptr(), c.v.data_ptr(), raw(c.ks), raw(c.vs), raw(out), stream_of(a[12]));
   if (code != FP8_OK) return status(code);
   if (!with_q) Py_RETURN_NONE;

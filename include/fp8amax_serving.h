@@ -90,7 +90,8 @@ fp8_status_t fp8_paged_plan(const int32_t* cached, const int32_t* added, int64_t
  * in one launch.
  *   k, v    : [tokens, kv_heads, head_dim] of dt, strided.
  *   slots   : int64 [tokens]; a slot outside [0, pages * page_size) is skipped (-1: padding).
- *             Two tokens with one slot leave either's values.
+ *             Two tokens with one slot leave parts of either's row there (a scale and codes that are not
+ *             of one token, too): a step's slots differ.
  *   k_cache, v_cache : as above; k_scales, v_scales : float32 (FP8_KV_E4M3) or bytes (FP8_KV_MXFP4),
  *   NULL for FP8_KV_SAME.
  */

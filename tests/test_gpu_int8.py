@@ -124,6 +124,12 @@ def test_large_tiles(M, N, K):
     check_gemm(operands(M, N, K, seed=N), "bf16")
 
 
+@pytest.mark.parametrize("M,N", [(0, 5), (5, 0), (0, 0)])
+def test_empty_products(M, N):
+    out = fp8.int8_gemm_scaled_rowwise(*(t.to(DEV) for t in operands(M, N, 32)))
+    assert out.shape == (M, N) and out.dtype == torch.bfloat16
+
+
 @pytest.mark.parametrize("M", [1, 3, 9, 40, 130])
 def test_largest_sums(M):
     """K at its limit with codes of -128 and 127 only: sums up to 2^31 - 2^18, exact."""

@@ -77,6 +77,7 @@ def four(*tail):
     (V, "out must have shape", dict(out=b16(3, 4, 32))),
     (T, "out must be", dict(out=b16(3, 4, 64).half())),
     (T, "k must be a tensor", dict(k=None)),
+    (RuntimeError, "ambiguous", dict(interleaved=torch.zeros(2))),
     (V, "k_scales must have shape", dict(kc=four(32), vc=four(32), k_scales=four(1), v_scales=four(1))),
     (V, "v_scales must have shape", dict(kc=four(32), vc=four(32), k_scales=four(2), v_scales=four(1))),
     (V, "go together", dict(kc=four(32), vc=four(32), k_scales=four(2))),
