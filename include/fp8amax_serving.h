@@ -45,7 +45,8 @@
  *
  * Sizes.  FP8_ERR_TOO_LARGE, before any HIP call, where tokens * heads passes 2^30 or the work would
  * need 2^24 workgroups or more (a launch holds less than 2^32 threads): a workgroup appends 16 rows
- * of 128 channels or 32 of 64 (with rotation at least as many), and attends for 128 rows or 32 of one request and key head.
+ * of 128 channels or 32 of 64 (with rotation at least as many), and attends for 128 rows or 32 of one request and key
+ * head (16 over FP8_KV_MXFP4).
  */
 #ifndef FP8AMAX_SERVING_H
 #define FP8AMAX_SERVING_H
