@@ -27,7 +27,7 @@
 //   gemm_skinny_kernel / gemm_grouped_kernel: 17-128 tokens (and the mixture-of-experts
 //     chunks), weight rows streamed into registers, the tokens staged in LDS by one wave.
 //   gemm_fp8_kernel: K not a multiple of 128 (or too large for 32-bit buffer offsets),
-//     slabs staged global -> VGPR -> LDS with a zero-filled K tail.
+//     slabs staged global -> VGPR -> LDS with a zero-filled K tail; e4m3 only.
 // 1-16 tokens go to the decode kernels of gemv.hip.  The LDS slab layout and the tile order
 // are in gemm_common.hpp; which kernel, tile and grid a shape gets is plan_gemm in
 // gemm_plan.hpp, whose 32-bit range and offset figures bound the buffer arithmetic here.
@@ -164,12 +164,11 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(
     }
   };
 
-  using Acc = typename Product<SM>::Acc;
-  Acc acc[TM][TN];
+  v4f acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   float scl[TM], scl_next[TM];
   int ea[TM], ea_next[TM], eb = 127, eb_next = 127;
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], scl[i], acc[i][j][r]);
         } else {
-          acc[i][j] = Product<SM>::add(bf, af[i], acc[i][j]);
+          acc[i][j] = mfma_fp8(bf, af[i], acc[i][j]);
         }
       }
     }
@@ -233,7 +232,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(
       uint32_t h[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[i][j][r], ff(alpha, i, j, r)));
+        h[r] = f32_to_out_bits<OUT>(acc[i][j][r] * ff(alpha, i, j, r));
       if (vec_store && n + 3 < N) {
         *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       } else {
@@ -274,6 +273,27 @@ __device__ __forceinline__ void wait_slabs_ahead(int ahead) {
   } else {
     wait_vmcnt<0>();
   }
+}
+
+// Slabs of K, and where in a row of A a chunk of a slab lies.  8-bit integers may have K % 128 != 0 in the
+// DMA kernels: A's chunks past K are asked for past any range and read as zeros, and what lies in their
+// place in B, the next row's codes or zeros past the last one, multiplies them: integers have no NaN.
+// (e4m3 has, and keeps the staged kernel.)  21 x 6263 x 9264 13.1 us, in the staged kernel 68; 32 x 46 x
+// 13392 14.6 and 83, 4096 x 14336 x 4112 273 and 357.
+template <int SM>
+__device__ __forceinline__ int slabs_of(int K) { return SM == SM_INT8 ? (K + kSlab - 1) / kSlab : K / kSlab; }
+template <int SM>
+__device__ __forceinline__ uint32_t a_column(uint32_t column, int K) {
+  return SM != SM_INT8 || column < static_cast<uint32_t>(K) ? column : kOOB;
+}
+
+// Four outputs of a row in one store.  With 8-bit integers also where N is no multiple of 4 and a row starts
+// at any even address, which global memory allows: 1887 x 3775 x 2016 28.2 us, output by
+// output 32.8; 2255 x 1961 x 352 11.4 and 17.0.
+template <int SM>
+__device__ __forceinline__ void store4(uint16_t* to, const uint2& h) {
+  if constexpr (SM == SM_INT8) __builtin_memcpy(to, &h, 8);
+  else *reinterpret_cast<uint2*>(to) = h;
 }
 
 template <int BM, int BN, int WM, int WN>
@@ -355,13 +375,15 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
   const uint32_t row_off_bp = static_cast<uint32_t>(((wp * IB) * 8 + (lane >> 3)) * K);
 
   // K % 128 == 0 here (plan_gemm sends other K to the staged kernel), so every
-  // offset is plain arithmetic and only the row range check can zero a chunk
+  // offset is plain arithmetic and only the row range check can zero a chunk; except with
+  // 8-bit integers (see a_column)
   auto issue_pair = [&](int s, int st) {
     const uint32_t k0 = static_cast<uint32_t>(s * kSlab);
+    const uint32_t a_even = a_column<SM>(k0 + c_even, K), a_odd = a_column<SM>(k0 + c_odd, K);
 #pragma unroll
     for (int j = 0; j < IA; ++j)
       dma16(ra, lds_addr(Abuf[st] + (wp * IA + j) * 1024),
-            row_off_p + static_cast<uint32_t>(j * 8 * K) + k0 + (((wp * IA + j) & 1) ? c_odd : c_even));
+            row_off_p + static_cast<uint32_t>(j * 8 * K) + (((wp * IA + j) & 1) ? a_odd : a_even));
 #pragma unroll
     for (int j = 0; j < IB; ++j)
       dma16(rb, lds_addr(Bbuf[st] + (wp * IB + j) * 1024),
@@ -380,12 +402,13 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
       issue_pair(s, st);
     }
     const uint32_t k0 = static_cast<uint32_t>(s * kSlab);
+    const uint32_t a_even = a_column<SM>(k0 + c_even, K), a_odd = a_column<SM>(k0 + c_odd, K);
     uint8_t* As = Abuf[st];
     uint8_t* Bs = Bbuf[st];
 #pragma unroll
     for (int j = 0; j < IA; ++j)
       dma16(ra, lds_addr(As + (w * IA + j) * 1024),
-            row_off + static_cast<uint32_t>(j * 8 * K) + k0 + (((w * IA + j) & 1) ? c_odd : c_even));
+            row_off + static_cast<uint32_t>(j * 8 * K) + (((w * IA + j) & 1) ? a_odd : a_even));
 #pragma unroll
     for (int j = 0; j < IB; ++j)
       dma16(rb, lds_addr(Bs + (w * IB + j) * 1024),
@@ -399,7 +422,7 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
                   : static_cast<uint32_t>(((j * 64 + lane) * KG + s) * 4));
     }
   };
-  const int nslabs = K / kSlab;
+  const int nslabs = slabs_of<SM>(K);
   auto frag = [&](const uint8_t* base, int row) -> v8i {
     const int sw = swz(row);
     const v4i lo = *reinterpret_cast<const v4i*>(base + row * kSlab + (((2 * kq) ^ sw) << 4));
@@ -525,7 +548,7 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
 
   float alpha = 1.0f;
   if constexpr (SM == SM_TENSOR) alpha = sa[0] * sb[0];
-  const bool vec_store = (N & 3) == 0;
+  const bool vec_store = SM == SM_INT8 || (N & 3) == 0;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int m = m0 + wm * WM + 16 * i + r16;
@@ -539,7 +562,7 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
       for (int r = 0; r < 4; ++r)
         h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[i][j][r], ff(alpha, i, j, r)));
       if (vec_store && n + 3 < N) {
-        *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        store4<SM>(crow + n, make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16)));
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -582,7 +605,7 @@ struct SkinnyShape {
 // The few-token product of one workgroup: A rows [0, M) (M <= 16 MB) times the 16 cw NB
 // weight rows of block `nblk`, written to C rows [0, M).  Abuf and Sbuf are the workgroup's
 // LDS rings; every wave of the workgroup calls this once per tile, and each call passes
-// exactly K / 128 barriers in every wave.
+// exactly slabs_of(K) barriers in every wave.
 template <int SM, int OUT, int NB, int MB, int NS, int UNROLL>
 __device__ __forceinline__ void skinny_body(
     const uint8_t* __restrict__ qa, const void* __restrict__ sa_, const uint8_t* __restrict__ qb,
@@ -601,7 +624,7 @@ __device__ __forceinline__ void skinny_body(
 
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nslabs = K / kSlab;                      // K % 128 == 0 on this path
+  const int nslabs = slabs_of<SM>(K);                // K % 128 == 0 on this path, but with 8-bit integers
   const int KG = nslabs;
   const int KG4 = static_cast<int>(e8m0_row_bytes(KG));   // UE8M0: bytes per scale row
   // Activation scales of a slab lie a scale row apart, one cache line per token, so fetching
@@ -626,10 +649,10 @@ __device__ __forceinline__ void skinny_body(
     const uint32_t row_off = static_cast<uint32_t>((lane >> 3) * K);
     auto issue = [&](int s, int st, bool scales) {
       const uint32_t k0 = static_cast<uint32_t>(s * kSlab);
+      const uint32_t a_even = a_column<SM>(k0 + c_even, K), a_odd = a_column<SM>(k0 + c_odd, K);
 #pragma unroll
       for (int j = 0; j < IA; ++j)
-        dma16(ra, lds_addr(Abuf[st] + j * 1024),
-              row_off + static_cast<uint32_t>(j * 8 * K) + k0 + ((j & 1) ? c_odd : c_even));
+        dma16(ra, lds_addr(Abuf[st] + j * 1024), row_off + static_cast<uint32_t>(j * 8 * K) + ((j & 1) ? a_odd : a_even));
       if constexpr (BLOCKWISE) {
         if (scales) {
 #pragma unroll
@@ -782,7 +805,7 @@ __device__ __forceinline__ void skinny_body(
 
   float alpha = 1.0f;
   if constexpr (SM == SM_TENSOR) alpha = sa[0] * sb[0];
-  const bool vec_store = (N & 3) == 0;
+  const bool vec_store = SM == SM_INT8 || (N & 3) == 0;
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
     const int m = 16 * b + r16;
@@ -795,7 +818,7 @@ __device__ __forceinline__ void skinny_body(
 #pragma unroll
       for (int r = 0; r < 4; ++r) h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[j][b][r], ff(alpha, b, j, r)));
       if (vec_store && n + 3 < N) {
-        *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        store4<SM>(crow + n, make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16)));
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -936,7 +959,8 @@ bool run_launch(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, c
     case FP8_KERNEL_GEMV_MFMA:
       return launch_gemv(SM, OUT, L, qa, sa, qb, sb, M, N, K, c, s);
     case FP8_KERNEL_STAGED:
-      if (L.tile_m == 16) launch_cfg<16, 256, 16, 64, SM, OUT>(L, qa, sa, qb, sb, M, N, K, c, s);
+      if constexpr (SM == SM_INT8) return false;       // the DMA kernels take every K
+      else if (L.tile_m == 16) launch_cfg<16, 256, 16, 64, SM, OUT>(L, qa, sa, qb, sb, M, N, K, c, s);
       else launch_cfg<128, 128, 64, 64, SM, OUT>(L, qa, sa, qb, sb, M, N, K, c, s);
       return true;
     case FP8_KERNEL_SKINNY:

@@ -50,9 +50,11 @@ constexpr int kDynStreamWaves = 4;
 constexpr int kDynStreamPerCu = 3;
 constexpr bool dynamic_stream(int sm) { return sm == SM_TENSOR || sm == SM_ROW; }
 
-// Whether the LDS-DMA kernels take K: whole slabs, and 256 rows of K bytes (the largest
-// tile) within 32-bit offsets.  Other K go to the register-staged kernel.
-inline bool dma_fits(int64_t K) { return K % kSlabK == 0 && K * 256 <= kLimit32; }
+// Whether the LDS-DMA kernels take K: whole slabs (8-bit integers: any K), and 256 rows of K bytes
+// (the largest tile) within 32-bit offsets.  Other K go to the register-staged kernel.
+inline bool dma_fits(int sm, int64_t K) { return (sm == SM_INT8 || K % kSlabK == 0) && K * 256 <= kLimit32; }
+// Bytes past a row's end that the last slab's offsets reach.
+inline int64_t tail_reach(int64_t K) { return K % kSlabK == 0 ? 0 : kSlabK; }
 
 inline fp8_gemm_launch_t make_launch(int kernel, int64_t tile_m, int64_t tile_n, int variant, int waves,
                                      int64_t grid, int64_t threads, int64_t n_begin, int64_t n_end) {
@@ -83,7 +85,7 @@ inline fp8_gemm_launch_t tile_launch(int sm, int64_t M, int64_t n0, int64_t n1, 
   l.paired = paired ? 1 : 0;
   const int64_t SR = scale_row_bytes(sm, K);
   l.max_range = std::max({std::min<int64_t>(BM, M) * K, std::min<int64_t>(BN, n) * K, std::min<int64_t>(WM, M) * SR});
-  l.max_offset = std::max({int64_t{BM} * K, int64_t{BN} * K, int64_t{WM} * SR});
+  l.max_offset = std::max({int64_t{BM} * K, int64_t{BN} * K, int64_t{WM} * SR}) + tail_reach(K);
   return l;
 }
 
@@ -125,7 +127,7 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K) {
   // K tail: the register-staged kernel zero-fills it.  It also takes K so large that 256
   // rows of K bytes overflow the 32-bit buffer offsets of the DMA kernels.  It addresses
   // its operands with 64-bit pointers and forms no buffer descriptors.
-  if (!dma_fits(K)) {
+  if (!dma_fits(sm, K)) {
     const int BM = M <= 16 ? 16 : 128, BN = M <= 16 ? 256 : 128;
     l = make_launch(FP8_KERNEL_STAGED, BM, BN, 2, 4, cdiv(M, BM) * cdiv(N, BN), 256, 0, N);
     return p;
@@ -151,7 +153,7 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K) {
     l = make_launch(FP8_KERNEL_SKINNY, M, rows, MB, cw, cdiv(N, rows), 64 * (cw + 1), 0, N);
     const int64_t scale_dma = slab_scaled(sm) ? cdiv(16 * MB, 64) * 64 * SR : 0;   // 64 rows per scale DMA
     l.max_range = std::max({M * K, M * SR, std::min<int64_t>(16, N) * K, SR});
-    l.max_offset = std::max({16 * int64_t{MB} * K, 16 * K, scale_dma, cdiv(M * SR, 256) * 256});
+    l.max_offset = std::max({16 * int64_t{MB} * K, 16 * K, scale_dma, cdiv(M * SR, 256) * 256}) + tail_reach(K);
     return p;
   }
   const int64_t big_tiles = cdiv(M, 256) * cdiv(N, 256);

@@ -124,6 +124,14 @@ def test_large_tiles(M, N, K):
     check_gemm(operands(M, N, K, seed=N), "bf16")
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 5632, 272), (1024, 1100, 528), (600, 9000, 144), (4100, 4200, 112), (2048, 9000, 240), (300, 300, 16),
+                                   (129, 5, 1568), (2255, 1961, 352), (4096, 4400, 6160), (21, 700, 9264), (128, 130, 1008), (33, 46, 13392)])
+def test_last_slab_of_every_length(M, N, K):
+    """K % 128 != 0: zeros of A stand against whatever lies behind a row of B."""
+    ops = operands(M, N, K, seed=K)
+    check_gemm(ops, "f16" if K % 32 else "bf16")
+
+
 @pytest.mark.parametrize("M,N", [(0, 5), (5, 0), (0, 0)])
 def test_empty_products(M, N):
     out = fp8.int8_gemm_scaled_rowwise(*(t.to(DEV) for t in operands(M, N, 32)))
