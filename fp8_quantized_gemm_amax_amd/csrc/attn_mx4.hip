@@ -48,6 +48,12 @@ constexpr int kWholeKeys = 512;
 template <int D>
 constexpr int kTileCost = D == 64 ? 2 : 1;
 constexpr int kManySteps = 2;
+// The last of a tile's workgroups reads its pieces eight at a time, each time at memory's latency, so a tile
+// of more than kManyPieces is cut into longer ones, up to the square root of a kPieceLength-th of its steps:
+// one request of 131072 keys over one key head 30.9 us, in 512 pieces 78.6; of 20635 over four heads 22.1
+// (26.1 in 81), of 60000 over eight 31.1 (34.8).  With 16 pieces and 64 and lengths of a 2nd and a 4th the
+// same calls took 31 to 41, 22 to 24 and 31 to 34 us.  (Up to 64 requests, whose lengths are in the lanes.)
+constexpr int kManyPieces = 24, kPieceLength = 8;
 #define FP8_GLOBAL __attribute__((address_space(1)))
 
 // x / d by d's reciprocal, x and d not negative: the quotient is off by one or two where it is below 2^22.
@@ -457,7 +463,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_mx4_few_kernel(AttnArgs a
   }
   const int total = sums.total;
   // Workgroup b has the steps from cut(b) to cut(b + 1), `each` of them, the first `more` one more.
-  const int each = max(uniform(quotient(total, groups, 1.0f / static_cast<float>(groups))), 1);
+  int each = max(uniform(quotient(total, groups, 1.0f / static_cast<float>(groups))), 1);
+  if (a.batch <= 64 && groups > kManyPieces) {
+    const Shape s = shape(sums.lane_request);
+    while (__any(lane < a.batch && s.tiles > 0 && (s.steps - 1) / kManyPieces >= each &&
+                 (s.steps - 1) / kPieceLength >= static_cast<int64_t>(each) * each)) ++each;
+  }
   const int more = max(total - each * groups, 0), b = blockIdx.x;
   const float per_each = 1.0f / static_cast<float>(each), per_wide = 1.0f / static_cast<float>(each + 1);
   auto cut = [&](int b) { return b * each + min(b, more); };
