@@ -957,6 +957,7 @@ bool run_launch(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, c
     case FP8_KERNEL_GEMV_STREAM:
     case FP8_KERNEL_GEMV_VALU:
     case FP8_KERNEL_GEMV_MFMA:
+      if (SM == SM_INT8 && L.paired) return launch_gemv(SM, OUT, L, qb, sb, qa, sa, N, M, K, c, s);
       return launch_gemv(SM, OUT, L, qa, sa, qb, sb, M, N, K, c, s);
     case FP8_KERNEL_STAGED:
       if constexpr (SM == SM_INT8) return false;       // the DMA kernels take every K

@@ -89,10 +89,20 @@ inline fp8_gemm_launch_t tile_launch(int sm, int64_t M, int64_t n0, int64_t n1, 
   return l;
 }
 
-// The plan of C[M, N] = A[M, K] B[N, K]^T in scale mode sm (shape already validated).
-inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K) {
+// The plan of C[M, N] = A[M, K] B[N, K]^T in scale mode sm (shape already validated); across: of the operands
+// in each other's place.
+inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool across = false) {
   fp8_gemm_plan_t p{};
   if (M <= 0 || N <= 0) return p;
+  // 8-bit integers with up to 16 output channels (a router, a value head) for more tokens: the decode kernels
+  // with the operands in each other's place, C[m, n] = sum_k qb[n, k] qa[m, k]; the launch says `paired`.
+  // Against the kernels for those tokens, 8 channels, us: K = 4096, 32, 128, 1024 and 16384 tokens 5.0, 5.0, 5.4
+  // and 15.0 (5.8, 13.5, 21.0, 21.8); K = 14112, 32 and 1024 tokens 9.2 and 9.8 (15.0, 58.8).
+  if (sm == SM_INT8 && N <= 16 && M > 16 && gemv_fits(N, K)) {
+    p = plan_gemm(sm, N, M, K, true);
+    p.launch[0].paired = 1;
+    return p;
+  }
   const int64_t SR = scale_row_bytes(sm, K);
   p.launches = 1;
   fp8_gemm_launch_t& l = p.launch[0];
@@ -104,7 +114,9 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K) {
     // block scales the persistent kernel with the activation row in registers is 10-12%
     // faster on both shapes (24 waves per CU led 16 and 32); per tensor and with UE8M0
     // scales the one-wave-per-row kernel stays ahead.  From two tokens on the MFMA kernel,
-    // with two row blocks per wave once the activation fragment is worth sharing (M > 4).
+    // with two row blocks per wave once the activation fragment is worth sharing (M > 4);
+    // not across, where there may be few rows of W (K = 4096, 8 channels: 128 tokens 7.1 us
+    // with two and 5.0 with one, 16384 15.1 and 15.0; 16 channels 15.8 and 17.3).
     if (sm == SM_BLOCK && M == 1 && K <= 8192 && N * K <= kLimit32) {
       const int64_t waves = std::min<int64_t>(N, int64_t{kCus} * kStreamPerCu);
       l = make_launch(FP8_KERNEL_GEMV_STREAM, 1, 1, static_cast<int>(cdiv(K, 1024)), 4, cdiv(waves, 4), 256, 0, N);
@@ -115,8 +127,8 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K) {
       l.max_range = std::max(K, SR);
       l.max_offset = l.max_range;
     } else {
-      const int NB = M <= 4 ? 1 : 2;                // 16-row weight blocks per wave
-      const int waves = M <= 4 ? 2 : 4;             // waves splitting the K slabs
+      const int NB = M <= 4 || across ? 1 : 2;      // 16-row weight blocks per wave
+      const int waves = M <= 4 || across ? 2 : 4;   // waves splitting the K slabs
       l = make_launch(FP8_KERNEL_GEMV_MFMA, M, 16 * NB, NB, waves, cdiv(N, 16 * NB), 64 * waves, 0, N);
       l.max_range = std::max({std::min<int64_t>(16 * NB, N) * K, M * K, M * SR, 2 * SR});
       l.max_offset = std::max<int64_t>(16 * NB, 16) * K + kSlabK;   // incl. the slab past a K tail

@@ -70,7 +70,8 @@ __device__ __forceinline__ v8i load32(const __amdgpu_buffer_rsrc_t& r, uint32_t 
 // (slab s to wave s % WAVES), so at any moment a workgroup reads WAVES * 128 contiguous
 // bytes of each of its rows.  A workgroup's rows may straddle a 128-row weight block; the
 // blockwise scale of each row block is looked up on its own.
-template <int SM, int OUT, int WAVES, int UNROLL, int NB, int MB>
+// ACROSS: C as [N, M], for operands that have changed places.
+template <int SM, int OUT, int WAVES, int UNROLL, int NB, int MB, bool ACROSS = false>
 __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
     const uint8_t* __restrict__ qa, const void* __restrict__ sa_, const uint8_t* __restrict__ qb,
     const void* __restrict__ sb_, int M, int N, int K, uint16_t* __restrict__ c) {
@@ -234,7 +235,11 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
       uint32_t h[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[j][b][r], ff(alpha, b, j, r)));
-      if ((N & 3) == 0 && n + 3 < N) {
+      if constexpr (ACROSS) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < N) c[static_cast<int64_t>(n + r) * M + m] = static_cast<uint16_t>(h[r]);
+      } else if ((N & 3) == 0 && n + 3 < N) {
         *reinterpret_cast<uint2*>(crow + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       } else {
 #pragma unroll
@@ -710,10 +715,10 @@ void launch_valu_t(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa
       qa, sa, qb, sb, M, N, K, static_cast<uint16_t*>(c));
 }
 
-template <int BW, int OUT, int WAVES, int UNROLL, int NB, int MB = 1>
+template <int BW, int OUT, int WAVES, int UNROLL, int NB, int MB = 1, bool ACROSS = false>
 void launch_t(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, const uint8_t* qb, const void* sb,
               int M, int N, int K, void* c, hipStream_t s) {
-  gemv_fp8_kernel<BW, OUT, WAVES, UNROLL, NB, MB><<<static_cast<unsigned>(L.grid), WAVES * 64, 0, s>>>(
+  gemv_fp8_kernel<BW, OUT, WAVES, UNROLL, NB, MB, ACROSS><<<static_cast<unsigned>(L.grid), WAVES * 64, 0, s>>>(
       qa, sa, qb, sb, M, N, K, static_cast<uint16_t*>(c));
 }
 
@@ -742,6 +747,12 @@ bool launch_m(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, con
       launch_valu_t<BW, OUT, 1, 1, 4>(L, qa, sa, qb, sb, M, N, K, c, s);
       return true;
     case FP8_KERNEL_GEMV_MFMA:
+      if constexpr (BW == SM_INT8) {
+        if (L.paired) {            // the operands have changed places
+          launch_t<BW, OUT, 2, 4, 1, 1, true>(L, qa, sa, qb, sb, M, N, K, c, s);
+          return true;
+        }
+      }
       if (L.variant == 1) launch_t<BW, OUT, 2, 4, 1>(L, qa, sa, qb, sb, M, N, K, c, s);
       else launch_t<BW, OUT, 4, 2, 2>(L, qa, sa, qb, sb, M, N, K, c, s);
       return true;

@@ -132,6 +132,13 @@ def test_last_slab_of_every_length(M, N, K):
     check_gemm(ops, "f16" if K % 32 else "bf16")
 
 
+@TYPES
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 8, 13, 16, 17])
+@pytest.mark.parametrize("M,K", [(17, 144), (130, 2064), (1000, 1024), (4099, 16), (20000, 112)])
+def test_few_channels_of_many_tokens(M, N, K, dtype):
+    check_gemm(operands(M, N, K, seed=N), dtype)
+
+
 @pytest.mark.parametrize("M,N", [(0, 5), (5, 0), (0, 0)])
 def test_empty_products(M, N):
     out = fp8.int8_gemm_scaled_rowwise(*(t.to(DEV) for t in operands(M, N, 32)))
