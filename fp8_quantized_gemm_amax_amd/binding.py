@@ -495,23 +495,25 @@ class _GemmLaunch(ctypes.Structure):
 
 
 class _GemmPlan(ctypes.Structure):
-    _fields_ = [("launches", _I32), ("reserved", _I32), ("launch", _GemmLaunch * 2)]
+    _fields_ = [("launches", _I32), ("swapped", _I32), ("launch", _GemmLaunch * 2)]
 
 
 GEMM_MODES = {"tensorwise": 0, "blockwise": 1, "blockwise_ue8m0": 2, "rowwise": 3}
+_PLAN_MODES = {**GEMM_MODES, "int8": 4}
 GEMM_KERNELS = {1: "gemv_stream", 2: "gemv_valu", 3: "gemv_mfma", 4: "skinny", 5: "tile", 6: "staged"}
 
 
 def fp8_debug_gemm_plan(mode, M, N, K):
     """The launches a scaled GEMM of this shape makes (host arithmetic only, no GPU): a list
-    of dicts with the kernel's name and the fields of fp8_gemm_launch_t."""
+    of dicts with the kernel's name, the fields of fp8_gemm_launch_t and whether the operands are
+    swapped; mode as in fp8_gemv_dynamic, or "int8"."""
     plan = _GemmPlan()
-    _check("fp8_debug_gemm_plan", lib().fp8_debug_gemm_plan(GEMM_MODES[mode], M, N, K, ctypes.byref(plan)))
+    _check("fp8_debug_gemm_plan", lib().fp8_debug_gemm_plan(_PLAN_MODES[mode], M, N, K, ctypes.byref(plan)))
     out = []
     for i in range(plan.launches):
         l = plan.launch[i]
         d = {name: getattr(l, name) for name, _ in _GemmLaunch._fields_}
-        d["kernel"] = GEMM_KERNELS[l.kernel]
+        d["kernel"], d["swapped"] = GEMM_KERNELS[l.kernel], plan.swapped
         out.append(d)
     return out
 

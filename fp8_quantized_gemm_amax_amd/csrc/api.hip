@@ -36,6 +36,7 @@ fp8_status_t finish_launch() {
 // Shape rules of the scaled GEMMs, and the plan of their launches (FP8_OK only).
 fp8_status_t gemm_shape(int mode, int64_t M, int64_t N, int64_t K, fp8_gemm_plan_t* plan) {
   const bool blockwise = fp8amax::slab_scaled(mode);
+  if (mode == fp8amax::SM_INT8 && K > kMaxInt8K) return FP8_ERR_TOO_LARGE;
   if (M < 0 || N < 0 || K <= 0) return FP8_ERR_BAD_SHAPE;
   if (blockwise ? (K % 128 != 0) : (K % 16 != 0)) return FP8_ERR_BAD_SHAPE;
   if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return FP8_ERR_TOO_LARGE;
@@ -165,7 +166,6 @@ fp8_status_t int8_quantize_rowwise(const void* x, fp8_dtype_t dt, int64_t rows, 
 
 fp8_status_t int8_gemm_scaled_rowwise(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M,
                                       int64_t N, int64_t K, void* c, fp8_dtype_t out_dt, void* stream) {
-  if (K > kMaxInt8K) return FP8_ERR_TOO_LARGE;
   return gemm_common(fp8amax::SM_INT8, reinterpret_cast<const uint8_t*>(qa), sa, reinterpret_cast<const uint8_t*>(qb), sb, M, N,
                      K, c, out_dt, stream);
 }
@@ -292,7 +292,7 @@ fp8_status_t fp8_debug_cast_f32(const float* v, uint8_t* q, int64_t n, void* str
 }
 
 fp8_status_t fp8_debug_gemm_plan(int32_t mode, int64_t M, int64_t N, int64_t K, fp8_gemm_plan_t* plan) {
-  if (mode < FP8_SCALE_TENSOR || mode > FP8_SCALE_ROW) return FP8_ERR_BAD_SHAPE;
+  if (mode < FP8_SCALE_TENSOR || mode > FP8_SCALE_INT8) return FP8_ERR_BAD_SHAPE;
   if (!plan) return FP8_ERR_NULL_POINTER;
   return gemm_shape(mode, M, N, K, plan);
 }

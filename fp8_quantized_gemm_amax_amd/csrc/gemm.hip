@@ -949,7 +949,7 @@ void launch_cfg(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, c
 // Carries out one launch of a plan (plan_gemm in gemm_plan.hpp chooses the kernel, tile,
 // grid and columns, and measures why).  Returns false for a launch no kernel here matches.
 template <int SM, int OUT>
-bool run_launch(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, const uint8_t* qb,
+bool run_launch(const fp8_gemm_launch_t& L, bool swapped, const uint8_t* qa, const void* sa, const uint8_t* qb,
                 const void* sb, int M, int N, int K, void* c, hipStream_t s) {
   constexpr bool BW = slab_scaled(SM);
   constexpr bool PAIR = SM != SM_BLOCK;            // the 256x256 kernel's DMA issue, per mode
@@ -957,8 +957,8 @@ bool run_launch(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, c
     case FP8_KERNEL_GEMV_STREAM:
     case FP8_KERNEL_GEMV_VALU:
     case FP8_KERNEL_GEMV_MFMA:
-      if (SM == SM_INT8 && L.paired) return launch_gemv(SM, OUT, L, qb, sb, qa, sa, N, M, K, c, s);
-      return launch_gemv(SM, OUT, L, qa, sa, qb, sb, M, N, K, c, s);
+      if (swapped) return launch_gemv(SM, OUT, L, true, qb, sb, qa, sa, N, M, K, c, s);
+      return launch_gemv(SM, OUT, L, false, qa, sa, qb, sb, M, N, K, c, s);
     case FP8_KERNEL_STAGED:
       if constexpr (SM == SM_INT8) return false;       // the DMA kernels take every K
       else if (L.tile_m == 16) launch_cfg<16, 256, 16, 64, SM, OUT>(L, qa, sa, qb, sb, M, N, K, c, s);
@@ -995,7 +995,7 @@ template <int SM, int OUT>
 bool launch_gemm_t(const fp8_gemm_plan_t& p, const uint8_t* qa, const void* sa, const uint8_t* qb,
                    const void* sb, int M, int N, int K, void* c, hipStream_t s) {
   for (int i = 0; i < p.launches; ++i)
-    if (!run_launch<SM, OUT>(p.launch[i], qa, sa, qb, sb, M, N, K, c, s)) return false;
+    if (!run_launch<SM, OUT>(p.launch[i], p.swapped != 0, qa, sa, qb, sb, M, N, K, c, s)) return false;
   return true;
 }
 

@@ -15,7 +15,8 @@ namespace fp8amax {
 namespace plan {
 
 static_assert(int{FP8_SCALE_TENSOR} == int{SM_TENSOR} && int{FP8_SCALE_BLOCK} == int{SM_BLOCK} &&
-                  int{FP8_SCALE_BLOCK_UE8M0} == int{SM_E8M0} && int{FP8_SCALE_ROW} == int{SM_ROW},
+                  int{FP8_SCALE_BLOCK_UE8M0} == int{SM_E8M0} && int{FP8_SCALE_ROW} == int{SM_ROW} &&
+                  int{FP8_SCALE_INT8} == int{SM_INT8},
               "the C ABI's scale modes are the kernels' template values");
 
 constexpr int kCus = 256;              // compute units of one MI355X
@@ -89,20 +90,17 @@ inline fp8_gemm_launch_t tile_launch(int sm, int64_t M, int64_t n0, int64_t n1, 
   return l;
 }
 
-// The plan of C[M, N] = A[M, K] B[N, K]^T in scale mode sm (shape already validated); across: of the operands
+// The plan of C[M, N] = A[M, K] B[N, K]^T in scale mode sm (shape already validated); swapped: of the operands
 // in each other's place.
-inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool across = false) {
+inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool swapped = false) {
   fp8_gemm_plan_t p{};
+  p.swapped = swapped ? 1 : 0;
   if (M <= 0 || N <= 0) return p;
   // 8-bit integers with up to 16 output channels (a router, a value head) for more tokens: the decode kernels
-  // with the operands in each other's place, C[m, n] = sum_k qb[n, k] qa[m, k]; the launch says `paired`.
+  // with the operands in each other's place, C[m, n] = sum_k qb[n, k] qa[m, k].
   // Against the kernels for those tokens, 8 channels, us: K = 4096, 32, 128, 1024 and 16384 tokens 5.0, 5.0, 5.4
   // and 15.0 (5.8, 13.5, 21.0, 21.8); K = 14112, 32 and 1024 tokens 9.2 and 9.8 (15.0, 58.8).
-  if (sm == SM_INT8 && N <= 16 && M > 16 && gemv_fits(N, K)) {
-    p = plan_gemm(sm, N, M, K, true);
-    p.launch[0].paired = 1;
-    return p;
-  }
+  if (sm == SM_INT8 && N <= 16 && M > 16 && gemv_fits(N, K)) return plan_gemm(sm, N, M, K, true);
   const int64_t SR = scale_row_bytes(sm, K);
   p.launches = 1;
   fp8_gemm_launch_t& l = p.launch[0];
@@ -115,7 +113,7 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool a
     // faster on both shapes (24 waves per CU led 16 and 32); per tensor and with UE8M0
     // scales the one-wave-per-row kernel stays ahead.  From two tokens on the MFMA kernel,
     // with two row blocks per wave once the activation fragment is worth sharing (M > 4);
-    // not across, where there may be few rows of W (K = 4096, 8 channels: 128 tokens 7.1 us
+    // not swapped, where there may be few rows of W (K = 4096, 8 channels: 128 tokens 7.1 us
     // with two and 5.0 with one, 16384 15.1 and 15.0; 16 channels 15.8 and 17.3).
     if (sm == SM_BLOCK && M == 1 && K <= 8192 && N * K <= kLimit32) {
       const int64_t waves = std::min<int64_t>(N, int64_t{kCus} * kStreamPerCu);
@@ -127,8 +125,8 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool a
       l.max_range = std::max(K, SR);
       l.max_offset = l.max_range;
     } else {
-      const int NB = M <= 4 || across ? 1 : 2;      // 16-row weight blocks per wave
-      const int waves = M <= 4 || across ? 2 : 4;   // waves splitting the K slabs
+      const int NB = M <= 4 || swapped ? 1 : 2;     // 16-row weight blocks per wave
+      const int waves = M <= 4 || swapped ? 2 : 4;  // waves splitting the K slabs
       l = make_launch(FP8_KERNEL_GEMV_MFMA, M, 16 * NB, NB, waves, cdiv(N, 16 * NB), 64 * waves, 0, N);
       l.max_range = std::max({std::min<int64_t>(16 * NB, N) * K, M * K, M * SR, 2 * SR});
       l.max_offset = std::max<int64_t>(16 * NB, 16) * K + kSlabK;   // incl. the slab past a K tail

@@ -70,8 +70,8 @@ __device__ __forceinline__ v8i load32(const __amdgpu_buffer_rsrc_t& r, uint32_t 
 // (slab s to wave s % WAVES), so at any moment a workgroup reads WAVES * 128 contiguous
 // bytes of each of its rows.  A workgroup's rows may straddle a 128-row weight block; the
 // blockwise scale of each row block is looked up on its own.
-// ACROSS: C as [N, M], for operands that have changed places.
-template <int SM, int OUT, int WAVES, int UNROLL, int NB, int MB, bool ACROSS = false>
+// SWAPPED: C as [N, M], for operands in each other's place.
+template <int SM, int OUT, int WAVES, int UNROLL, int NB, int MB, bool SWAPPED = false>
 __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
     const uint8_t* __restrict__ qa, const void* __restrict__ sa_, const uint8_t* __restrict__ qb,
     const void* __restrict__ sb_, int M, int N, int K, uint16_t* __restrict__ c) {
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_fp8_kernel(
       uint32_t h[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) h[r] = f32_to_out_bits<OUT>(Product<SM>::scaled(acc[j][b][r], ff(alpha, b, j, r)));
-      if constexpr (ACROSS) {
+      if constexpr (SWAPPED) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (n + r < N) c[static_cast<int64_t>(n + r) * M + m] = static_cast<uint16_t>(h[r]);
@@ -715,17 +715,17 @@ void launch_valu_t(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa
       qa, sa, qb, sb, M, N, K, static_cast<uint16_t*>(c));
 }
 
-template <int BW, int OUT, int WAVES, int UNROLL, int NB, int MB = 1, bool ACROSS = false>
+template <int BW, int OUT, int WAVES, int UNROLL, int NB, int MB = 1, bool SWAPPED = false>
 void launch_t(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, const uint8_t* qb, const void* sb,
               int M, int N, int K, void* c, hipStream_t s) {
-  gemv_fp8_kernel<BW, OUT, WAVES, UNROLL, NB, MB, ACROSS><<<static_cast<unsigned>(L.grid), WAVES * 64, 0, s>>>(
+  gemv_fp8_kernel<BW, OUT, WAVES, UNROLL, NB, MB, SWAPPED><<<static_cast<unsigned>(L.grid), WAVES * 64, 0, s>>>(
       qa, sa, qb, sb, M, N, K, static_cast<uint16_t*>(c));
 }
 
 // Carries out a decode launch of a plan (plan_gemm in gemm_plan.hpp picks the kernel and
 // says why).  The persistent one-token kernel exists for float32 block scales only.
 template <int BW, int OUT>
-bool launch_m(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, const uint8_t* qb, const void* sb,
+bool launch_m(const fp8_gemm_launch_t& L, bool swapped, const uint8_t* qa, const void* sa, const uint8_t* qb, const void* sb,
               int M, int N, int K, void* c, hipStream_t s) {
   switch (L.kernel) {
     case FP8_KERNEL_GEMV_STREAM:
@@ -748,7 +748,7 @@ bool launch_m(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, con
       return true;
     case FP8_KERNEL_GEMV_MFMA:
       if constexpr (BW == SM_INT8) {
-        if (L.paired) {            // the operands have changed places
+        if (swapped) {
           launch_t<BW, OUT, 2, 4, 1, 1, true>(L, qa, sa, qb, sb, M, N, K, c, s);
           return true;
         }
@@ -762,10 +762,10 @@ bool launch_m(const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, con
 }
 
 template <int SM>
-bool launch_gemv_m(int out_dt, const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa, const uint8_t* qb,
+bool launch_gemv_m(int out_dt, const fp8_gemm_launch_t& L, bool swapped, const uint8_t* qa, const void* sa, const uint8_t* qb,
                    const void* sb, int M, int N, int K, void* c, hipStream_t s) {
-  if (out_dt == DT_BF16) return launch_m<SM, DT_BF16>(L, qa, sa, qb, sb, M, N, K, c, s);
-  return launch_m<SM, DT_F16>(L, qa, sa, qb, sb, M, N, K, c, s);
+  if (out_dt == DT_BF16) return launch_m<SM, DT_BF16>(L, swapped, qa, sa, qb, sb, M, N, K, c, s);
+  return launch_m<SM, DT_F16>(L, swapped, qa, sa, qb, sb, M, N, K, c, s);
 }
 
 
@@ -814,13 +814,13 @@ void launch_dynamic_m(int in_dt, int out_dt, const void* x, const uint8_t* qb, c
 
 }  // namespace
 
-bool launch_gemv(int mode, int out_dt, const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa,
+bool launch_gemv(int mode, int out_dt, const fp8_gemm_launch_t& L, bool swapped, const uint8_t* qa, const void* sa,
                  const uint8_t* qb, const void* sb, int M, int N, int K, void* c, hipStream_t s) {
-  if (mode == SM_INT8) return launch_gemv_m<SM_INT8>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
-  if (mode == SM_ROW) return launch_gemv_m<SM_ROW>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
-  if (mode == SM_E8M0) return launch_gemv_m<SM_E8M0>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
-  if (mode == SM_BLOCK) return launch_gemv_m<SM_BLOCK>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
-  return launch_gemv_m<SM_TENSOR>(out_dt, L, qa, sa, qb, sb, M, N, K, c, s);
+  if (mode == SM_INT8) return launch_gemv_m<SM_INT8>(out_dt, L, swapped, qa, sa, qb, sb, M, N, K, c, s);
+  if (mode == SM_ROW) return launch_gemv_m<SM_ROW>(out_dt, L, swapped, qa, sa, qb, sb, M, N, K, c, s);
+  if (mode == SM_E8M0) return launch_gemv_m<SM_E8M0>(out_dt, L, swapped, qa, sa, qb, sb, M, N, K, c, s);
+  if (mode == SM_BLOCK) return launch_gemv_m<SM_BLOCK>(out_dt, L, swapped, qa, sa, qb, sb, M, N, K, c, s);
+  return launch_gemv_m<SM_TENSOR>(out_dt, L, swapped, qa, sa, qb, sb, M, N, K, c, s);
 }
 
 void launch_gemv_dynamic(int mode, int in_dt, int out_dt, const void* x, const uint8_t* qb, const void* sb,

@@ -78,8 +78,9 @@ bool launch_grouped(int mode, int out_dt, const uint8_t* qa, const void* sa, con
                     const int* offsets, int E, int T, int N, int K, void* c, hipStream_t s);
 
 // One decode launch of a plan (kernels FP8_KERNEL_GEMV_*).  sa and sb point at float32
-// scales, or at e8m0fnu bytes for SM_E8M0.  False for a launch it has no kernel for.
-bool launch_gemv(int mode, int out_dt, const fp8_gemm_launch_t& L, const uint8_t* qa, const void* sa,
+// scales, or at e8m0fnu bytes for SM_E8M0.  swapped: qa and qb are in each other's place, and c
+// is [N, M] (SM_INT8).  False for a launch it has no kernel for.
+bool launch_gemv(int mode, int out_dt, const fp8_gemm_launch_t& L, bool swapped, const uint8_t* qa, const void* sa,
                  const uint8_t* qb, const void* sb, int M, int N, int K, void* c, hipStream_t s);
 
 // The fused one-token step (plan::dynamic_fits(N, K)): x [K] quantized with the scheme of

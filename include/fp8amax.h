@@ -343,7 +343,8 @@ typedef enum FP8_ENUM_BASE {
   FP8_SCALE_TENSOR = 0,      /* fp8_gemm_scaled_tensorwise */
   FP8_SCALE_BLOCK = 1,       /* fp8_gemm_scaled_blockwise */
   FP8_SCALE_BLOCK_UE8M0 = 2, /* fp8_gemm_scaled_blockwise_ue8m0 */
-  FP8_SCALE_ROW = 3          /* fp8_gemm_scaled_rowwise */
+  FP8_SCALE_ROW = 3,         /* fp8_gemm_scaled_rowwise */
+  FP8_SCALE_INT8 = 4         /* int8_gemm_scaled_rowwise (fp8amax_int8.h); fp8_debug_gemm_plan only */
 } fp8_scale_mode_t;
 
 typedef enum FP8_ENUM_BASE {
@@ -375,7 +376,9 @@ typedef struct {
 
 typedef struct {
   int32_t launches;    /* 0, 1 or 2, in the order they are enqueued */
-  int32_t reserved;
+  int32_t swapped;     /* 1 (FP8_SCALE_INT8 only) where the kernel takes the operands in each other's
+                          place: the launch is then that of M channels for N tokens, and its columns
+                          are rows of C */
   fp8_gemm_launch_t launch[2];
 } fp8_gemm_plan_t;
 

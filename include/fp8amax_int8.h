@@ -39,8 +39,8 @@ fp8_status_t int8_quantize_rowwise(const void* x, fp8_dtype_t dt, int64_t rows, 
  *   sa : float32 [M], sb : float32 [N] (device), 4-byte aligned.
  *   c  : bf16/fp16 output [M, N] (device), 16-byte aligned.
  * Requires K % 16 == 0, 0 < K <= 131071 (larger sums could pass 2^31: FP8_ERR_TOO_LARGE); M == 0 or
- * N == 0 returns FP8_OK.  Other errors as fp8_gemm_scaled_rowwise, whose launches (see
- * fp8_debug_gemm_plan) it has for the same shape where K % 128 == 0 and N > 16 or M <= 16.
+ * N == 0 returns FP8_OK.  Other errors as fp8_gemm_scaled_rowwise.  fp8_debug_gemm_plan with
+ * FP8_SCALE_INT8 tells a shape's launches: fp8_gemm_scaled_rowwise's where K % 128 == 0 and N > 16 or M <= 16.
  */
 fp8_status_t int8_gemm_scaled_rowwise(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M,
                                       int64_t N, int64_t K, void* c, fp8_dtype_t out_dt, void* stream);
