@@ -90,6 +90,14 @@ inline fp8_gemm_launch_t tile_launch(int sm, int64_t M, int64_t n0, int64_t n1, 
   return l;
 }
 
+// Whether the launches of a plan can be made: each holds fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;
+inline bool launches_hold(const fp8_gemm_plan_t& p) {
+  for (int i = 0; i < p.launches; ++i)
+    if (p.launch[i].grid > kMaxThreads / p.launch[i].threads) return false;
+  return true;
+}
+
 // The plan of C[M, N] = A[M, K] B[N, K]^T in scale mode sm (shape already validated); swapped: of the operands
 // in each other's place.
 inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool swapped = false) {
@@ -100,7 +108,13 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool s
   // with the operands in each other's place, C[m, n] = sum_k qb[n, k] qa[m, k].
   // Against the kernels for those tokens, 8 channels, us: K = 4096, 32, 128, 1024 and 16384 tokens 5.0, 5.0, 5.4
   // and 15.0 (5.8, 13.5, 21.0, 21.8); K = 14112, 32 and 1024 tokens 9.2 and 9.8 (15.0, 58.8).
-  if (sm == SM_INT8 && N <= 16 && M > 16 && gemv_fits(N, K)) return plan_gemm(sm, N, M, K, true);
+  // Tokens are the launch's workgroups then: not where that is more than it holds (2^26 tokens for one
+  // channel, 2^29 for more), which the tiles of 256 tokens take.
+  if (sm == SM_INT8 && N <= 16 && M > 16 && gemv_fits(N, K)) {
+    p = plan_gemm(sm, N, M, K, true);
+    if (launches_hold(p)) return p;
+    p = {};
+  }
   const int64_t SR = scale_row_bytes(sm, K);
   p.launches = 1;
   fp8_gemm_launch_t& l = p.launch[0];

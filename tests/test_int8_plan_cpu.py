@@ -20,12 +20,19 @@ def plan(M, N, K):
     return fp8.fp8_debug_gemm_plan("int8", M, N, K)
 
 
+def swaps(M, N):
+    """Up to 16 channels for more tokens, as long as a launch holds the threads: fewer than 2^32."""
+    return N <= 16 < M and (256 * cdiv(M, 4) if N == 1 else 128 * cdiv(M, 16)) < 2 ** 32
+
+
 def check(M, N, K, launches):
-    swapped = N <= 16 < M
+    swapped = swaps(M, N)
     assert launches[0]["n_begin"] == 0 and launches[-1]["n_end"] == (M if swapped else N)
     for a, b in zip(launches, launches[1:]):
         assert a["n_end"] == b["n_begin"] and a["n_begin"] < a["n_end"]
     m, n = (N, M) if swapped else (M, N)            # as the kernels see them
+    if N <= 16 < M < 2 ** 31 - 256:
+        assert all(L["grid"] * L["threads"] < 2 ** 32 for L in launches)
     for L in launches:
         kind, cols = L["kernel"], L["n_end"] - L["n_begin"]
         assert L["swapped"] == swapped
@@ -70,10 +77,17 @@ def test_every_accepted_shape_has_a_plan_within_32_bit_addressing():
 
 def test_whole_slabs_have_the_launches_of_the_product_with_a_scale_a_row():
     for M, N, K in itertools.product(MS, NS8, [k for k in KS if k % 128 == 0]):
-        if not too_large(M, N, K) and (N > 16 or M <= 16):
+        if not too_large(M, N, K) and not (N <= 16 < M):
             launches = plan(M, N, K)
             check_plan("rowwise", M, N, K, launches)
             assert launches == fp8.fp8_debug_gemm_plan("rowwise", M, N, K)
+
+
+@pytest.mark.parametrize("N,most", [(1, 2 ** 26 - 4), (2, 2 ** 29 - 16), (16, 2 ** 29 - 16)])
+def test_operands_change_places_only_where_a_launch_holds_the_tokens(N, most):
+    (a,), (b,) = plan(most, N, 16), plan(most + 1, N, 16)
+    assert a["swapped"] and a["kernel"].startswith("gemv") and 2 ** 32 - 256 <= a["grid"] * a["threads"] < 2 ** 32
+    assert not b["swapped"] and b["kernel"] == "tile" and b["grid"] * b["threads"] < 2 ** 32
 
 
 def test_query_errors():
