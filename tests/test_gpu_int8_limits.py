@@ -1,13 +1,28 @@
-"""The 8-bit integer product at its limits where the operands change places: as many tokens as a
-launch holds, and more."""
+"""The 8-bit integer product at its limits where the operands change places: K at its limit for up to 16
+output channels, and as many tokens as a launch holds, and more."""
 
 import pytest
 import torch
 
 import fp8_quantized_gemm_amax_amd as fp8
 from parity_util import DEV
+from test_gpu_int8 import check_gemm, operands
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M", [17, 40, 200])
+@pytest.mark.parametrize("N", [1, 2, 16])
+def test_largest_sums_of_few_channels(N, M):
+    """Codes of -128 and 127 only at K = 131056: sums up to 2^31 - 2^18, exact."""
+    K = 131056
+    assert fp8.fp8_debug_gemm_plan("int8", M, N, K)[0]["swapped"]
+    qa, sa, qb, sb = operands(M, N, K, seed=M)
+    qa[:], qb[:] = -128, -128
+    qb[1::2] = 127
+    qa[M // 2:, ::3] = 127
+    assert int(qa[0].long() @ qb[0].long()) == 128 * 128 * K
+    check_gemm((qa, sa, qb, sb), "bf16")
 
 
 @pytest.mark.parametrize("M", [2 ** 26 - 4, 2 ** 26 + 5])
