@@ -52,6 +52,7 @@ fp8_status_t gemm_common(int mode, const uint8_t* qa, const void* sa, const uint
   fp8_gemm_plan_t plan;
   const fp8_status_t st = gemm_shape(mode, M, N, K, &plan);
   if (st != FP8_OK) return st;
+  if (!fp8amax::plan::launches_hold(plan)) return FP8_ERR_TOO_LARGE;
   if (!valid_dt(out_dt)) return FP8_ERR_BAD_DTYPE;
   if (M == 0 || N == 0) return FP8_OK;
   if (!qa || !sa || !qb || !sb || !c) return FP8_ERR_NULL_POINTER;
@@ -304,6 +305,7 @@ fp8_status_t fp8_gemv_dynamic(int32_t mode, const void* x, fp8_dtype_t in_dt, co
   fp8_gemm_plan_t plan;
   const fp8_status_t st = gemm_shape(mode, 1, N, K, &plan);
   if (st != FP8_OK) return st;
+  if (!fp8amax::plan::dynamic_fits(N, K) && !fp8amax::plan::launches_hold(plan)) return FP8_ERR_TOO_LARGE;
   if (!valid_dt(in_dt) || !valid_dt(out_dt)) return FP8_ERR_BAD_DTYPE;
   if (!x || !qa || !sa || (N > 0 && (!qb || !sb || !c))) return FP8_ERR_NULL_POINTER;
   if (!aligned16(x) || !aligned16(qa) || !aligned4(sa) ||

@@ -128,7 +128,9 @@ fp8_status_t fp8_quantize_per_token_group(const void* x, fp8_dtype_t dt, int64_t
  * Requires K % 16 == 0 (the task page pads hidden sizes to a multiple of 16) and K > 0.
  * M == 0 or N == 0 returns FP8_OK with nothing launched.
  * Every GEMM entry point returns FP8_ERR_TOO_LARGE, before any HIP call, when M, N or K
- * exceeds 2^31 - 1 or one of M K, N K, M N exceeds 2^40.
+ * exceeds 2^31 - 1 or one of M K, N K, M N exceeds 2^40, and where a launch would need 2^32
+ * threads or more (one token: about 2^26 channels, 2 to 16: 2^29; fp8_debug_gemm_plan tells the
+ * plan of such a shape all the same).
  */
 fp8_status_t fp8_gemm_scaled_tensorwise(const uint8_t* qa, const float* sa,
                                         const uint8_t* qb, const float* sb,
