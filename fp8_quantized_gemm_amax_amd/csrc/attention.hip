@@ -134,14 +134,14 @@ int64_t attn_paged_groups(int format, int64_t tokens, int64_t batch, int64_t hq,
   return format == FP8_KV_MXFP4 ? mx4_groups(tokens, batch, group, hk, capacity, split) : few_groups(tokens, batch, group, hk, capacity, split);
 }
 
-int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
+int64_t attn_paged_workspace(int format, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
                              int64_t max_new) {
   using namespace attn;
   if (!may_split(tokens, hq / hk, batch, hk, capacity)) return 0;
-  auto bytes = [&](bool few) {
-    return workspace_bytes(few ? 2 * std::max<int64_t>(kFewGroups, hk) : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim);
-  };
-  // Enough for every format of the cache.
+  // Few rows over mxfp4: a key head has a workgroup at least, each with two partial results.
+  const int64_t groups = format == FP8_KV_MXFP4 ? std::max<int64_t>(kFewGroups, hk) : kFewGroups;
+  auto bytes = [&](bool few) { return workspace_bytes(few ? 2 * groups : 2 * extra_units(hk) * hk, few ? 32 : 128, head_dim); };
+  // Whichever kernel a format's rule chooses; FP8_KV_MXFP4 has the most, which is enough for every format.
   int64_t most = 0;
   for (int format : {FP8_KV_SAME, FP8_KV_E4M3, FP8_KV_MXFP4}) most = std::max(most, bytes(few_rows(format, max_new, hq / hk, tokens, batch)));
   return most;

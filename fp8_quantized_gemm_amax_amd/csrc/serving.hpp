@@ -72,7 +72,7 @@ void launch_attn_prompt(int dt, int head_dim, const AttnArgs& a, hipStream_t s);
 void launch_attn_paged(int dt, int head_dim, int format, int max_new, const AttnArgs& a, hipStream_t s);
 int64_t attn_prompt_groups(int64_t tokens, int64_t batch, int64_t hq, int64_t hk);   // workgroups of the launch
 int64_t attn_paged_groups(int format, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int64_t capacity, int64_t max_new);
-int64_t attn_paged_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
+int64_t attn_paged_workspace(int format, int64_t tokens, int64_t batch, int64_t hq, int64_t hk, int head_dim, int64_t capacity,
                              int64_t max_new);
 
 }  // namespace fp8amax

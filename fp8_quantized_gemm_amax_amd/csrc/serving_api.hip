@@ -202,7 +202,7 @@ int64_t fp8_attn_paged_workspace(int64_t tokens, int64_t batch, int64_t q_heads,
   if (check_heads(tokens, batch, q_heads, kv_heads, head_dim, 1.0f, 0) != FP8_OK || !valid_page(page_size) ||
       width < 1 || width > kMaxKeys / page_size || max_new < 0)
     return 0;
-  return fp8amax::attn_paged_workspace(tokens, batch, q_heads, kv_heads, head_dim, width * page_size, max_new);
+  return fp8amax::attn_paged_workspace(FP8_KV_MXFP4, tokens, batch, q_heads, kv_heads, head_dim, width * page_size, max_new);
 }
 
 fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const int32_t* cu_tokens, int64_t batch,
@@ -223,7 +223,7 @@ fp8_status_t fp8_attn_paged(const void* q, fp8_dtype_t dt, int64_t tokens, const
   const bool scaled = format != FP8_KV_SAME;
   if (fp8amax::attn_paged_groups(format, tokens, batch, q_heads, kv_heads, width * page_size, max_new) > kMaxGroups)
     return FP8_ERR_TOO_LARGE;
-  const int64_t need = fp8amax::attn_paged_workspace(tokens, batch, q_heads, kv_heads, head_dim, width * page_size, max_new);
+  const int64_t need = fp8amax::attn_paged_workspace(format, tokens, batch, q_heads, kv_heads, head_dim, width * page_size, max_new);
   if (workspace_bytes < need) return FP8_ERR_BAD_SHAPE;
   if (!q || !cu_tokens || !k_cache || !v_cache || !block_table || !seq_lens || !out || (need > 0 && !workspace) ||
       (scaled && (!k_scales || !v_scales)))
