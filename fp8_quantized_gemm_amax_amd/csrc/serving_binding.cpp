@@ -147,6 +147,12 @@ Cache cache_of(PyObject* k, PyObject* v, PyObject* ks, PyObject* vs, at::ScalarT
   c.format = FP8_KV_E4M3;
   return c;
 }
+// For the calls that write a cache: its tensors share no memory with each other.
+void apart(const Cache& c) {
+  const at::Tensor* const t[4] = {&c.k, &c.v, &c.ks, &c.vs};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j) TORCH_CHECK_VALUE(!t[i]->defined() || !t[j]->defined() || !overlaps(*t[i], *t[j]), "caches or their scales overlap");
+}
 void on_cache(const at::Tensor& like, const Cache& c) {
   on(like, {{&c.k, "k_cache"}, {&c.v, "v_cache"}});
   if (c.format != FP8_KV_SAME) on(like, {{&c.ks, "k_scales"}, {&c.vs, "v_scales"}});
@@ -255,7 +261,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   TORCH_CHECK_VALUE(k.size(1) == heads, "k has ", k.size(1), " heads, the cache ", heads);
   const at::Tensor slots = vec(tensor(a[2], "slots"), "slots", at::kLong, k.size(0));
   for (const at::Tensor* t : {&c.k, &c.v, &c.ks, &c.vs})
-    TORCH_CHECK_VALUE(!t->defined() || (!overlaps(*t, k) && !overlaps(*t, v)), "a cache overlaps k or v");
+    TORCH_CHECK_VALUE(!t->defined() || (!overlaps(*t, k) && !overlaps(*t, v) && !overlaps(*t, slots)), "a cache overlaps k, v or slots");
+  apart(c);
   on(k, {{&v, "v"}, {&slots, "slots"}});
   on_cache(k, c);
   const c10::DeviceGuard guard(k.device());   // the launch goes to the tensors' GPU
@@ -300,6 +307,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   for (const at::Tensor* t : {&c.k, &c.v, &c.ks, &c.vs})
     for (const at::Tensor* in : std::initializer_list<const at::Tensor*>{&q, &k, &v, &positions, &table, &slots})
       TORCH_CHECK_VALUE(!t->defined() || !in->defined() || !overlaps(*t, *in), "a cache overlaps an input");
+  apart(c);
   if (a[11] == Py_None) {
     on(k, {{&v, "v"}, {&positions, "positions"}, {&table, "cos_sin"}, {&slots, "slots"}});
     on_cache(k, c);
