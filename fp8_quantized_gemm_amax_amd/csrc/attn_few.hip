@@ -182,10 +182,14 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, bool split
               s[u][i] = key <= hi && key >= lo ? s[u][i] : -INFINITY;
             }
         }
-        uint32_t seen = 0;      // ODD: the keys that this lane's row sees
+        uint32_t seen = 0;      // ODD: the keys that this lane's row sees, by their places: also one whose score is -infinity
         if constexpr (ODD) {
+          const int hi = pos - t - 4 * half, lo = low - t - 4 * half;
 #pragma unroll
-          for (int i = 0; i < 16 * kSub; ++i) seen |= (s[i / 16][i % 16] == -INFINITY ? 0u : 1u) << i;
+          for (int i = 0; i < 16 * kSub; ++i) {
+            const int key = 8 * (i / 4) + i % 4;
+            seen |= (key <= hi && key >= lo ? 1u : 0u) << i;
+          }
         }
         float top = s[0][0];
 #pragma unroll

@@ -334,9 +334,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_mx4_few_kernel(AttnArgs a
           score(codes, s);
           fetch(a.v, a.vs, voff, vscale, at, codes);
           mask(t, s);
-          uint32_t seen = 0;
+          const int hi = pos - t - 4 * quarter, lo = a.window > 0 ? hi - a.window + 1 : -t - 4 * quarter;
+          uint32_t seen = 0;       // by the keys' places: also one whose score is -infinity
 #pragma unroll
-          for (int i = 0; i < 16; ++i) seen |= (s[i / 4][i % 4] == -INFINITY ? 0u : 1u) << i;
+          for (int i = 0; i < 16; ++i) {
+            const int key = 16 * (i / 4) + i % 4;
+            seen |= (key <= hi && key >= lo ? 1u : 0u) << i;
+          }
           v8s p[kTileKeys / 32];
           weigh(part, s, p);
           clear(lane >> 2, t, at.holes, codes);

@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           for (int x = 0; x < 16; ++x) o[i][x] *= keep;
       }
     };
-    auto weigh = [&](auto odd_c, const v16f (&s)[2], int w, float mb, const float* scale, float (&x)[8]) {
+    auto weigh = [&](auto odd_c, const v16f (&s)[2], int w, float mb, const float* scale, float (&x)[8], uint32_t seen = 0) {
       constexpr bool ODD = decltype(odd_c)::value;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float z = x[4 * g + i] * y[i];
-            x[4 * g + i] = ODD && s[w / 2][8 * (w & 1) + 4 * g + i] == -INFINITY ? 0.0f : z;
+            x[4 * g + i] = ODD && !(seen >> (4 * g + i) & 1) ? 0.0f : z;
           }
         }
       }
@@ -421,11 +421,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(AttnArgs a, b
           const float mb = m == -INFINITY ? 0.0f : m;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            float z[8];
-            weigh(std::true_type{}, s, w, mb, vscale[0], z);
-            uint32_t seen = 0;
+            const int hi = pos - t - 16 * w - 4 * half, lo = low - t - 16 * w - 4 * half;
+            uint32_t seen = 0;     // by the keys' places: also one whose score is -infinity
 #pragma unroll
-            for (int i = 0; i < 8; ++i) seen |= (s[w / 2][8 * (w & 1) + i] == -INFINITY ? 0u : 1u) << i;
+            for (int i = 0; i < 8; ++i) {
+              const int key = 8 * (i / 4) + i % 4;
+              seen |= (key <= hi && key >= lo ? 1u : 0u) << i;
+            }
+            float z[8];
+            weigh(std::true_type{}, s, w, mb, vscale[0], z, seen);
             part[0] = mfma_odd<DT, kSplit>(read_v1(0, w, x), z, seen, part[0]);
           }
         }
