@@ -35,6 +35,9 @@ namespace {
 // No number of rows suits every length: at the limits the kernel for few is up to 23% faster over short
 // caches and up to 37% slower over long ones in 16 bits (above 12 rows), 25% faster to 8% slower over e4m3,
 // 25% faster to 9% slower over mxfp4.
+// Nor is the limit of 512 rows right for every length: over mxfp4 such a request reads its keys 32 times.  One of
+// 512 rows among 63 (15) single tokens over 2000 to 4000 keys each, many : few: over 1000 keys 125 : 55 (57 : 27),
+// over 4000 133 : 64 (63 : 40), over 16000 176 : 119 (111 : 100), over 100000 346 : 549 (260 : 511).
 bool few_rows(int format, int64_t max_new, int64_t group, int64_t tokens, int64_t batch) {
   return std::min(max_new, tokens) * group <= 512 && tokens * group <= (format == FP8_KV_SAME ? 32 : format == FP8_KV_E4M3 ? 64 : 48) * batch;
 }

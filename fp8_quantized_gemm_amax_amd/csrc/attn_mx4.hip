@@ -12,14 +12,16 @@
 // A workgroup of four waves takes one unit of keys; each wave walks over its own tiles of 64 without a
 // barrier, and the four results are joined in LDS at the end.  The next tile's codes are on their way
 // while this one is multiplied.
-// Bound by the reads of the cache, 144 bytes a key and head of 128 channels, once their number is large.
-// Measured on one card, 32 heads on 8 of 128 channels, bf16, one new token a request: 128 requests of up to
-// 8192 keys 92 us (431 MB, 4.7 TB/s), four of up to 131072 53 us (232 MB, 4.4 TB/s); the walks inside read
-// at 6.8 TB/s, and around them a call has 12 us that do not depend on the keys: the launch, the cut (one
-// microsecond), the first reads' latency, the join of the waves (two) and of the pieces (two to five).  One
-// request of 701 keys 8.4 us.  Of other arrangements, one wider (32 rows for a tile of 64 keys) spilled and
-// took 153 us where two passes over 16 rows take 65; a second tile on its way, three waves a SIMD, eight
-// waves a workgroup and 768 to 2048 workgroups were all slower than this with two workgroups a CU.
+// Bound by the reads of the cache, 136 bytes a key and head of 128 channels, once their number is large.
+// Measured on one card, 32 heads on 8 of 128 channels, bf16, one new token a request, everything from
+// memory: 16, 32, 64 and 128 requests of 4096 to 8192 keys 28.1, 49.6, 89.2 and 170 us (104, 210, 429 and 870
+// MB), four of 32768, 65536 and 131072 34.7, 59.5 and 109 us (143, 285 and 570 MB): 5.5 and 5.8 TB/s for what
+// is added, and some 10 us that do not depend on the keys: the launch, the cut (one microsecond), the first
+// reads' latency, the join of the waves and of the pieces.  One request of 701 keys 8.4 us.  Every 16 rows of
+// a request are a tile of their own, which reads the keys again: 64 requests of 2000 to 4000 keys, 4, 8, 16, 32
+// and 48 rows 51.5, 52.1, 55.2, 85.9 and 115 us.  Of other arrangements, one wider (32 rows for a tile of 64
+// keys) spilled and took 153 us where two passes over 16 rows take 65; a second tile on its way, three waves a
+// SIMD, eight waves a workgroup and 768 to 2048 workgroups were all slower than this with two workgroups a CU.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -37,7 +39,8 @@ constexpr int kStep = kWaves * kTileKeys;                 // and the workgroup: 
 static_assert(kStep == kMinKeys, "pieces of the cut");
 // Up to this many keys a tile is not worth cutting.  One request over 4 key heads, 400, 701 and 1000 keys:
 // whole 8.7, 10.2 and 12.0 us, cut 9.0, 9.2 and 9.4; 16 requests over 8: whole 9.1, 10.8 and 15.3, cut
-// 11.8, 12.9 and 13.0.
+// 11.8, 12.9 and 13.0.  Up to 64 requests, whose lengths are in the lanes: 64 of 450 keys over two key heads
+// 9.2 us, 65 13.4, over one 9.2 and 11.0.
 constexpr int kWholeKeys = 512;
 // What a tile costs a workgroup besides its keys (finding it, its queries, the first codes' latency, the
 // join and the result: 3.7 us, measured inside 64 requests' step), in steps; counted where a workgroup has
@@ -52,7 +55,8 @@ constexpr int kManySteps = 2;
 // of more than kManyPieces is cut into longer ones, up to the square root of a kPieceLength-th of its steps:
 // one request of 131072 keys over one key head 30.9 us, in 512 pieces 78.6; of 20635 over four heads 22.1
 // (26.1 in 81), of 60000 over eight 31.1 (34.8).  With 16 pieces and 64 and lengths of a 2nd and a 4th the
-// same calls took 31 to 41, 22 to 24 and 31 to 34 us.  (Up to 64 requests, whose lengths are in the lanes.)
+// same calls took 31 to 41, 22 to 24 and 31 to 34 us.  Up to 64 requests, as above: one of 131072 keys among ones
+// of 100, over one key head 37.9 us with 64 requests and 70.6 with 65, over four 35.4 and 37.4.
 constexpr int kManyPieces = 24, kPieceLength = 8;
 #define FP8_GLOBAL __attribute__((address_space(1)))
 

@@ -15,8 +15,8 @@
 // workgroups share it are 39 us, the rest is that the longest tiles, 32 steps, share to their end.  3442
 // new tokens of four requests over up to 16000 cached keys 455 us (1032 TFLOP/s).
 // Over an mxfp4 cache a tile's codes are converted on their way into LDS, 32 conversions and 8 LDS writes a
-// wave, which the next products' start waits for: 3037 new tokens of four requests over up to 16000 keys 325 us
-// (915 TFLOP/s) where a cache of 16-bit numbers takes 298 to 307.  With those spread between the products,
+// wave, which the next products' start waits for: 3037 new tokens of four requests over up to 16000 keys 318 us
+// (934 TFLOP/s) where a cache of 16-bit numbers takes 309, with 64 channels 257 and 228.  With those spread between the products,
 // from a second set of registers or the first, the registers spill: 361 to 569 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -106,8 +106,9 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool s
   if (M <= 0 || N <= 0) return p;
   // 8-bit integers with up to 16 output channels (a router, a value head) for more tokens: the decode kernels
   // with the operands in each other's place, C[m, n] = sum_k qb[n, k] qa[m, k].
-  // Against the kernels for those tokens, 8 channels, us: K = 4096, 32, 128, 1024 and 16384 tokens 5.0, 5.0, 5.4
-  // and 15.0 (5.8, 13.5, 21.0, 21.8); K = 14112, 32 and 1024 tokens 9.2 and 9.8 (15.0, 58.8).
+  // Against the kernels for those tokens, 8 channels, operands from memory, us: K = 4096, 32, 128, 1024 and
+  // 16384 tokens 4.9, 5.0, 5.4 and 15.7 (6.0, 13.5, 21.0, 22.8); K = 14112, 32 and 1024 tokens 9.3 and 11.6
+  // (15.2, 65.8).  From 17 channels on the others take over: 1024 x 17 x 4096 20.7, 1024 x 16 x 4096 6.0.
   // Tokens are the launch's workgroups then: not where that is more than it holds (2^26 tokens for one
   // channel, 2^29 for more), which the tiles of 256 tokens take.
   if (sm == SM_INT8 && N <= 16 && M > 16 && gemv_fits(N, K)) {

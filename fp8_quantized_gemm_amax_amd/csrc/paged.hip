@@ -141,8 +141,9 @@ constexpr int kAppendThreads = 256;
 // 23.4 us (4.4 TB/s; a 2 GiB copy runs at 4.9).  Key and value of a row in one thread, so that two
 // loads are under way: with one tensor a workgroup it took 23% longer; with two and four rows a
 // thread 2% and 20%.  To mxfp4 a lane's eight channels are a quarter of a block, whose largest magnitude
-// four lanes find by DPP, and 4 bytes of codes: the same call 20.7 us (85 MB, 4.1 TB/s), 64 tokens 2.6 us
-// in a graph, where e4m3 takes 2.8 and a launch by itself 2.
+// four lanes find by DPP, and 4 bytes of codes.  Views of a fused projection, from memory: 16384 tokens into
+// pages in order 22.1 us (85 MB, 3.8 TB/s), into shuffled slots, 64 bytes each, 24.4, where e4m3 takes 25.3 and
+// 25.5; 64 tokens 2.6 us in a graph (e4m3 2.8, a launch by itself 2).
 template <int DT, int D, int FORMAT>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8;
@@ -293,8 +294,8 @@ __device__ __forceinline__ void store_row(void* cache, void* scales, int64_t row
 // A group of D / 16 lanes takes a unit of a token: kRopeHeads query heads, or the keys and values of half
 // as many key heads, whose loads are all in flight while the table's row, that comes after the position,
 // is on its way.  Bound by memory: 16384 tokens of 32 heads over 8 of 128 channels into an e4m3 cache, 373
-// MB, 69 us (5.4 TB/s; a copy of 1 GiB runs at 5.2), into mxfp4 71 us, 64 channels 45 us; and by the chain
-// of reads where there are few: 64 tokens 3.1 us in a graph.  With four heads a unit and with eight, both
+// MB, 69 us (5.4 TB/s; the best copy of 1 GiB 5.7), into mxfp4 67 us in pages in order and 73 in shuffled
+// slots, 64 channels 45 us; and by the chain of reads where there are few: 64 tokens 3.3 us in a graph.  With four heads a unit and with eight, both
 // sizes were slower: 73.8 and 81.2 us, 5.0 and 8.3 us (fewer workgroups, longer each).
 constexpr int kRopeHeads = 2;
 template <int DT, int D, int FORMAT, bool PAIRS>

@@ -44,7 +44,7 @@ def int8_quantize_rowwise(x, q=None, scales=None):
 
 def int8_gemm_scaled_rowwise(qa, sa, qb, sb, out_dtype=torch.bfloat16, out=None):
     """C [M, N] = (qa @ qb^T) * sa[m] * sb[n]; qa int8 [M, K], qb int8 [N, K]; sa float32 [M] (per
-    token), sb float32 [N] (per output channel)."""
+    token), sb float32 [N] (per output channel).  out_dtype is a new output's; `out` keeps its own type."""
     if out is None:
         binding._out_dt(out_dtype)
     r = (serving._ext or serving._load()).gemm8(qa, sa, qb, sb, out_dtype is torch.bfloat16, out, serving._stream(qa))
