@@ -284,15 +284,16 @@ __device__ __forceinline__ void wait_slabs_ahead(int ahead) {
 template <int SM>
 __device__ __forceinline__ int slabs_of(int K) { return SM == SM_INT8 ? (K + kSlab - 1) / kSlab : K / kSlab; }
 template <int SM>
-__device__ __forceinline__ uint32_t a_column(uint32_t column, int K) {
-  return SM != SM_INT8 || column < static_cast<uint32_t>(K) ? column : kOOB;
+__device__ __forceinline__ uint32_t a_offset(uint32_t row, uint32_t k0, uint32_t chunk, int K) {
+  if constexpr (SM == SM_INT8) return row + (k0 + chunk < static_cast<uint32_t>(K) ? k0 + chunk : kOOB);
+  else return row + k0 + chunk;
 }
 
 // Four outputs of a row in one store.  With 8-bit integers also where N is no multiple of 4 and a row starts
 // at any even address, which global memory allows.  Operands in the caches: 1887 x 3775 x 2016 28.2 us,
 // output by output 32.8; 2255 x 1961 x 352 11.4 and 17.0.
 template <int SM>
-__device__ __forceinline__ void store4(uint16_t* to, const uint2& h) {
+__device__ __forceinline__ void store4(uint16_t* to, uint2 h) {
   if constexpr (SM == SM_INT8) __builtin_memcpy(to, &h, 8);
   else *reinterpret_cast<uint2*>(to) = h;
 }
@@ -377,14 +378,13 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
 
   // K % 128 == 0 here (plan_gemm sends other K to the staged kernel), so every
   // offset is plain arithmetic and only the row range check can zero a chunk; except with
-  // 8-bit integers (see a_column)
+  // 8-bit integers (see a_offset)
   auto issue_pair = [&](int s, int st) {
     const uint32_t k0 = static_cast<uint32_t>(s * kSlab);
-    const uint32_t a_even = a_column<SM>(k0 + c_even, K), a_odd = a_column<SM>(k0 + c_odd, K);
 #pragma unroll
     for (int j = 0; j < IA; ++j)
       dma16(ra, lds_addr(Abuf[st] + (wp * IA + j) * 1024),
-            row_off_p + static_cast<uint32_t>(j * 8 * K) + (((wp * IA + j) & 1) ? a_odd : a_even));
+            a_offset<SM>(row_off_p + static_cast<uint32_t>(j * 8 * K), k0, ((wp * IA + j) & 1) ? c_odd : c_even, K));
 #pragma unroll
     for (int j = 0; j < IB; ++j)
       dma16(rb, lds_addr(Bbuf[st] + (wp * IB + j) * 1024),
@@ -403,13 +403,12 @@ __global__ __launch_bounds__((dma_threads<BM, BN, WM, WN>())) void gemm_dma_kern
       issue_pair(s, st);
     }
     const uint32_t k0 = static_cast<uint32_t>(s * kSlab);
-    const uint32_t a_even = a_column<SM>(k0 + c_even, K), a_odd = a_column<SM>(k0 + c_odd, K);
     uint8_t* As = Abuf[st];
     uint8_t* Bs = Bbuf[st];
 #pragma unroll
     for (int j = 0; j < IA; ++j)
       dma16(ra, lds_addr(As + (w * IA + j) * 1024),
-            row_off + static_cast<uint32_t>(j * 8 * K) + (((w * IA + j) & 1) ? a_odd : a_even));
+            a_offset<SM>(row_off + static_cast<uint32_t>(j * 8 * K), k0, ((w * IA + j) & 1) ? c_odd : c_even, K));
 #pragma unroll
     for (int j = 0; j < IB; ++j)
       dma16(rb, lds_addr(Bs + (w * IB + j) * 1024),
@@ -650,10 +649,10 @@ __device__ __forceinline__ void skinny_body(
     const uint32_t row_off = static_cast<uint32_t>((lane >> 3) * K);
     auto issue = [&](int s, int st, bool scales) {
       const uint32_t k0 = static_cast<uint32_t>(s * kSlab);
-      const uint32_t a_even = a_column<SM>(k0 + c_even, K), a_odd = a_column<SM>(k0 + c_odd, K);
 #pragma unroll
       for (int j = 0; j < IA; ++j)
-        dma16(ra, lds_addr(Abuf[st] + j * 1024), row_off + static_cast<uint32_t>(j * 8 * K) + ((j & 1) ? a_odd : a_even));
+        dma16(ra, lds_addr(Abuf[st] + j * 1024),
+              a_offset<SM>(row_off + static_cast<uint32_t>(j * 8 * K), k0, (j & 1) ? c_odd : c_even, K));
       if constexpr (BLOCKWISE) {
         if (scales) {
 #pragma unroll
