@@ -11,9 +11,9 @@
 //     Transformer Engine page §5, per-channel scaling), applied once like tensorwise;
 //   int8: the same over 8-bit integers, whose products are summed exactly in 32 bits (K up to
 //     131071: 128 * 128 K stays below 2^31) and rounded to float32 once, in the epilogue.  At the
-//     matrix unit's rate for e4m3, and within 6% of that mode's times: 4096x14336x4096 209 us with
-//     one set of operands and 224 with seven in turn (2.15 POP/s; e4m3 203 and 214), 8192^3 409 and
-//     432 us (2.54; 393 and 409).  Operands of zeros take 176 and 214, 341 and 404: power bounds it
+//     matrix unit's rate for e4m3, and within 5% of that mode's times: 4096x14336x4096 210 us with
+//     one set of operands and 221 with seven in turn (2.18 POP/s; e4m3 204 and 214), 8192^3 412 and
+//     432 us (2.54; 394 and 413).  Operands of zeros take 176 and 208, 338 and 391: power bounds it
 //     where the operands are in the caches, and their way from memory where they are not.
 //
 // Kernels (CDNA4).  Every kernel walks K in 128-byte slabs and multiplies with
@@ -279,8 +279,9 @@ __device__ __forceinline__ void wait_slabs_ahead(int ahead) {
 // Slabs of K, and where in a row of A a chunk of a slab lies.  8-bit integers may have K % 128 != 0 in the
 // DMA kernels: A's chunks past K are asked for past any range and read as zeros, and what lies in their
 // place in B, the next row's codes or zeros past the last one, multiplies them: integers have no NaN.
-// (e4m3 has, and keeps the staged kernel.)  Operands from memory: 21 x 6263 x 9264 19.4 us, in the staged
-// kernel 91; 32 x 46 x 13392 15.6 and 83, 4096 x 14336 x 4112 289 and 371.
+// (e4m3 has, and keeps the staged kernel.)  Operands from memory: 21 x 6263 x 9264 18.5 us, in the staged
+// kernel 91; 32 x 46 x 13392 14.8 and 83, 4096 x 14336 x 4112 269 and 371.  Apart from e4m3's sum, which as
+// one expression with this is compiled to slower code (128 tokens per row 5% longer).
 template <int SM>
 __device__ __forceinline__ int slabs_of(int K) { return SM == SM_INT8 ? (K + kSlab - 1) / kSlab : K / kSlab; }
 template <int SM>

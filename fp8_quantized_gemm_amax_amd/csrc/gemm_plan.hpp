@@ -108,7 +108,7 @@ inline fp8_gemm_plan_t plan_gemm(int sm, int64_t M, int64_t N, int64_t K, bool s
   // with the operands in each other's place, C[m, n] = sum_k qb[n, k] qa[m, k].
   // Against the kernels for those tokens, 8 channels, operands from memory, us: K = 4096, 32, 128, 1024 and
   // 16384 tokens 4.9, 5.0, 5.4 and 15.7 (6.0, 13.5, 21.0, 22.8); K = 14112, 32 and 1024 tokens 9.3 and 11.6
-  // (15.2, 65.8).  From 17 channels on the others take over: 1024 x 17 x 4096 20.7, 1024 x 16 x 4096 6.0.
+  // (15.2, 65.8).  From 17 channels on the others take over: 1024 x 17 x 4096 20.2, 1024 x 16 x 4096 6.0.
   // Tokens are the launch's workgroups then: not where that is more than it holds (2^26 tokens for one
   // channel, 2^29 for more), which the tiles of 256 tokens take.
   if (sm == SM_INT8 && N <= 16 && M > 16 && gemv_fits(N, K)) {
