@@ -78,15 +78,17 @@ fp8_status_t check_append(const void* k, const void* v, fp8_dtype_t dt, int64_t 
   return FP8_OK;
 }
 
-// The caches of keys and values and their scales, which an append writes, stand apart (checked last).
-fp8_status_t check_apart(const fp8amax::AppendArgs& a, int32_t head_dim, fp8_kv_format_t format) {
+// The caches of keys and values and their scales, which an append writes, stand apart (checked last).  `one`: keys and
+// values are the same rows, which may go to one cache.
+fp8_status_t check_apart(const fp8amax::AppendArgs& a, int32_t head_dim, fp8_kv_format_t format, bool one) {
   const int64_t rows = a.n_slots * a.heads;
   const int64_t codes = rows * head_dim * (format == FP8_KV_SAME ? 4 : format == FP8_KV_E4M3 ? 2 : 1) / 2;
   const int64_t scales = format == FP8_KV_SAME ? 0 : format == FP8_KV_E4M3 ? rows * 4 : rows * (head_dim / 32);
   const void* const at[4] = {a.kc, a.vc, a.ks, a.vs};
+  const bool shared = one && a.kc == a.vc && (scales == 0 || a.ks == a.vs);
   for (int i = 0; i < 4; ++i)
     for (int j = i + 1; j < 4; ++j)
-      if (overlap(at[i], i < 2 ? codes : scales, at[j], j < 2 ? codes : scales)) return FP8_ERR_BAD_SHAPE;
+      if (!(shared && at[i] == at[j]) && overlap(at[i], i < 2 ? codes : scales, at[j], j < 2 ? codes : scales)) return FP8_ERR_BAD_SHAPE;
   return FP8_OK;
 }
 
@@ -143,7 +145,8 @@ fp8_status_t fp8_kv_append(const void* k, const void* v, fp8_dtype_t dt, int64_t
   fp8_status_t st = check_append(k, v, dt, tokens, kv_heads, head_dim, k_token_stride, k_head_stride, v_token_stride,
                                  v_head_stride, slots, pages, page_size, format, k_cache, v_cache, k_scales, v_scales, a);
   if (st != FP8_OK || tokens == 0) return st;
-  if ((st = check_apart(a, head_dim, format)) != FP8_OK) return st;
+  const bool one = k == v && k_token_stride == v_token_stride && k_head_stride == v_head_stride;
+  if ((st = check_apart(a, head_dim, format, one)) != FP8_OK) return st;
   (void)hipGetLastError();
   fp8amax::launch_kv_append(static_cast<int>(dt), head_dim, format, a, static_cast<hipStream_t>(stream));
   return finish_launch();
@@ -171,7 +174,7 @@ fp8_status_t fp8_rope_append(const void* q, const void* k, const void* v, fp8_dt
   if (!positions || (n_positions > 0 && !cos_sin) || (q_heads > 0 && (!q || !q_out))) return FP8_ERR_NULL_POINTER;
   if (!aligned(positions, 4) || !aligned(cos_sin, 16) || (q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))))
     return FP8_ERR_MISALIGNED;
-  if ((st = check_apart(a.kv, head_dim, format)) != FP8_OK) return st;
+  if ((st = check_apart(a.kv, head_dim, format, false)) != FP8_OK) return st;
   a.q = q; a.q_out = q_out; a.qts = q_token_stride; a.qhs = q_head_stride; a.q_heads = static_cast<int>(q_heads);
   a.positions = positions; a.cos_sin = cos_sin; a.n_positions = static_cast<int>(n_positions); a.rotary = rotary_dim;
   (void)hipGetLastError();

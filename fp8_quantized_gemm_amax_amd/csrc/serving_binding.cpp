@@ -147,18 +147,22 @@ Cache cache_of(PyObject* k, PyObject* v, PyObject* ks, PyObject* vs, at::ScalarT
   c.format = FP8_KV_E4M3;
   return c;
 }
-// For the calls that write a cache: its tensors share no memory with each other.
-void apart(const Cache& c) {
+void* raw(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// For the calls that write a cache: its tensors share no memory with each other.  `one`: keys and values are the
+// same rows, which may go to one cache.
+void apart(const Cache& c, bool one) {
   const at::Tensor* const t[4] = {&c.k, &c.v, &c.ks, &c.vs};
+  const bool shared = one && c.k.data_ptr() == c.v.data_ptr() && raw(c.ks) == raw(c.vs);
   for (int i = 0; i < 4; ++i)
-    for (int j = i + 1; j < 4; ++j) TORCH_CHECK_VALUE(!t[i]->defined() || !t[j]->defined() || !overlaps(*t[i], *t[j]), "caches or their scales overlap");
+    for (int j = i + 1; j < 4; ++j)
+      TORCH_CHECK_VALUE(!t[i]->defined() || !t[j]->defined() || (shared && j - i == 1 && i != 1) || !overlaps(*t[i], *t[j]), "caches or their scales overlap");
 }
 void on_cache(const at::Tensor& like, const Cache& c) {
   on(like, {{&c.k, "k_cache"}, {&c.v, "v_cache"}});
   if (c.format != FP8_KV_SAME) on(like, {{&c.ks, "k_scales"}, {&c.vs, "v_scales"}});
 }
 
-void* raw(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 template <typename T>
 T* ptr(const at::Tensor& t) { return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr; }
 
@@ -257,12 +261,13 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                     k0.scalar_type(), " ", shape_of(k0));
   const Cache c = cache_of(a[3], a[4], a[5], a[6], k0.scalar_type());
   const int64_t heads = c.k.size(1), dim = c.dim, page = c.k.size(2);
-  const at::Tensor k = rows(k0, "k", dim), v = rows(v0, "v", dim);
+  const bool one = k0.data_ptr() == v0.data_ptr() && k0.strides() == v0.strides();
+  const at::Tensor k = rows(k0, "k", dim), v = one ? k : rows(v0, "v", dim);
   TORCH_CHECK_VALUE(k.size(1) == heads, "k has ", k.size(1), " heads, the cache ", heads);
   const at::Tensor slots = vec(tensor(a[2], "slots"), "slots", at::kLong, k.size(0));
   for (const at::Tensor* t : {&c.k, &c.v, &c.ks, &c.vs})
     TORCH_CHECK_VALUE(!t->defined() || (!overlaps(*t, k) && !overlaps(*t, v) && !overlaps(*t, slots)), "a cache overlaps k, v or slots");
-  apart(c);
+  apart(c, one);
   on(k, {{&v, "v"}, {&slots, "slots"}});
   on_cache(k, c);
   const c10::DeviceGuard guard(k.device());   // the launch goes to the tensors' GPU
@@ -307,7 +312,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   for (const at::Tensor* t : {&c.k, &c.v, &c.ks, &c.vs})
     for (const at::Tensor* in : std::initializer_list<const at::Tensor*>{&q, &k, &v, &positions, &table, &slots})
       TORCH_CHECK_VALUE(!t->defined() || !in->defined() || !overlaps(*t, *in), "a cache overlaps an input");
-  apart(c);
+  apart(c, false);
   if (a[11] == Py_None) {
     on(k, {{&v, "v"}, {&positions, "positions"}, {&table, "cos_sin"}, {&slots, "slots"}});
     on_cache(k, c);

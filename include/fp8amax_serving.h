@@ -42,7 +42,8 @@
  * and scale pointers 4-byte, int64 pointers 8-byte alignment.
  *
  * What a call writes shares no memory with what it reads or else writes; an append refuses caches and
- * scales that share memory with each other (FP8_ERR_BAD_SHAPE).
+ * scales that share memory with each other (FP8_ERR_BAD_SHAPE), but for fp8_kv_append of one tensor as k
+ * and v into one cache.
  *
  * Sizes.  FP8_ERR_TOO_LARGE, before any HIP call, where tokens * heads passes 2^30 or the work would
  * need 2^24 workgroups or more (a launch holds less than 2^32 threads): a workgroup appends 16 rows

@@ -17,7 +17,9 @@ CODES, SCALES = {SAME: 32768, E4M3: 16384, MXFP4: 8192}, {SAME: 0, E4M3: 512, MX
 @pytest.mark.parametrize("fmt", [SAME, E4M3, MXFP4])
 def test_entry_points_refuse_caches_that_share_memory(fmt, name, base):
     B = 1 << 24                                                        # places far from each other
-    apart = dict(kc=B, vc=2 * B, ks=3 * B, vs=4 * B) if fmt != SAME else dict(kc=B, vc=2 * B, ks=None, vs=None)
+    apart = dict(v=A + 4096, kc=B, vc=2 * B, ks=3 * B, vs=4 * B)
+    if fmt == SAME:
+        apart.update(ks=None, vs=None)
     for at, to in (("vc", B), ("vc", B + CODES[fmt] - 16), ("kc", 2 * B + CODES[fmt] - 16)):
         assert call(name, base, fmt=fmt, **dict(apart, **{at: to})) == SHAPE
     if fmt != SAME:
